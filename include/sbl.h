@@ -462,6 +462,77 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
                            const float* beta, const float* x, const int8_t* xq, const float* gamma,
                            float* dx, float* dw, void* workspace, int64_t workspace_bytes, sbl_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Losses of the output head: what a training step of these layers ends with.
+ * The head itself stays dense in 16 bits (embedding and head are not
+ * ternarized); with z[t][v] = sum_d h[t][d] w[v][d] its losses are taken
+ * straight from the hidden states and the weights, the vocabulary a range at
+ * a time, and the logits (m_tok x n_vocab) are never stored.
+ *
+ * Cross entropy (sbl_head_ce_*):
+ *   lse[t] = log sum_v exp z[t][v];   loss[t] = lse[t] - z[t][target[t]]
+ *   dz[t][v] = (dloss[t] + dlse[t]) softmax(z[t])[v] - dloss[t] [v = target[t]]
+ *   target[t] < 0 takes the row out.
+ * Distillation from a teacher's top logits (sbl_head_kd_*), tau the temperature:
+ *   p[t] = softmax over the row's entries of teacher[t][.] / tau
+ *   lse[t] = log sum_v exp(z[t][v] / tau)
+ *   loss[t] = tau^2 sum_k p[t][k] (log p[t][k] - z[t][index[t][k]] / tau + lse[t])
+ *   dz[t][v] = dloss[t] tau (softmax(z[t] / tau)[v] - sum_k p[t][k] [v = index[t][k]])
+ *   An entry with a negative index or a teacher logit of -infinity is absent;
+ *   an id may be listed twice (both entries count).  A row without entries is
+ *   taken out.
+ * Both: dh = dz w, dw = dz^T h.
+ * A row that is taken out has loss = lse = 0 and a zero dh, adds nothing to
+ * dw, and its h (NaN and infinities included), lse, dloss and dlse are not
+ * used.  An id past the vocabulary makes its row's loss NaN, and takes the
+ * row out of the backward.
+ *
+ *   h          [m_tok] rows of k values, row t at h + t * h_stride (h_stride a
+ *              multiple of 8, >= k).
+ *   w          [n_vocab][k].
+ *   dtype      SBL_BF16 or SBL_FP16: the 16-bit type of h, w, dh and dw.
+ *   target     [m_tok];  index, teacher [m_tok][top], 1 <= top <= 256.
+ *   loss, lse  [m_tok] fp32 outputs of the forward; lse goes into the backward.
+ *   dloss      [m_tok] fp32: the gradient of each row's loss.
+ *   dlse       [m_tok] fp32 or NULL: the gradient of lse (e.g. of a penalty on it).
+ *   dh         [m_tok][k] output (dense), or NULL;  dw [n_vocab][k] output, or NULL.
+ *   workspace  sbl_head_workspace_bytes(m_tok, n_vocab, k, top, backward) bytes
+ *              (top = 1 for cross entropy), 256-byte aligned, any contents; calls
+ *              in flight at the same time need their own.  Backward: the
+ *              gradient of at most 2^27 logits at a time (256 ids at least), a
+ *              copy of h and fp32 partial sums of dh.
+ * Products are exact and summed in fp32; softmax statistics and the loss are
+ * fp32.  The backward rounds dz once to the 16-bit type before the two
+ * products that read it, scaled so that the largest coefficient becomes 1
+ * (BF16) or 2^14 (FP16): relative error 2^-8 (2^-11) of each at most, the size
+ * of the outputs' own rounding.  Sums have a fixed order: results repeat bit for bit.
+ * Limits: 8 <= k <= 131072, k % 8 == 0; n_vocab * k <= 2^34; m_tok <= 2^22 and
+ * (m_tok + 256) * k and the span of h at most 2^30 values; 1e-4 <= tau <= 1e4.
+ * m_tok == 0: the forward does nothing, the backward sets dw to zero.
+ * Non-finite h or w in rows that take part: results are unspecified. */
+typedef enum { SBL_BF16 = 0, SBL_FP16 = 1 } sbl_dtype;
+
+/* Bytes of workspace of a head call; -1 for invalid sizes. */
+int64_t sbl_head_workspace_bytes(int64_t m_tok, int64_t n_vocab, int64_t k, int32_t top, int32_t backward);
+
+int sbl_head_ce_forward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* target,
+                        int64_t m_tok, int64_t n_vocab, int64_t k, float* loss, float* lse, void* workspace,
+                        int64_t workspace_bytes, sbl_stream stream);
+
+int sbl_head_ce_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* target,
+                         const float* lse, const float* dloss, const float* dlse, int64_t m_tok, int64_t n_vocab,
+                         int64_t k, uint16_t* dh, uint16_t* dw, void* workspace, int64_t workspace_bytes,
+                         sbl_stream stream);
+
+int sbl_head_kd_forward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* index,
+                        const float* teacher, int32_t top, float tau, int64_t m_tok, int64_t n_vocab, int64_t k,
+                        float* loss, float* lse, void* workspace, int64_t workspace_bytes, sbl_stream stream);
+
+int sbl_head_kd_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* index,
+                         const float* teacher, int32_t top, float tau, const float* lse, const float* dloss,
+                         int64_t m_tok, int64_t n_vocab, int64_t k, uint16_t* dh, uint16_t* dw, void* workspace,
+                         int64_t workspace_bytes, sbl_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

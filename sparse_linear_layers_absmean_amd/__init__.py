@@ -15,7 +15,10 @@ from .sbl import (SBL_FMT_DENSE2, SBL_FMT_NM, SblError, linear, load, new_backwa
                   sbl_packed_bytes, sbl_quant_acts, sbl_quant_weights, sbl_quant_weights_batch,
                   sbl_quant_weights_batch_noalloc,
                   sbl_workspace_bytes,
-                  sbl_workspace_init)
+                  sbl_workspace_init,
+                  SBL_BF16, SBL_FP16, head_ce, head_ce_backward, head_kd, head_kd_backward, new_head_workspace,
+                  sbl_head_ce_backward, sbl_head_ce_forward, sbl_head_kd_backward, sbl_head_kd_forward,
+                  sbl_head_workspace_bytes)
 
 __all__ = [
     "SBL_FMT_DENSE2", "SBL_FMT_NM", "SblError", "linear", "load", "new_backward_workspace", "new_workspace",
@@ -29,4 +32,7 @@ __all__ = [
     "sbl_quant_weights_batch_noalloc",
     "sbl_workspace_bytes",
     "sbl_workspace_init",
+    "SBL_BF16", "SBL_FP16", "head_ce", "head_ce_backward", "head_kd", "head_kd_backward", "new_head_workspace",
+    "sbl_head_ce_backward", "sbl_head_ce_forward", "sbl_head_kd_backward", "sbl_head_kd_forward",
+    "sbl_head_workspace_bytes",
 ]

@@ -1,0 +1,277 @@
+// The per-token side of the output head's losses: which rows take part, the
+// teacher's distribution, the joined softmax statistics and the loss, and for
+// the backward each row's coefficients and a dense copy of its hidden state.
+//
+//   cross entropy  takes part: target >= 0
+//   distillation   an entry counts when its index >= 0 and its teacher logit is
+//                  not -infinity; takes part: any entry counts
+// Only rows that take part are read and multiplied afterwards, so whatever a
+// row that is taken out holds (NaN, infinities) reaches nothing.
+#include "sbl_head.h"
+#include "sbl_head_tile.h"
+
+namespace sbl {
+namespace head {
+
+namespace {
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+  return x;
+}
+
+__device__ __forceinline__ bool counts(int64_t id, float teacher) {
+  return id >= 0 && teacher != -__builtin_inff();
+}
+
+// Distillation: one wave per row, flag = takes part.  strict: a row that lists
+// an id past the vocabulary does not (its loss is NaN, it has no gradient).
+__global__ __launch_bounds__(256) void flag_kernel(const RowArgs a, bool strict) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.m_tok) return;
+  bool any = false, bad = false;
+  for (int k = threadIdx.x & 63; k < a.top; k += 64) {
+    const int64_t id = a.index[t * a.top + k];
+    any |= counts(id, a.teacher[t * a.top + k]);
+    bad |= id >= a.n_vocab;
+  }
+  const bool in = __ballot(any) != 0 && !(strict && __ballot(bad) != 0);
+  if ((threadIdx.x & 63) == 0) a.flag[t] = in;
+}
+
+// One workgroup: numbers the rows that take part, in order, and (backward)
+// finds the largest coefficient.  A few microseconds at thousands of tokens.
+__global__ __launch_bounds__(1024) void rows_kernel(const RowArgs a, bool backward) {
+  __shared__ int32_t wave_count[16];
+  __shared__ float wave_top[16];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  int32_t before = 0;
+  float top = 0.f;
+  for (int64_t t0 = 0; t0 < a.m_tok; t0 += 1024) {
+    const int64_t t = t0 + tid;
+    bool in = false;
+    if (t < a.m_tok) in = a.target ? a.target[t] >= 0 && !(backward && a.target[t] >= a.n_vocab) : a.flag[t] != 0;
+    const uint64_t m = __ballot(in);
+    if (lane == 0) wave_count[wave] = __popcll(m);
+    __syncthreads();
+    int32_t at = before, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      at += w < wave ? wave_count[w] : 0;
+      all += wave_count[w];
+    }
+    at += __popcll(m & ((1ull << lane) - 1));
+    if (t < a.m_tok) a.pos[t] = in ? at : -1;
+    if (in) {
+      a.rows[at] = (int32_t)t;
+      if (backward) {
+        const float g = a.dloss[t];
+        top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[t]) : 0.f));
+      }
+    }
+    before += all;
+    __syncthreads();
+  }
+  top = wave_max(top);
+  if (lane == 0) wave_top[wave] = top;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < 16; ++w) top = fmaxf(top, wave_top[w]);
+    a.hdr->count = before;
+    // 1e-30: keeps up finite when every coefficient is zero (or next to it)
+    const float amax = fmaxf(top * a.tau, 1e-30f);
+    a.hdr->amax = amax;
+    a.hdr->up = a.up / amax;
+    a.hdr->down = amax / a.up;
+  }
+}
+
+// The teacher's probability of this lane's entries (k = lane + 64 i) and its
+// logarithm; p = 0 for entries that do not count.
+constexpr int kPerLane = kMaxTop / 64;
+__device__ __forceinline__ void teacher_row(const RowArgs& a, int64_t t, int lane, int64_t* id, float* p, float* logp) {
+  float x[kPerLane], mx = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int k = lane + 64 * i;
+    id[i] = -1;
+    x[i] = -__builtin_inff();
+    if (k < a.top) {
+      const int64_t d = a.index[t * a.top + k];
+      const float y = a.teacher[t * a.top + k];
+      if (counts(d, y)) {
+        id[i] = d;
+        x[i] = y;
+      }
+    }
+    mx = fmaxf(mx, x[i]);
+  }
+  mx = wave_max(mx);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    // the difference first: finite logits then never give inf - inf
+    logp[i] = id[i] >= 0 ? (x[i] - mx) * a.inv_tau : 0.f;
+    p[i] = id[i] >= 0 ? __builtin_amdgcn_exp2f(logp[i] * kLog2e) : 0.f;
+    sum += p[i];
+  }
+  sum = wave_sum(sum);
+  const float lsum = kLn2 * __builtin_amdgcn_logf(sum);
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    p[i] = id[i] >= 0 ? p[i] / sum : 0.f;
+    logp[i] -= lsum;
+  }
+}
+
+// Forward, one wave per row: joins the softmax statistics, takes the loss.
+__global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compact) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (t >= a.m_tok) return;
+  const int64_t c = compact ? a.pos[t] : t;
+  int64_t id[kPerLane];
+  float p[kPerLane], logp[kPerLane];
+  bool in, bad = false;
+  if (a.target) {
+    const int64_t y = a.target[t];
+    in = y >= 0;
+    bad = y >= a.n_vocab;
+  } else {
+    teacher_row(a, t, lane, id, p, logp);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      any |= id[i] >= 0;
+      bad |= id[i] >= a.n_vocab;
+    }
+    in = __ballot(any) != 0;
+    bad = __ballot(bad) != 0;
+  }
+  if (!in) {
+    if (lane == 0) {
+      a.loss[t] = 0.f;
+      a.lse[t] = 0.f;
+    }
+    return;
+  }
+  const float* pm = a.part_max + c * a.np;
+  const float* ps = a.part_sum + c * a.np;
+  float mx = -__builtin_inff();
+  for (int i = lane; i < a.np; i += 64) mx = fmaxf(mx, pm[i]);
+  mx = wave_max(mx);
+  float sum = 0.f;
+  for (int i = lane; i < a.np; i += 64)
+    sum += ps[i] * (pm[i] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(pm[i] - mx));
+  sum = wave_sum(sum);
+  // in base 2, the reference against the logit first: what cancels is exact
+  const float l2 = __builtin_amdgcn_logf(sum);
+  float loss;
+  if (a.target) {
+    loss = kLn2 * ((mx - a.zlist[bad ? 0 : c]) + l2);
+  } else {
+    loss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (!(p[i] == 0.f) && id[i] < a.n_vocab)             // not p > 0: a NaN teacher shows
+        loss += p[i] * (logp[i] + kLn2 * ((mx - a.zlist[c * a.top + lane + 64 * i]) + l2));
+    loss = wave_sum(loss) * (a.tau * a.tau);
+  }
+  if (lane == 0) {
+    a.loss[t] = bad ? __builtin_nanf("") : loss;
+    a.lse[t] = kLn2 * (mx + l2);
+  }
+}
+
+// Backward, one workgroup per original row: the row's place among those that
+// take part gets its hidden state and coefficients; a row that does not take
+// part gets a zero gradient.
+__global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
+  __shared__ int32_t ids[kMaxTop];
+  __shared__ float ps[kMaxTop];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int c = a.pos[t];
+  const int vecs = a.k / 8;
+  if (c < 0) {
+    if (a.dh) {
+      u32x4* o = reinterpret_cast<u32x4*>(a.dh + t * a.k);
+      for (int i = tid; i < vecs; i += 256) o[i] = u32x4{0, 0, 0, 0};
+    }
+    return;
+  }
+  const u32x4* src = reinterpret_cast<const u32x4*>(a.h + t * a.h_stride);
+  u32x4* dst = reinterpret_cast<u32x4*>(a.hc + (int64_t)c * a.k);
+  for (int i = tid; i < vecs; i += 256) dst[i] = src[i];
+  const float amax = a.hdr->amax;
+  // divided by the largest coefficient first: equal weights give exactly 1
+  const float g = a.dloss[t] * a.tau / amax * a.up;
+  if (tid == 0) {
+    a.lse2[c] = a.lse_in[t] * kLog2e;
+    a.coef[c] = a.dlse ? (a.dloss[t] + a.dlse[t]) * a.tau / amax * a.up : g;
+  }
+  if (a.target) {
+    if (tid == 0) {
+      a.index32[c] = (int32_t)a.target[t];
+      a.sub[c] = g;
+    }
+    return;
+  }
+  if (tid < 64) {
+    int64_t id[kPerLane];
+    float p[kPerLane], logp[kPerLane];
+    teacher_row(a, t, tid, id, p, logp);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (tid + 64 * i < a.top) {
+        ids[tid + 64 * i] = (int32_t)id[i];
+        ps[tid + 64 * i] = p[i];
+      }
+  }
+  __syncthreads();
+  // an id listed twice is subtracted once, with both probabilities
+  for (int k = tid; k < a.top; k += 256) {
+    const int id = ids[k];
+    bool first = id >= 0;
+    float sum = 0.f;
+    for (int j = 0; j < a.top; ++j)
+      if (ids[j] == id) {
+        if (j < k) first = false;
+        sum += ps[j];
+      }
+    a.index32[(int64_t)c * a.top + k] = first ? id : -1;
+    a.sub[(int64_t)c * a.top + k] = g * sum;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rows(const RowArgs& a, bool backward, hipStream_t s) {
+  if (!a.target) {
+    flag_kernel<<<dim3((unsigned)((a.m_tok + 3) / 4)), 256, 0, s>>>(a, backward);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  rows_kernel<<<1, 1024, 0, s>>>(a, backward);
+  return hipGetLastError();
+}
+
+hipError_t launch_finish(const RowArgs& a, bool compact, hipStream_t s) {
+  finish_kernel<<<dim3((unsigned)((a.m_tok + 3) / 4)), 256, 0, s>>>(a, compact);
+  return hipGetLastError();
+}
+
+hipError_t launch_gather(const RowArgs& a, hipStream_t s) {
+  gather_kernel<<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace head
+}  // namespace sbl

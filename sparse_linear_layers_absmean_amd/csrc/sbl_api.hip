@@ -2,6 +2,7 @@
 #include <mutex>
 
 #include "sbl.h"
+#include "sbl_head.h"
 #include "sbl_internal.h"
 
 namespace {
@@ -655,6 +656,294 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
       (dw && ranges_overlap(workspace, wb, xq, m_tok * k)))
     return SBL_ERR_SHAPE;
   return launch_status(sbl::launch_backward_ws(a, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Losses of the output head.
+namespace {
+
+constexpr int64_t kMaxHeadTokens = int64_t(1) << 22;
+constexpr int64_t kMaxHeadBytes = int64_t(1) << 31;      // one operand, 32-bit buffer offsets
+constexpr int64_t kHeadGradValues = int64_t(1) << 27;    // logit gradients held at a time (256 MB)
+
+bool head_shape_ok(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top) {
+  return m_tok >= 0 && m_tok <= kMaxHeadTokens && n_vocab >= 1 && n_vocab <= INT32_MAX - 1024 && k >= 8 && k <= kMaxK &&
+         k % 8 == 0 && n_vocab * k <= kMaxElems && (m_tok + 256) * k * 2 <= kMaxHeadBytes && top >= 1 &&
+         top <= sbl::head::kMaxTop;
+}
+
+// The workspace's parts, in bytes from its start.
+struct HeadLayout {
+  int64_t hdr, rows, pos, flag;
+  int64_t part_max, part_sum, zlist;                             // forward
+  int64_t lse2, coef, index32, sub, hc, dz, part;                // backward
+  int64_t bytes;
+  int64_t np;                                                    // forward: statistics per token
+  int64_t range;                                                 // backward: ids per range of the vocabulary
+  int splits;
+};
+
+HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, bool backward) {
+  HeadLayout l{};
+  auto take = [&](int64_t bytes) {
+    const int64_t at = l.bytes;
+    l.bytes += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  l.hdr = take(sizeof(sbl::head::Header));
+  l.rows = take(m_tok * 4);
+  l.pos = take(m_tok * 4);
+  l.flag = take(m_tok);
+  if (!backward) {
+    l.np = sbl::head::logits_tiles((int32_t)m_tok, (int32_t)n_vocab);
+    l.part_max = take(m_tok * l.np * 4);
+    l.part_sum = take(m_tok * l.np * 4);
+    l.zlist = take(m_tok * top * 4);
+    return l;
+  }
+  // ranges of equal width (a multiple of 256 ids), as few as hold
+  // kHeadGradValues gradients (256 ids at least) and 2 GiB of weights
+  int64_t most = kHeadGradValues / (m_tok < 1 ? 1 : m_tok);
+  const int64_t by_w = kMaxHeadBytes / (2 * k) - 512;
+  if (most > by_w) most = by_w;
+  most = most < 256 ? 256 : most / 256 * 256;
+  const int64_t ranges = (n_vocab + most - 1) / most;
+  l.range = ((n_vocab + ranges - 1) / ranges + 255) / 256 * 256;
+  l.splits = sbl::head::hidden_splits((int32_t)m_tok, (int32_t)l.range, (int32_t)k);
+  l.lse2 = take(m_tok * 4);
+  l.coef = take(m_tok * 4);
+  l.index32 = take(m_tok * top * 4);
+  l.sub = take(m_tok * top * 4);
+  l.hc = take(m_tok * k * 2);
+  l.dz = take(m_tok * l.range * 2);
+  l.part = take((int64_t)l.splits * m_tok * k * 4);
+  return l;
+}
+
+// the arguments that the four calls share, in the order of the checks
+struct HeadCall {
+  const uint16_t* h;
+  int64_t h_stride;
+  const uint16_t* w;
+  int32_t dtype;
+  const int64_t* target;                                         // cross entropy
+  const int64_t* index;                                          // distillation
+  const float* teacher;
+  int32_t top;
+  float tau;
+  int64_t m_tok, n_vocab, k;
+  void* workspace;
+  int64_t workspace_bytes;
+};
+
+int check_head(const HeadCall& c, bool ce, bool backward, HeadLayout& l) {
+  if (!head_shape_ok(c.m_tok, c.n_vocab, c.k, c.top)) return SBL_ERR_SHAPE;
+  if (c.h_stride < c.k || c.h_stride % 8 != 0 || c.h_stride > kMaxHeadBytes ||
+      (c.m_tok > 0 && ((c.m_tok - 1) * c.h_stride + c.k) * 2 > kMaxHeadBytes))
+    return SBL_ERR_SHAPE;
+  if (!(c.tau >= 1e-4f && c.tau <= 1e4f)) return SBL_ERR_SHAPE;
+  if (c.dtype != SBL_BF16 && c.dtype != SBL_FP16) return SBL_ERR_UNSUPPORTED;
+  if (c.m_tok == 0) return SBL_OK;
+  if (!c.h || !c.w || (ce ? !c.target : (!c.index || !c.teacher))) return SBL_ERR_NULL;
+  l = head_layout(c.m_tok, c.n_vocab, c.k, c.top, backward);
+  if (!c.workspace || c.workspace_bytes < l.bytes) return SBL_ERR_WORKSPACE;
+  if (!aligned(c.h, 16) || !aligned(c.w, 16) || !aligned(c.workspace, 256) ||
+      (ce ? !aligned(c.target, 8) : (!aligned(c.index, 8) || !aligned(c.teacher, 4))))
+    return SBL_ERR_ALIGN;
+  return SBL_OK;
+}
+
+// whether an output (or the workspace) shares a byte with any input
+bool head_input_overlap(const HeadCall& c, const void* p, int64_t bytes) {
+  return ranges_overlap(p, bytes, c.h, ((c.m_tok - 1) * c.h_stride + c.k) * 2) ||
+         ranges_overlap(p, bytes, c.w, c.n_vocab * c.k * 2) || ranges_overlap(p, bytes, c.target, c.m_tok * 8) ||
+         ranges_overlap(p, bytes, c.index, c.m_tok * c.top * 8) ||
+         ranges_overlap(p, bytes, c.teacher, c.m_tok * c.top * 4);
+}
+
+template <class P> P* at(const HeadCall& c, int64_t offset) {
+  return reinterpret_cast<P*>(static_cast<uint8_t*>(c.workspace) + offset);
+}
+
+sbl::head::RowArgs head_rows(const HeadCall& c, const HeadLayout& l) {
+  sbl::head::RowArgs r{};
+  r.target = c.target;
+  r.index = c.index;
+  r.teacher = c.teacher;
+  r.top = c.top;
+  r.tau = c.tau;
+  r.inv_tau = 1.0f / c.tau;
+  r.m_tok = (int32_t)c.m_tok;
+  r.n_vocab = c.n_vocab;
+  r.k = (int32_t)c.k;
+  r.h = c.h;
+  r.h_stride = c.h_stride;
+  r.hdr = at<sbl::head::Header>(c, l.hdr);
+  r.rows = at<int32_t>(c, l.rows);
+  r.pos = at<int32_t>(c, l.pos);
+  r.flag = at<uint8_t>(c, l.flag);
+  return r;
+}
+
+int head_forward(const HeadCall& c, bool ce, float* loss, float* lse, hipStream_t s) {
+  HeadLayout l{};
+  int st = check_head(c, ce, false, l);
+  if (st != SBL_OK || c.m_tok == 0) return st;
+  if (!loss || !lse) return SBL_ERR_NULL;
+  if (!aligned(loss, 4) || !aligned(lse, 4)) return SBL_ERR_ALIGN;
+  const int64_t ob = c.m_tok * 4;
+  if (ranges_overlap(loss, ob, lse, ob) || head_input_overlap(c, loss, ob) || head_input_overlap(c, lse, ob) ||
+      head_input_overlap(c, c.workspace, l.bytes) || ranges_overlap(c.workspace, l.bytes, loss, ob) ||
+      ranges_overlap(c.workspace, l.bytes, lse, ob))
+    return SBL_ERR_SHAPE;
+  sbl::head::RowArgs r = head_rows(c, l);
+  r.part_max = at<float>(c, l.part_max);
+  r.part_sum = at<float>(c, l.part_sum);
+  r.np = (int32_t)l.np;
+  r.zlist = at<float>(c, l.zlist);
+  r.loss = loss;
+  r.lse = lse;
+  // more than one tile of tokens: only the rows that take part are multiplied
+  const bool compact = c.m_tok > 256;
+  if (compact && (st = launch_status(sbl::head::launch_rows(r, false, s))) != SBL_OK) return st;
+  sbl::head::LogitsArgs a{};
+  a.h = c.h;
+  a.h_stride = c.h_stride;
+  a.h_rows = c.m_tok;
+  a.rows = compact ? r.rows : nullptr;
+  a.hdr = compact ? r.hdr : nullptr;
+  a.m_tok = (int32_t)c.m_tok;
+  a.w = c.w;
+  a.n_vocab = (int32_t)c.n_vocab;
+  a.k = (int32_t)c.k;
+  a.top = c.top;
+  a.scale = sbl::head::kLog2e / c.tau;
+  a.index = ce ? c.target : c.index;
+  a.part_max = at<float>(c, l.part_max);
+  a.part_sum = at<float>(c, l.part_sum);
+  a.np = (int32_t)l.np;
+  a.zlist = at<float>(c, l.zlist);
+  st = launch_status(sbl::head::launch_logits(a, c.dtype == SBL_FP16, false, s));
+  return st != SBL_OK ? st : launch_status(sbl::head::launch_finish(r, compact, s));
+}
+
+int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dloss, const float* dlse, uint16_t* dh,
+                  uint16_t* dw, hipStream_t s) {
+  HeadLayout l{};
+  int st = check_head(c, ce, true, l);
+  if (st != SBL_OK) return st;
+  const int64_t dwb = c.n_vocab * c.k * 2, dhb = c.m_tok * c.k * 2, fb = c.m_tok * 4;
+  if (c.m_tok == 0) {                                            // no token: dw = 0
+    if (!dw) return SBL_OK;
+    if (!aligned(dw, 16)) return SBL_ERR_ALIGN;
+    return launch_status(sbl::launch_workspace_init(reinterpret_cast<uint64_t*>(dw), dwb / 8, s));
+  }
+  if (!lse || !dloss) return SBL_ERR_NULL;
+  if (!aligned(lse, 4) || !aligned(dloss, 4) || (dlse && !aligned(dlse, 4)) || (dh && !aligned(dh, 16)) ||
+      (dw && !aligned(dw, 16)))
+    return SBL_ERR_ALIGN;
+  auto bad = [&](const void* p, int64_t b) {
+    return head_input_overlap(c, p, b) || ranges_overlap(p, b, lse, fb) || ranges_overlap(p, b, dloss, fb) ||
+           ranges_overlap(p, b, dlse, fb);
+  };
+  if (bad(dh, dhb) || bad(dw, dwb) || bad(c.workspace, l.bytes) || ranges_overlap(dh, dhb, dw, dwb) ||
+      ranges_overlap(c.workspace, l.bytes, dh, dhb) || ranges_overlap(c.workspace, l.bytes, dw, dwb))
+    return SBL_ERR_SHAPE;
+  if (!dh && !dw) return SBL_OK;
+  const bool fp16 = c.dtype == SBL_FP16;
+  sbl::head::RowArgs r = head_rows(c, l);
+  r.lse_in = lse;
+  r.dloss = dloss;
+  r.dlse = dlse;
+  r.up = fp16 ? 16384.0f : 1.0f;
+  r.lse2 = at<float>(c, l.lse2);
+  r.coef = at<float>(c, l.coef);
+  r.index32 = at<int32_t>(c, l.index32);
+  r.sub = at<float>(c, l.sub);
+  r.hc = at<uint16_t>(c, l.hc);
+  r.dh = dh;
+  if ((st = launch_status(sbl::head::launch_rows(r, true, s))) != SBL_OK) return st;
+  if ((st = launch_status(sbl::head::launch_gather(r, s))) != SBL_OK) return st;
+  for (int64_t v0 = 0; v0 < c.n_vocab; v0 += l.range) {
+    const int64_t n = c.n_vocab - v0 < l.range ? c.n_vocab - v0 : l.range;
+    sbl::head::LogitsArgs a{};
+    a.h = r.hc;
+    a.h_stride = c.k;
+    a.h_rows = c.m_tok;
+    a.hdr = r.hdr;
+    a.m_tok = (int32_t)c.m_tok;
+    a.w = c.w + v0 * c.k;
+    a.n_vocab = (int32_t)n;
+    a.k = (int32_t)c.k;
+    a.top = c.top;
+    a.scale = sbl::head::kLog2e / c.tau;
+    a.v0 = v0;
+    a.lse2 = r.lse2;
+    a.coef = r.coef;
+    a.index32 = r.index32;
+    a.sub = r.sub;
+    a.dz = at<uint16_t>(c, l.dz);
+    a.ldz = (int32_t)l.range;
+    if ((st = launch_status(sbl::head::launch_logits(a, fp16, true, s))) != SBL_OK) return st;
+    if (dw) {
+      const sbl::head::WeightGradArgs g{a.dz, a.ldz, r.hc, r.hdr, a.m_tok, a.n_vocab, a.k, dw + v0 * c.k};
+      if ((st = launch_status(sbl::head::launch_weight_grad(g, fp16, s))) != SBL_OK) return st;
+    }
+    if (dh) {
+      const int64_t steps = (l.range + 63) / 64;
+      const sbl::head::HiddenGradArgs g{a.dz, a.ldz, a.w, r.hdr, a.m_tok, a.n_vocab, a.k, l.splits,
+                                        (int32_t)((steps + l.splits - 1) / l.splits), at<float>(c, l.part), v0 > 0};
+      if ((st = launch_status(sbl::head::launch_hidden_grad(g, fp16, s))) != SBL_OK) return st;
+    }
+  }
+  if (!dh) return SBL_OK;
+  return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), l.splits, r.hdr, r.rows, (int32_t)c.m_tok,
+                                                      (int32_t)c.k, dh, fp16, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sbl_head_workspace_bytes(int64_t m_tok, int64_t n_vocab, int64_t k, int32_t top, int32_t backward) {
+  if (!head_shape_ok(m_tok, n_vocab, k, top)) return -1;
+  return head_layout(m_tok, n_vocab, k, top, backward != 0).bytes;
+}
+
+int sbl_head_ce_forward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* target,
+                        int64_t m_tok, int64_t n_vocab, int64_t k, float* loss, float* lse, void* workspace,
+                        int64_t workspace_bytes, sbl_stream stream) {
+  const HeadCall c{h, h_stride, w, dtype, target, nullptr, nullptr, 1, 1.0f, m_tok, n_vocab, k, workspace,
+                   workspace_bytes};
+  return head_forward(c, true, loss, lse, reinterpret_cast<hipStream_t>(stream));
+}
+
+int sbl_head_ce_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* target,
+                         const float* lse, const float* dloss, const float* dlse, int64_t m_tok, int64_t n_vocab,
+                         int64_t k, uint16_t* dh, uint16_t* dw, void* workspace, int64_t workspace_bytes,
+                         sbl_stream stream) {
+  const HeadCall c{h, h_stride, w, dtype, target, nullptr, nullptr, 1, 1.0f, m_tok, n_vocab, k, workspace,
+                   workspace_bytes};
+  return head_backward(c, true, lse, dloss, dlse, dh, dw, reinterpret_cast<hipStream_t>(stream));
+}
+
+int sbl_head_kd_forward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* index,
+                        const float* teacher, int32_t top, float tau, int64_t m_tok, int64_t n_vocab, int64_t k,
+                        float* loss, float* lse, void* workspace, int64_t workspace_bytes, sbl_stream stream) {
+  const HeadCall c{h, h_stride, w, dtype, nullptr, index, teacher, top, tau, m_tok, n_vocab, k, workspace,
+                   workspace_bytes};
+  return head_forward(c, false, loss, lse, reinterpret_cast<hipStream_t>(stream));
+}
+
+int sbl_head_kd_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w, int32_t dtype, const int64_t* index,
+                         const float* teacher, int32_t top, float tau, const float* lse, const float* dloss,
+                         int64_t m_tok, int64_t n_vocab, int64_t k, uint16_t* dh, uint16_t* dw, void* workspace,
+                         int64_t workspace_bytes, sbl_stream stream) {
+  const HeadCall c{h, h_stride, w, dtype, nullptr, index, teacher, top, tau, m_tok, n_vocab, k, workspace,
+                   workspace_bytes};
+  return head_backward(c, false, lse, dloss, nullptr, dh, dw, reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -24,6 +24,8 @@ SBL_FMT_NM = 1
 # weight-preparation variants and execution choices (sbl_quant_weights_batch_ex flags)
 SBL_QW_DEFAULT, SBL_QW_BETA_KEPT, SBL_QW_MASK_FROM_CODES = 0, 1, 2
 SBL_QW_TWO_PASS, SBL_QW_NO_WAIT = 4, 8
+# 16-bit types of the output head's losses (sbl_dtype)
+SBL_BF16, SBL_FP16 = 0, 1
 ABI_VERSION = 11
 
 _c_i64 = ctypes.c_int64
@@ -129,6 +131,18 @@ def load():
     lib.sbl_linear_backward_ws.restype = ctypes.c_int
     lib.sbl_linear_backward_ws.argtypes = [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_i32, _c_i32,
                                            _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p]
+    lib.sbl_head_workspace_bytes.restype = _c_i64
+    lib.sbl_head_workspace_bytes.argtypes = [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32]
+    sizes, tail = [_c_i64, _c_i64, _c_i64], [_c_p, _c_p, _c_p, _c_i64, _c_p]
+    lib.sbl_head_ce_forward.restype = ctypes.c_int
+    lib.sbl_head_ce_forward.argtypes = [_c_p, _c_i64, _c_p, _c_i32, _c_p, *sizes, *tail]
+    lib.sbl_head_ce_backward.restype = ctypes.c_int
+    lib.sbl_head_ce_backward.argtypes = [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p, *sizes, *tail]
+    lib.sbl_head_kd_forward.restype = ctypes.c_int
+    lib.sbl_head_kd_forward.argtypes = [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_i32, ctypes.c_float, *sizes, *tail]
+    lib.sbl_head_kd_backward.restype = ctypes.c_int
+    lib.sbl_head_kd_backward.argtypes = [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_i32, ctypes.c_float, _c_p, _c_p,
+                                         *sizes, *tail]
     if lib.sbl_abi_version() != ABI_VERSION:
         raise RuntimeError("libsbl.so ABI version mismatch: rebuild it")
     _lib = lib
@@ -485,6 +499,100 @@ def sbl_linear_acts_batch(x, xq, gamma, items, fmt: int, n: int, m: int, stream=
     _check("sbl_linear_acts_batch", st)
 
 
+# ---------------------------------------------------------------- losses of the output head
+
+def sbl_head_workspace_bytes(m_tok: int, n_vocab: int, k: int, top: int = 1, backward: bool = False) -> int:
+    return load().sbl_head_workspace_bytes(m_tok, n_vocab, k, top, int(backward))
+
+
+def _head_args(h, w):
+    """(h pointer, row stride, w pointer, dtype, m_tok, n_vocab, k): h [m_tok][k] with rows of
+    contiguous values (any row stride that is a multiple of 8), w [n_vocab][k] contiguous, both
+    bfloat16 (or its 16-bit patterns as int16/uint16) or both float16."""
+    for t, name in ((h, "h"), (w, "w")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{name} must have two dimensions")
+    fp16 = h.dtype == torch.float16
+    types = (torch.float16,) if fp16 else _W16
+    if h.dtype not in types or w.dtype not in types:
+        raise TypeError(f"h and w have dtypes {h.dtype} and {w.dtype}, expected two of {types}")
+    m_tok, k = h.shape
+    n_vocab = w.shape[0]
+    if w.shape[1] != k:
+        raise ValueError(f"h has {k} features, w {w.shape[1]}")
+    if not h.is_cuda:
+        raise ValueError("h must be a GPU tensor")
+    if h.device != w.device:
+        raise ValueError("h and w must be on one device")
+    if h.stride(1) != 1 and k > 1 or (m_tok > 1 and h.stride(0) < k):
+        raise ValueError("h must have rows of contiguous values")
+    stride = h.stride(0) if m_tok > 1 else k
+    return (h.data_ptr() if m_tok else None, stride, _ptr(w, types, n_vocab * k * 2, "w"),
+            SBL_FP16 if fp16 else SBL_BF16, m_tok, n_vocab, k)
+
+
+def _teacher_args(index, teacher, m_tok: int):
+    if index.dim() != 2 or index.shape != teacher.shape or index.shape[0] != m_tok:
+        raise ValueError("index and teacher must be [m_tok][top]")
+    top = index.shape[1]
+    return (_ptr(index, torch.int64, m_tok * top * 8, "index"),
+            _ptr(teacher, torch.float32, m_tok * top * 4, "teacher"), top)
+
+
+def sbl_head_ce_forward(h, w, target, loss, lse, workspace, stream=None):
+    """Cross entropy of the output head: h [m_tok][k], w [n_vocab][k] (16-bit), target int64
+    [m_tok] (negative: row taken out) -> loss, lse fp32 [m_tok].  The logits are never stored."""
+    lib = load()
+    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
+    st = lib.sbl_head_ce_forward(hp, stride, wp, dtype, _ptr(target, torch.int64, m_tok * 8, "target"), m_tok, n_vocab,
+                                 k, _ptr(loss, torch.float32, m_tok * 4, "loss"),
+                                 _ptr(lse, torch.float32, m_tok * 4, "lse"), _ptr(workspace, None, 0, "workspace"),
+                                 _nbytes(workspace), _stream(stream))
+    _check("sbl_head_ce_forward", st)
+
+
+def sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw, workspace, dlse=None, stream=None):
+    """Gradients of the cross entropy: dloss (and dlse) fp32 [m_tok] -> dh [m_tok][k] and dw
+    [n_vocab][k] in the type of h and w (either may be None)."""
+    lib = load()
+    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
+    st = lib.sbl_head_ce_backward(hp, stride, wp, dtype, _ptr(target, torch.int64, m_tok * 8, "target"),
+                                  _ptr(lse, torch.float32, m_tok * 4, "lse"),
+                                  _ptr(dloss, torch.float32, m_tok * 4, "dloss"),
+                                  _ptr(dlse, torch.float32, m_tok * 4, "dlse"), m_tok, n_vocab, k,
+                                  _ptr(dh, h.dtype, m_tok * k * 2, "dh"), _ptr(dw, w.dtype, n_vocab * k * 2, "dw"),
+                                  _ptr(workspace, None, 0, "workspace"), _nbytes(workspace), _stream(stream))
+    _check("sbl_head_ce_backward", st)
+
+
+def sbl_head_kd_forward(h, w, index, teacher, tau: float, loss, lse, workspace, stream=None):
+    """Distillation from a teacher's top logits: index int64, teacher fp32 [m_tok][top]
+    (negative index: no entry), tau the temperature -> loss, lse fp32 [m_tok]."""
+    lib = load()
+    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
+    ip, tp, top = _teacher_args(index, teacher, m_tok)
+    st = lib.sbl_head_kd_forward(hp, stride, wp, dtype, ip, tp, top, tau, m_tok, n_vocab, k,
+                                 _ptr(loss, torch.float32, m_tok * 4, "loss"),
+                                 _ptr(lse, torch.float32, m_tok * 4, "lse"), _ptr(workspace, None, 0, "workspace"),
+                                 _nbytes(workspace), _stream(stream))
+    _check("sbl_head_kd_forward", st)
+
+
+def sbl_head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, dh, dw, workspace, stream=None):
+    """Gradients of the distillation loss: dloss fp32 [m_tok] -> dh [m_tok][k] and dw
+    [n_vocab][k] in the type of h and w (either may be None)."""
+    lib = load()
+    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
+    ip, tp, top = _teacher_args(index, teacher, m_tok)
+    st = lib.sbl_head_kd_backward(hp, stride, wp, dtype, ip, tp, top, tau, _ptr(lse, torch.float32, m_tok * 4, "lse"),
+                                  _ptr(dloss, torch.float32, m_tok * 4, "dloss"), m_tok, n_vocab, k,
+                                  _ptr(dh, h.dtype, m_tok * k * 2, "dh"), _ptr(dw, w.dtype, n_vocab * k * 2, "dw"),
+                                  _ptr(workspace, None, 0, "workspace"), _nbytes(workspace), _stream(stream))
+    _check("sbl_head_kd_backward", st)
+
+
 # ---------------------------------------------------------------- allocating conveniences
 
 def new_workspace(n_out: int, k: int, device="cuda"):
@@ -528,3 +636,51 @@ def linear(packed, meta, fmt, n, m, beta, xq, gamma, n_out, want_acc=False, stre
     acc = torch.empty((m_tok, n_out), dtype=torch.int32, device=xq.device) if want_acc else None
     sbl_linear(packed, meta, fmt, n, m, beta, xq, gamma, n_out, y, acc, stream=stream)
     return y, acc
+
+
+def new_head_workspace(m_tok: int, n_vocab: int, k: int, top: int = 1, backward: bool = False, device="cuda"):
+    """Scratch for the head calls at these sizes (any contents)."""
+    nbytes = sbl_head_workspace_bytes(m_tok, n_vocab, k, top, backward)
+    if nbytes < 0:
+        raise ValueError("unsupported shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _head_workspace(workspace, h, w, top: int, backward: bool, stream):
+    if workspace is None:
+        workspace = new_head_workspace(h.shape[0], w.shape[0], h.shape[1], top, backward, h.device)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)      # freed on return, still in use there
+    return workspace
+
+
+def head_ce(h, w, target, workspace=None, stream=None):
+    """Allocate outputs (and a workspace) and run sbl_head_ce_forward; returns (loss, lse)."""
+    workspace = _head_workspace(workspace, h, w, 1, False, stream)
+    loss, lse = torch.empty((2, h.shape[0]), dtype=torch.float32, device=h.device).unbind(0)
+    sbl_head_ce_forward(h, w, target, loss, lse, workspace, stream=stream)
+    return loss, lse
+
+
+def head_ce_backward(h, w, target, lse, dloss, dlse=None, workspace=None, stream=None):
+    """Allocate outputs (and a workspace) and run sbl_head_ce_backward; returns (dh, dw)."""
+    workspace = _head_workspace(workspace, h, w, 1, True, stream)
+    dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
+    sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw, workspace, dlse=dlse, stream=stream)
+    return dh, dw
+
+
+def head_kd(h, w, index, teacher, tau: float, workspace=None, stream=None):
+    """Allocate outputs (and a workspace) and run sbl_head_kd_forward; returns (loss, lse)."""
+    workspace = _head_workspace(workspace, h, w, index.shape[1], False, stream)
+    loss, lse = torch.empty((2, h.shape[0]), dtype=torch.float32, device=h.device).unbind(0)
+    sbl_head_kd_forward(h, w, index, teacher, tau, loss, lse, workspace, stream=stream)
+    return loss, lse
+
+
+def head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, workspace=None, stream=None):
+    """Allocate outputs (and a workspace) and run sbl_head_kd_backward; returns (dh, dw)."""
+    workspace = _head_workspace(workspace, h, w, index.shape[1], True, stream)
+    dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
+    sbl_head_kd_backward(h, w, index, teacher, tau, lse, dloss, dh, dw, workspace, stream=stream)
+    return dh, dw
