@@ -499,7 +499,7 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  *   workspace  sbl_head_workspace_bytes(m_tok, n_vocab, k, top, backward) bytes
  *              (top = 1 for cross entropy), 256-byte aligned, any contents; calls
  *              in flight at the same time need their own.  Backward: the
- *              gradient of at most 2^27 logits at a time (256 ids at least), a
+ *              gradient of at most 2^28 logits at a time (256 ids at least), a
  *              copy of h and fp32 partial sums of dh.
  * Products are exact and summed in fp32; softmax statistics and the loss are
  * fp32.  The backward rounds dz once to the 16-bit type before the two

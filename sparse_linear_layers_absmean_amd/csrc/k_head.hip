@@ -2,8 +2,8 @@
 // they are made and never stored, and the two gradients.
 //
 //   z[t][v] = sum_d h[t][d] w[v][d]
-//   forward   per token: max and sum of 2^(z scale) over each 128 ids (or
-//             fewer), joined later, and z at the token's listed ids
+//   forward   per token: max of z and sum of 2^((z - max) scale) over each
+//             tile's ids, joined later, and z at the token's listed ids
 //   backward  dz[t][v] = coef[t] 2^(z scale - lse2[t]) - sub at the listed ids,
 //             rounded once to 16 bits, a range of the vocabulary at a time;
 //             dw = dz^T h, dh = dz w
@@ -22,24 +22,33 @@ namespace {
 // the thread index occupies a register during the products.
 __device__ __forceinline__ int lane_again() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0)); }
 
+// The logit gradients of a range, in panels of 256 ids: [panel][m_tok][256].  A
+// 256 x 256 tile is one run of 128 KB, wherever it is written or read, and rows
+// are 512 bytes apart (rows of the whole range, 64 or 128 KB apart, would touch
+// a page each).
+__device__ __forceinline__ uint16_t* dz_at(uint16_t* dz, int m_tok, int t, int v) {
+  return dz + ((int64_t)(v >> 8) * m_tok + t) * 256 + (v & 255);
+}
+
 // ---------------------------------------------------------------- logits
 // Rows of the tile (MFMA rows) are vocabulary entries, columns are tokens: a
 // lane holds one token's logits of 4 consecutive ids per 16-row tile, and with
 // the permuted row order 8 consecutive ids per pair of tiles, so softmax
 // statistics reduce over registers and two lane exchanges, and the gradient
 // leaves as 16-byte stores.
-template <class E, int TM, int TN, int WM, int WN, bool kBackward>
-__global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArgs a) {
-  using T = Tile<E, kRows, kRows, TM, TN, WM, WN, true, false, !kBackward>;
-  __shared__ __align__(16) uint8_t lds0[T::kStageBytes];
-  __shared__ __align__(16) uint8_t lds1[T::kStageBytes];
-  __shared__ __align__(16) uint8_t lds2[TN == 256 ? 16 : T::kStageBytes];
-  __shared__ int32_t row_of[TN];           // original row of each of the tile's tokens, -1: none
+template <class E, int TM, int TN, int WM, int WN, bool kBackward, class St>
+__device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const St& st) {
+  using T = Tile<E, kRows, kRows, TM, TN, WM, WN, true, !kBackward>;
+  __shared__ int32_t row_of[kBackward ? 1 : TN];   // original row of each of the tile's tokens, -1: none
+  __shared__ float2 stat[kBackward ? 1 : WM][kBackward ? 1 : TN];
+  constexpr int kHits = TN <= 64 ? 512 : 1024;
+  __shared__ uint32_t hit_at[kHits];       // listed ids in this tile: id less vt0, token less t0, entry; 8 bits each
+  __shared__ float hit_sub[kBackward ? kHits : 1];
+  __shared__ int hit_count;
   const int count = a.hdr ? a.hdr->count : a.m_tok;
   const int nvt = (a.n_vocab + TM - 1) / TM, ntt = (a.m_tok + TN - 1) / TN;
   // groups of kGroup vocabulary tiles x every token tile
   constexpr int kGroup = 4;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
   const int group = tile / (kGroup * ntt), in_group = tile % (kGroup * ntt);
   const int gv = nvt - group * kGroup < kGroup ? nvt - group * kGroup : kGroup;
   const int vt = group * kGroup + in_group % gv, tt = in_group / gv;
@@ -48,82 +57,159 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
   const int64_t vt0 = (int64_t)vt * TM;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int lane = tid & 63;
-  for (int i = tid; i < TN; i += T::kThreads) {
-    const int t = t0 + i;
-    row_of[i] = t < count ? (a.rows ? a.rows[t] : t) : -1;
-  }
-  __syncthreads();
-
   T tl;
   const int64_t wrows = a.n_vocab - vt0 < TM ? a.n_vocab - vt0 : TM;
   tl.sa.init_rows(make_rsrc(a.w + vt0 * a.k, wrows * a.k * 2), wave, lane, 2 * a.k);
-  if constexpr (kBackward)
+  if constexpr (kBackward) {
     tl.sb.init_rows(make_rsrc(a.h + (int64_t)t0 * a.k, (int64_t)(count - t0) * a.k * 2), wave, lane, 2 * a.k);
-  else
+  } else {
+    for (int i = tid; i < TN; i += T::kThreads) {
+      const int t = t0 + i;
+      row_of[i] = t < count ? (a.rows ? a.rows[t] : t) : -1;
+    }
+    __syncthreads();
     tl.sb.init_list(make_rsrc(a.h, ((a.h_rows - 1) * a.h_stride + a.k) * 2), wave, lane, [&](int r) {
       const int row = row_of[r];
       return row < 0 ? kFar : (uint32_t)((int64_t)row * a.h_stride * 2);
     });
-  if constexpr (TN == 256) {
-    uint8_t* const st[2] = {lds0, lds1};
-    tl.run_wide(st, wave, lane, a.k);
-  } else {
-    uint8_t* const st[3] = {lds0, lds1, lds2};
-    tl.template run<3>(st, wave, lane, a.k);
   }
-
+  if constexpr (TN == 256) tl.start(st, wave, a.k);
+  // Backward: what the end needs is loaded now.  There, a load would wait for
+  // the stores before it (the memory counter counts both, in order).
+  constexpr int kMT = T::kMT, kNT = T::kNT, kRowsW = TM / WM, kColsW = TN / WN;
   const int wm = wave / WN, wn = wave % WN;
+  float lse2[kNT], coef[kNT];
+  if constexpr (kBackward) {
+#pragma unroll
+    for (int j = 0; j < kNT; ++j) {
+      const int t = t0 + wn * kColsW + 16 * j + (lane & 15);
+      lse2[j] = t < count ? a.lse2[t] : 0.f;
+      coef[j] = t < count ? a.coef[t] : 0.f;
+    }
+  }
+  // The listed ids that fall into this tile, found by all threads.  Their order
+  // does not matter: each has a place of its own to go to.
+  if (tid == 0) hit_count = 0;
+  __syncthreads();
+  auto found_one = [&](int tok, int ent) {
+    const int n = atomicAdd(&hit_count, 1);
+    if (n < kHits) hit_at[n] = (uint32_t)tok << 8 | (uint32_t)ent << 16;
+  };
+  auto id_of = [&](int tok, int ent) -> int64_t {   // less the range's first id
+    if constexpr (kBackward)
+      return (int64_t)a.index32[(int64_t)(t0 + tok) * a.top + ent] - a.v0;
+    else
+      return a.index[(int64_t)row_of[tok] * a.top + ent];
+  };
+  if (TN == 256 && a.near) {
+    // 8 entries' 256-id blocks in 16 bytes, 4 loads of a thread at a time
+    constexpr int kBatch = 4;
+    const int per_row = (a.top + 7) / 8, units = TN * per_row;
+    const uint32_t want = (uint32_t)((a.v0 + vt0) >> 8);
+    for (int u0 = tid; u0 < units; u0 += T::kThreads * kBatch) {
+      u32x4 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int n = u0 + u * T::kThreads, tok = n / per_row;
+        x[u] = u32x4{~0u, ~0u, ~0u, ~0u};
+        if (n < units && t0 + tok < count) {
+          const int64_t row = kBackward ? t0 + tok : row_of[tok];
+          x[u] = reinterpret_cast<const u32x4*>(a.near)[row * per_row + n % per_row];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int n = u0 + u * T::kThreads;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (((x[u][q >> 1] >> (16 * (q & 1))) & 0xFFFFu) == want) found_one(n / per_row, 8 * (n % per_row) + q);
+      }
+    }
+  } else {
+    constexpr int kBatch = 4;
+    const int step_t = T::kThreads / a.top, step_k = T::kThreads % a.top;
+    int et = tid / a.top, ek = tid % a.top;
+    for (int e0 = 0; e0 < TN * a.top; e0 += T::kThreads * kBatch) {
+      int64_t id[kBatch];
+      int tok[kBatch], ent[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        tok[u] = et;
+        ent[u] = ek;
+        id[u] = et < TN && t0 + et < count ? id_of(et, ek) : -1;
+        et += step_t;
+        ek += step_k;
+        if (ek >= a.top) {
+          ek -= a.top;
+          ++et;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t d = id[u] - vt0;
+        if (id[u] >= 0 && d >= 0 && d < TM) found_one(tok[u], ent[u]);
+      }
+    }
+  }
+  __syncthreads();
+  for (int n = tid; n < hit_count && n < kHits; n += T::kThreads) {
+    const int tok = (int)(hit_at[n] >> 8 & 255), ent = (int)(hit_at[n] >> 16);
+    hit_at[n] |= (uint32_t)(id_of(tok, ent) - vt0);
+    if constexpr (kBackward) hit_sub[n] = a.sub[(int64_t)(t0 + tok) * a.top + ent];
+  }
+  if constexpr (TN == 256)
+    tl.run_wide(st, wave, lane, a.k);
+  else
+    tl.template run<3>(st, wave, lane, a.k);
+
   lane = lane_again();
   const int r = lane & 15, g = lane >> 4;
-  constexpr int kMT = T::kMT, kNT = T::kNT, kRowsW = TM / WM, kColsW = TN / WN;
   const int vw = (int)vt0 + wm * kRowsW;   // first id (in this range) of the wave's rows
-  const bool tail = vw + kRowsW > a.n_vocab;
-  // id of tl.acc[i][.][e] less vw
-  auto id_of = [&](int i, int e) { return 32 * (i >> 1) + 8 * g + 4 * (i & 1) + e; };
+  if (vw + kRowsW > a.n_vocab) {           // the last tile: no logit past the vocabulary
+#pragma unroll
+    for (int i = 0; i < kMT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (vw + 32 * (i >> 1) + 8 * g + 4 * (i & 1) + e >= a.n_vocab) {
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) tl.acc[i][j][e] = -__builtin_inff();
+        }
+  }
 
 #pragma unroll
   for (int j = 0; j < kNT; ++j) {
     const int tw = wn * kColsW + 16 * j + r;
     const int t = t0 + tw;
     if constexpr (!kBackward) {
+      // the largest logit stays unscaled: what later cancels (it against a listed
+      // logit) then cancels without a rounding of either
       float mx = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = tl.acc[i][j][e] * a.scale;
-          if (tail && vw + id_of(i, e) >= a.n_vocab) x = -__builtin_inff();
-          tl.acc[i][j][e] = x;
-          mx = fmaxf(mx, x);
-        }
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, tl.acc[i][j][e]);
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float ref = mx == -__builtin_inff() ? 0.f : mx;   // no finite logit here: a sum of zeros
+      const float top = mx == -__builtin_inff() ? 0.f : mx;   // no finite logit here: a sum of zeros
+      const float ref = top * a.scale, off = __builtin_fmaf(top, a.scale, -ref);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(tl.acc[i][j][e] - ref);
+        for (int e = 0; e < 4; ++e)
+          sum += __builtin_amdgcn_exp2f(__builtin_fmaf(tl.acc[i][j][e], a.scale, -ref));
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (g == 0 && t < count && vw < a.n_vocab) {
-        const int64_t o = (int64_t)t * a.np + vw / kRowsW;
-        a.part_max[o] = mx;
-        a.part_sum[o] = sum;
-      }
+      sum *= __builtin_amdgcn_exp2f(-off);                    // ref's own rounding, exactly known
+      if (g == 0) stat[wm][tw] = float2{mx, sum};
     } else {
-      const bool in = t < count;
-      const float lse2 = in ? a.lse2[t] : 0.f, coef = in ? a.coef[t] : 0.f;
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p = coef * __builtin_amdgcn_exp2f(__builtin_fmaf(tl.acc[i][j][e], a.scale, -lse2));
-          if (tail && vw + id_of(i, e) >= a.n_vocab) p = 0.f;
-          tl.acc[i][j][e] = p;
-        }
-      if (in) {
-        uint16_t* o = a.dz + (int64_t)t * a.ldz + vw + 8 * g;
+        for (int e = 0; e < 4; ++e)
+          tl.acc[i][j][e] = coef[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(tl.acc[i][j][e], a.scale, -lse2[j]));
+      if (t < count) {
+        uint16_t* o = dz_at(a.dz, a.m_tok, t, vw) + 8 * g;
 #pragma unroll
         for (int i = 0; i < kMT; i += 2) {
           const v4f x = tl.acc[i][j], y = tl.acc[i + 1][j];
@@ -133,36 +219,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
       }
     }
   }
-
-  // The listed ids that fall on this wave's rows and columns, 64 entries at a
-  // time: the wave finds them by ballot, then takes them one by one (a
-  // wave-uniform walk to the accumulator, a handful per tile).  Forward: the
-  // scaled logit.  Backward: the lane that stored the id's gradient stores it
-  // again with the listed part taken off, still from 32 bits.
-  const int entries = kColsW * a.top;
-  const int step_t = 64 / a.top, step_k = 64 % a.top;
-  int et = lane / a.top, ek = lane % a.top;
-  for (int e0 = 0; e0 < entries; e0 += 64) {
-    const int tw = wn * kColsW + et;
-    int rel = -1;
-    int64_t slot = 0;
-    if (et < kColsW && t0 + tw < count) {
-      const int64_t t = t0 + tw;
-      slot = t * a.top + ek;
-      const int64_t id = kBackward ? (int64_t)a.index32[slot] - a.v0
-                                   : a.index[(int64_t)row_of[tw] * a.top + ek];
-      const int64_t d = id - vw;
-      if (d >= 0 && d < kRowsW) rel = (int)d;
+  if constexpr (!kBackward) {
+    // joins the waves' statistics: one entry per token and tile
+    __syncthreads();
+    for (int i = tid; i < TN; i += T::kThreads) {
+      if (t0 + i >= count) break;
+      float2 x = stat[0][i];
+#pragma unroll
+      for (int w = 1; w < WM; ++w) {
+        const float2 y = stat[w][i];
+        const float mx = fmaxf(x.x, y.x), ref = mx == -__builtin_inff() ? 0.f : mx;
+        x.y = x.y * __builtin_amdgcn_exp2f((x.x - ref) * a.scale) + y.y * __builtin_amdgcn_exp2f((y.x - ref) * a.scale);
+        x.x = mx;
+      }
+      a.part[(int64_t)(t0 + i) * a.np + vt] = x;
     }
+  }
+
+  // Listed ids on this wave's rows and columns, 64 at a time by ballot, then one
+  // by one (a wave-uniform walk to the accumulator, a handful per tile).
+  // Forward: the logit.  Backward: the lane that stored the id's gradient
+  // stores it again with the listed part taken off, still from 32 bits.
+  auto take = [&](int rel, int et, int ek, float sub) {
     uint64_t hits = __ballot(rel >= 0);
     while (hits) {
       const int src = __builtin_ctzll(hits);
       hits &= hits - 1;
       const int hr = __builtin_amdgcn_readlane(rel, src), ht = __builtin_amdgcn_readlane(et, src);
-      const int64_t hs = (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(slot >> 32), src) << 32) |
-                                   (uint32_t)__builtin_amdgcn_readlane((int)slot, src));
       const int hi = 2 * (hr >> 5) + ((hr >> 2) & 1), hj = ht >> 4, he = hr & 3;
-      float val = 0.f;
+      float val = 0.f;                     // not a switch or a tree: the compiler would put the sums in memory
 #pragma unroll
       for (int j = 0; j < kNT; ++j)
         if (hj == j) {
@@ -173,21 +258,68 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
               val = he == 0 ? x[0] : he == 1 ? x[1] : he == 2 ? x[2] : x[3];
             }
         }
-      if (r == (ht & 15) && g == ((hr >> 3) & 3)) {
-        if constexpr (!kBackward) {
-          a.zlist[hs] = val;
-        } else {
-          const uint32_t o = E::pack2(val - a.sub[hs], 0.f);
-          a.dz[(int64_t)(t0 + wn * kColsW + ht) * a.ldz + vw + hr] = (uint16_t)o;
-        }
+      const int64_t t = t0 + wn * kColsW + ht;
+      const bool mine = r == (ht & 15) && g == ((hr >> 3) & 3);
+      if constexpr (!kBackward) {
+        const int hk = __builtin_amdgcn_readlane(ek, src);
+        if (mine) a.zlist[t * a.top + hk] = val;
+      } else {
+        const float hsub = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sub), src));
+        if (mine) *dz_at(a.dz, a.m_tok, (int)t, vw + hr) = (uint16_t)E::pack2(val - hsub, 0.f);
       }
     }
-    et += step_t;
-    ek += step_k;
-    if (ek >= a.top) {
-      ek -= a.top;
-      ++et;
+  };
+  const int found = hit_count;             // written before the products' first barrier
+  if (found <= kHits) {
+    for (int n0 = 0; n0 < found; n0 += 64) {
+      int rel = -1, et = 0, ek = 0;
+      float sub = 0.f;
+      if (n0 + lane < found) {
+        const uint32_t x = hit_at[n0 + lane];
+        et = (int)(x >> 8 & 255) - wn * kColsW;
+        ek = (int)(x >> 16);
+        const int d = (int)(x & 255) - wm * kRowsW;
+        if (d >= 0 && d < kRowsW && et >= 0 && et < kColsW) rel = d;
+        if constexpr (kBackward) sub = hit_sub[n0 + lane];
+      }
+      take(rel, et, ek, sub);
     }
+    return;
+  }
+  // more listed ids in one tile than the list holds: every entry of the wave's tokens
+  for (int e0 = 0; e0 < kColsW * a.top; e0 += 64) {
+    const int e = e0 + lane, et = e / a.top, ek = e % a.top, tw = wn * kColsW + et;
+    int rel = -1;
+    float sub = 0.f;
+    if (et < kColsW && t0 + tw < count) {
+      int64_t id;
+      if constexpr (kBackward) {
+        const int64_t slot = (int64_t)(t0 + tw) * a.top + ek;
+        id = a.index32[slot] - a.v0;
+        sub = a.sub[slot];
+      } else {
+        id = a.index[(int64_t)row_of[tw] * a.top + ek];
+      }
+      const int64_t d = id - vw;
+      if (id >= 0 && d >= 0 && d < kRowsW) rel = (int)d;
+    }
+    take(rel, et, ek, sub);
+  }
+}
+
+template <class E, int TM, int TN, int WM, int WN, bool kBackward>
+__global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArgs a) {
+  constexpr int kStage = (TM + TN) * kBK * 2;
+  __shared__ __align__(16) uint8_t lds0[kStage];
+  __shared__ __align__(16) uint8_t lds1[kStage];
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  if constexpr (TN == 256) {
+    uint8_t* const st[2] = {lds0, lds1};
+    logits_tile<E, TM, TN, WM, WN, kBackward>(a, tile, st);
+  } else {
+    __shared__ __align__(16) uint8_t lds2[kStage];
+    uint8_t* const st[3] = {lds0, lds1, lds2};
+    logits_tile<E, TM, TN, WM, WN, kBackward>(a, tile, st);
   }
 }
 
@@ -195,140 +327,244 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
 // Rows of the tile are features (contiguous in memory, read down the k axis),
 // so a lane's 4 consecutive results are 4 consecutive features of an output row.
 
-template <class E>
-__global__ __launch_bounds__(512, 2) void weight_grad_kernel(const WeightGradArgs a) {
-  using T = Tile<E, kCols, kCols, 256, 256, 2, 4, false>;
-  __shared__ __align__(16) uint8_t lds0[T::kStageBytes];
-  __shared__ __align__(16) uint8_t lds1[T::kStageBytes];
+template <class E, int TM, int TN, int WM, int WN, class St>
+__device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int tile, const St& st) {
+  using T = Tile<E, kCols, kCols, TM, TN, WM, WN, false>;
   const int count = a.hdr->count;
-  const int ndt = (a.k + 255) / 256;
-  const int nvt = (a.n_vocab + 255) / 256;
+  const int ndt = (a.k + TM - 1) / TM, nvt = (a.n_vocab + TN - 1) / TN;
   constexpr int kGroup = 4;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
   const int group = tile / (kGroup * ndt), in_group = tile % (kGroup * ndt);
   const int gv = nvt - group * kGroup < kGroup ? nvt - group * kGroup : kGroup;
   const int vt = group * kGroup + in_group % gv, dt = in_group / gv;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int lane = threadIdx.x & 63;
   T tl;
-  tl.sa.init_cols(make_rsrc(a.h, (int64_t)count * a.k * 2), wave, lane, 2 * a.k, 512 * dt);
-  tl.sb.init_cols(make_rsrc(a.dz, (int64_t)count * a.ldz * 2), wave, lane, 2 * a.ldz, 512 * vt);
-  uint8_t* const st[2] = {lds0, lds1};
-  tl.run_wide(st, wave, lane, count);
+  tl.sa.init_cols(make_rsrc(a.h, (int64_t)count * a.k * 2), wave, lane, 2 * a.k, 2 * TM * dt);
+  tl.sb.init_cols(make_rsrc(a.dz + (int64_t)(vt * TN / 256) * a.m_tok * 256, (int64_t)count * 512), wave, lane, 512,
+                  2 * (vt * TN % 256));
+  if constexpr (TN == 256) {
+    tl.start(st, wave, count);
+    tl.run_wide(st, wave, lane, count);
+  } else {
+    tl.run_once(st[0], wave, lane, count);
+  }
   lane = lane_again();
-  const int wm = wave / 4, wn = wave % 4, r = lane & 15, g = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN, r = lane & 15, g = lane >> 4;
   const float down = a.hdr->down;
+  // A lane holds features 4g .. 4g + 3 of a 16-feature tile.  Of two tiles, the
+  // even groups of lanes give their part of the second to the odd ones for
+  // those's part of the first: 8 consecutive features each, 64-byte runs per
+  // store (runs of 32 bytes reach memory at 3.8 TB/s, of 64 at 6.1).
+  const int d0 = dt * TM + wm * (TM / WM) + ((g & 1) ? 16 + 4 * (g - 1) : 4 * g);
 #pragma unroll
   for (int j = 0; j < T::kNT; ++j) {
-    const int v = vt * 256 + wn * 64 + 16 * j + r;
-    if (v >= a.n_vocab) continue;
+    const int v = vt * TN + wn * (TN / WN) + 16 * j + r;
     uint16_t* o = a.dw + (int64_t)v * a.k;
 #pragma unroll
-    for (int i = 0; i < T::kMT; ++i) {
-      const int d = dt * 256 + wm * 128 + 16 * i + 4 * g;
-      const v4f x = tl.acc[i][j];
-      if (d < a.k)
-        *reinterpret_cast<uint2*>(o + d) = uint2{E::pack2(x[0] * down, x[1] * down), E::pack2(x[2] * down, x[3] * down)};
+    for (int i = 0; i < T::kMT; i += 2) {
+      const v4f x = tl.acc[i][j] * down, y = tl.acc[i + 1][j] * down;
+      const auto lo = __builtin_amdgcn_permlane16_swap(E::pack2(x[0], x[1]), E::pack2(y[0], y[1]), false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(E::pack2(x[2], x[3]), E::pack2(y[2], y[3]), false, false);
+      const int d = d0 + 16 * i;
+      if (v < a.n_vocab && d < a.k) *reinterpret_cast<u32x4*>(o + d) = u32x4{lo[0], hi[0], lo[1], hi[1]};
     }
   }
 }
 
-template <class E, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, TN == 256 ? 2 : 1) void hidden_grad_kernel(const HiddenGradArgs a) {
-  using T = Tile<E, kCols, kRows, 256, TN, WM, WN, false, WM * WN == 4>;
-  __shared__ __align__(16) uint8_t lds0[T::kStageBytes];
-  __shared__ __align__(16) uint8_t lds1[T::kStageBytes];
-  __shared__ __align__(16) uint8_t lds2[TN == 256 ? 16 : T::kStageBytes];
+template <class E, int TM, int TN, int WM, int WN, class St>
+__device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int tile, const St& st) {
+  using T = Tile<E, kCols, kRows, TM, TN, WM, WN, false, false, true>;
   const int count = a.hdr->count;
-  const int ndt = (a.k + 255) / 256, ntt = (a.m_tok + TN - 1) / TN;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int ndt = (a.k + TM - 1) / TM, ntt = (a.m_tok + TN - 1) / TN;
   // a share's tiles together: they read the same rows of w
   const int s = tile / (ndt * ntt), in = tile % (ndt * ntt);
-  const int dt = in % ndt, t0 = in / ndt * TN;
+  // groups of kGroup token tiles x every feature tile
+  constexpr int kGroup = 4;
+  const int group = in / (kGroup * ndt), in_group = in % (kGroup * ndt);
+  const int gt = ntt - group * kGroup < kGroup ? ntt - group * kGroup : kGroup;
+  const int dt = in_group / gt, t0 = (group * kGroup + in_group % gt) * TN;
   if (t0 >= count) return;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int lane = threadIdx.x & 63;
   const int64_t v0 = (int64_t)s * a.split_steps * kBK;
   int64_t vs = a.n_vocab - v0;
   if (vs > (int64_t)a.split_steps * kBK) vs = (int64_t)a.split_steps * kBK;
   if (vs < 0) vs = 0;
   T tl;
-  tl.sa.init_cols(make_rsrc(a.w + v0 * a.k, vs * a.k * 2), wave, lane, 2 * a.k, 512 * dt);
-  tl.sb.init_rows(make_rsrc(a.dz + (int64_t)t0 * a.ldz + v0, ((int64_t)(count - t0) * a.ldz - v0) * 2), wave, lane,
-                  2 * a.ldz);
+  tl.sa.init_cols(make_rsrc(a.w + v0 * a.k, vs * a.k * 2), wave, lane, 2 * a.k, 2 * TM * dt);
+  // rows past the last token read other rows of the panel, for columns that are not stored
+  tl.sb.init_rows(make_rsrc(a.dz + (int64_t)t0 * 256, ((int64_t)(a.n_vocab + 255) / 256 * a.m_tok - t0) * 512), wave, lane,
+                  512);
+  tl.sb.panel = (uint32_t)a.m_tok * 512;
+  tl.sb.first = s * a.split_steps;
   if constexpr (TN == 256) {
-    uint8_t* const st[2] = {lds0, lds1};
+    tl.start(st, wave, (int)vs);
     tl.run_wide(st, wave, lane, (int)vs);
   } else {
-    uint8_t* const st[3] = {lds0, lds1, lds2};
     tl.template run<3>(st, wave, lane, (int)vs);
   }
   lane = lane_again();
   const int wm = wave / WN, wn = wave % WN, r = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < T::kNT; ++j) {
-    const int t = t0 + wn * (TN / WN) + 16 * j + r;
-    if (t >= count) continue;
-    float* o = a.part + ((int64_t)s * a.m_tok + t) * a.k;
+  // what earlier ranges left is loaded a column tile ahead of the stores (a
+  // load waits for every store before it)
+  auto at = [&](int j, int i) -> v4f* {
+    const int t = t0 + wn * (TN / WN) + 16 * j + r, d = dt * TM + wm * (TM / WM) + 16 * i + 4 * g;
+    return t < count && d < a.k ? reinterpret_cast<v4f*>(a.part + ((int64_t)s * a.m_tok + t) * a.k + d) : nullptr;
+  };
+  v4f old[2][T::kMT];
+  auto load = [&](int j) {
 #pragma unroll
     for (int i = 0; i < T::kMT; ++i) {
-      const int d = dt * 256 + wm * (256 / WM) + 16 * i + 4 * g;
-      if (d < a.k) {
-        v4f x = tl.acc[i][j];
-        v4f* p = reinterpret_cast<v4f*>(o + d);
-        if (a.add) x += *p;
-        *p = x;
-      }
+      old[j & 1][i] = v4f{0.f, 0.f, 0.f, 0.f};
+      const v4f* p = at(j, i);
+      if (p) old[j & 1][i] = *p;
+    }
+  };
+  if (a.add) load(0);
+#pragma unroll
+  for (int j = 0; j < T::kNT; ++j) {
+    if (a.add && j + 1 < T::kNT) load(j + 1);
+#pragma unroll
+    for (int i = 0; i < T::kMT; ++i) {
+      v4f x = tl.acc[i][j];
+      if (a.add) x += old[j & 1][i];
+      v4f* p = at(j, i);
+      if (p) *p = x;
     }
   }
 }
 
+// More than 128 tokens: both gradients of a range in one launch (either may be
+// absent), so that one's last, part empty round is filled by the other.  Each
+// XCD takes a contiguous run of each kind's tiles, the hidden gradient's, the
+// longer ones, first.  (Taking the two in turn costs a quarter more time:
+// workgroups of one kind run in step and share operands in L2.)
+template <class E>
+__global__ __launch_bounds__(512, 2) void grads_wide_kernel(const WeightGradArgs w, const HiddenGradArgs h, int n_w,
+                                                            int n_h) {
+  __shared__ __align__(16) uint8_t lds0[512 * kBK * 2];
+  __shared__ __align__(16) uint8_t lds1[512 * kBK * 2];
+  uint8_t* const st[2] = {lds0, lds1};
+  const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  auto share = [&](int n, int& first) {    // this XCD's run of n tiles
+    const int per = (n + 7) / 8;
+    first = x * per < n ? x * per : n;
+    return n - first < per ? n - first : per;
+  };
+  int w0, h0;
+  const int nw = share(n_w, w0), nh = share(n_h, h0);
+  if (i < nh)
+    hidden_grad_tile<E, 256, 256, 2, 4>(h, h0 + i, st);
+  else if (i < nh + nw)
+    weight_grad_tile<E, 256, 256, 2, 4>(w, w0 + i - nh, st);
+}
+
+// 65 to 128 tokens
+template <class E>
+__global__ __launch_bounds__(512, 2) void weight_grad_kernel(const WeightGradArgs a) {
+  __shared__ __align__(16) uint8_t lds0[512 * kBK * 2];
+  __shared__ __align__(16) uint8_t lds1[512 * kBK * 2];
+  uint8_t* const st[2] = {lds0, lds1};
+  weight_grad_tile<E, 256, 256, 2, 4>(a, xcd_tile(blockIdx.x, gridDim.x), st);
+}
+
+template <class E>
+__global__ __launch_bounds__(512, 2) void hidden_grad_kernel(const HiddenGradArgs a) {
+  constexpr int kStage = (256 + 128) * kBK * 2;
+  __shared__ __align__(16) uint8_t lds0[kStage];
+  __shared__ __align__(16) uint8_t lds1[kStage];
+  __shared__ __align__(16) uint8_t lds2[kStage];
+  uint8_t* const st[3] = {lds0, lds1, lds2};
+  hidden_grad_tile<E, 256, 128, 4, 2>(a, xcd_tile(blockIdx.x, gridDim.x), st);
+}
+
+// Few tokens: dw is bound by its writes, dh by its reads of w, so both go in one
+// launch, on alternating workgroups while both last (n_dw and n_dh of them).
+template <class E>
+__global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, const HiddenGradArgs h, int n_dw, int n_dh) {
+  constexpr int kStage = (128 + kFewTokens) * kBK * 2;   // of dh; dw's only one is smaller than two of them
+  __shared__ __align__(16) uint8_t lds0[kStage < 256 * kBK * 2 ? 256 * kBK * 2 : kStage];
+  __shared__ __align__(16) uint8_t lds1[kStage];
+  __shared__ __align__(16) uint8_t lds2[kStage];
+  const int b = blockIdx.x, both = 2 * (n_dw < n_dh ? n_dw : n_dh);
+  const bool is_dw = b < both ? (b & 1) != 0 : n_dw > n_dh;
+  const int tile = b < both ? b >> 1 : b - (both >> 1);
+  uint8_t* const st[3] = {lds0, lds1, lds2};
+  if (is_dw)
+    weight_grad_tile<E, 128, 128, 2, 2>(w, tile, st);
+  else
+    hidden_grad_tile<E, 128, kFewTokens, 2, 2>(h, tile, st);
+}
+
+// One workgroup per token and 256 features: 64 threads of 4 features x 4 groups
+// of shares.
 template <class E>
 __global__ __launch_bounds__(256) void hidden_final_kernel(const float* part, int splits, const Header* hdr,
                                                            const int32_t* rows, int32_t m_tok, int32_t k,
                                                            uint16_t* dh) {
+  __shared__ v4f joined[4][64];
   const int t = blockIdx.x;
   if (t >= hdr->count) return;
-  const int d = 4 * (blockIdx.y * 256 + threadIdx.x);
-  if (d >= k) return;
-  const float down = hdr->down;
+  const int q = threadIdx.x >> 6, lane = threadIdx.x & 63, d = 4 * (blockIdx.y * 64 + lane);
+  const bool in = d < k;
   v4f x = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s) x += *reinterpret_cast<const v4f*>(part + ((int64_t)s * m_tok + t) * k + d);
-  *reinterpret_cast<uint2*>(dh + (int64_t)rows[t] * k + d) =
-      uint2{E::pack2(x[0] * down, x[1] * down), E::pack2(x[2] * down, x[3] * down)};
+  if (in) {
+    const float* p = part + (int64_t)t * k + d;
+    const int64_t next = (int64_t)m_tok * k;
+#pragma unroll 4
+    for (int s = q; s < splits; s += 4) x += *reinterpret_cast<const v4f*>(p + s * next);
+  }
+  joined[q][lane] = x;
+  __syncthreads();
+  if (q != 0 || !in) return;
+  const float down = hdr->down;
+  x = ((joined[0][lane] + joined[1][lane]) + (joined[2][lane] + joined[3][lane])) * down;
+  *reinterpret_cast<uint2*>(dh + (int64_t)rows[t] * k + d) = uint2{E::pack2(x[0], x[1]), E::pack2(x[2], x[3])};
 }
+
+// ids per tile of the logits kernel, and tokens per tile of every kernel
+int vocab_tile(int m_tok) { return m_tok <= kFewTokens ? 128 : 256; }
+int token_tile(int m_tok) { return m_tok <= 32 ? 32 : m_tok <= 64 ? 64 : m_tok <= 128 ? 128 : 256; }
 
 template <class E, bool kBackward>
 hipError_t logits(const LogitsArgs& a, hipStream_t s) {
-  auto grid = [&](int tm, int tn) {
-    return dim3((unsigned)(((int64_t)a.n_vocab + tm - 1) / tm * ((a.m_tok + tn - 1) / tn)));
-  };
-  if (a.m_tok <= 32)
-    logits_kernel<E, 128, 32, 4, 1, kBackward><<<grid(128, 32), 256, 0, s>>>(a);
-  else if (a.m_tok <= 64)
-    logits_kernel<E, 128, 64, 4, 1, kBackward><<<grid(128, 64), 256, 0, s>>>(a);
+  const int tm = vocab_tile(a.m_tok), tn = token_tile(a.m_tok);
+  const dim3 grid((unsigned)(((int64_t)a.n_vocab + tm - 1) / tm * ((a.m_tok + tn - 1) / tn)));
+  if (tn == 32)
+    logits_kernel<E, 128, 32, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
+  else if (tn == 64)
+    logits_kernel<E, 128, 64, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
+  else if (tn == 128)
+    logits_kernel<E, 256, 128, 4, 2, kBackward><<<grid, 512, 0, s>>>(a);
   else
-    logits_kernel<E, 256, 256, 2, 4, kBackward><<<grid(256, 256), 512, 0, s>>>(a);
+    logits_kernel<E, 256, 256, 2, 4, kBackward><<<grid, 512, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class E>
-hipError_t hidden_grad(const HiddenGradArgs& a, hipStream_t s) {
-  auto grid = [&](int tn) { return dim3((unsigned)((a.k + 255) / 256 * ((a.m_tok + tn - 1) / tn) * a.splits)); };
-  if (a.m_tok <= 64)
-    hidden_grad_kernel<E, 64, 4, 1><<<grid(64), 256, 0, s>>>(a);
-  else
-    hidden_grad_kernel<E, 256, 2, 4><<<grid(256), 512, 0, s>>>(a);
+hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, hipStream_t s) {
+  const int tn = token_tile(h.m_tok);
+  const int td = tn <= kFewTokens ? 128 : 256;
+  const int n_w = w.dw ? (w.k + td - 1) / td * ((w.n_vocab + td - 1) / td) : 0;
+  const int n_h = h.part ? (h.k + td - 1) / td * ((h.m_tok + tn - 1) / tn) * h.splits : 0;
+  if (tn <= kFewTokens) {
+    grads_kernel<E><<<dim3((unsigned)(n_w + n_h)), 256, 0, s>>>(w, h, n_w, n_h);
+  } else if (tn == 256) {
+    grads_wide_kernel<E><<<dim3((unsigned)(8 * ((n_w + 7) / 8 + (n_h + 7) / 8))), 512, 0, s>>>(w, h, n_w, n_h);
+  } else {
+    if (n_w > 0) weight_grad_kernel<E><<<dim3((unsigned)n_w), 512, 0, s>>>(w);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (n_h > 0) hidden_grad_kernel<E><<<dim3((unsigned)n_h), 512, 0, s>>>(h);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-// every variant of the logits kernel leaves one statistic per wave's rows:
-// 32 ids for the narrow tiles (4 waves over 128), 128 for the wide one
 int64_t logits_tiles(int32_t m_tok, int32_t n_vocab) {
-  const int rows = m_tok <= 64 ? 32 : 128;
-  return ((int64_t)n_vocab + rows - 1) / rows;
+  const int tm = vocab_tile(m_tok);
+  return ((int64_t)n_vocab + tm - 1) / tm;
 }
 
 hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStream_t s) {
@@ -336,34 +572,27 @@ hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStrea
   return backward ? logits<Bf16, true>(a, s) : logits<Bf16, false>(a, s);
 }
 
-hipError_t launch_weight_grad(const WeightGradArgs& a, bool fp16, hipStream_t s) {
-  const dim3 grid((unsigned)((a.k + 255) / 256 * ((a.n_vocab + 255) / 256)));
-  if (fp16)
-    weight_grad_kernel<Fp16><<<grid, 512, 0, s>>>(a);
-  else
-    weight_grad_kernel<Bf16><<<grid, 512, 0, s>>>(a);
-  return hipGetLastError();
+hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, bool fp16, hipStream_t s) {
+  return fp16 ? grads<Fp16>(w, h, s) : grads<Bf16>(w, h, s);
 }
 
-// shares of the vocabulary per hidden-gradient tile: enough workgroups for
-// every CU, at least 8 steps each
+// Shares of a range per hidden-gradient tile.  Few tokens: two workgroups per
+// CU or so, 4 steps each at least.  More: short enough to go round with the
+// launch's weight-gradient tiles, a third of a CU's work at most.
 int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k) {
   if (m_tok < 1) return 1;
-  const int tn = m_tok <= 64 ? 64 : 256;
-  const int64_t tiles = (int64_t)((k + 255) / 256) * ((m_tok + tn - 1) / tn);
+  const int tn = token_tile(m_tok), td = m_tok <= kFewTokens ? 128 : 256;
+  const int64_t tiles = (int64_t)((k + td - 1) / td) * ((m_tok + tn - 1) / tn);
   const int64_t steps = ((int64_t)n_vocab + kBK - 1) / kBK;
-  int64_t s = tiles >= 1024 ? 1 : (1024 + tiles - 1) / tiles;
-  if (s > steps / 8) s = steps / 8;
+  const int64_t want = m_tok <= 128 ? 512 : 427;
+  int64_t s = (want + tiles - 1) / tiles;
+  if (s > steps / 4) s = steps / 4;
   return s < 1 ? 1 : (int)s;
-}
-
-hipError_t launch_hidden_grad(const HiddenGradArgs& a, bool fp16, hipStream_t s) {
-  return fp16 ? hidden_grad<Fp16>(a, s) : hidden_grad<Bf16>(a, s);
 }
 
 hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,
                                int32_t k, uint16_t* dh, bool fp16, hipStream_t s) {
-  const dim3 grid((unsigned)m_tok, (unsigned)((k + 1023) / 1024));
+  const dim3 grid((unsigned)m_tok, (unsigned)((k + 255) / 256));
   if (fp16)
     hidden_final_kernel<Fp16><<<grid, 256, 0, s>>>(part, splits, hdr, rows, m_tok, k, dh);
   else

@@ -31,16 +31,23 @@ __device__ __forceinline__ bool counts(int64_t id, float teacher) {
   return id >= 0 && teacher != -__builtin_inff();
 }
 
-// Distillation: one wave per row, flag = takes part.  strict: a row that lists
+// What the logit gradients are divided by: the largest coefficient; 1e-30
+// keeps the quotient finite when every one is zero (or next to it).
+__device__ __forceinline__ float scale_base(float top, float tau) { return fmaxf(top * tau, 1e-30f); }
+
+// Distillation: one wave per row, flag = takes part; forward: the blocks of the
+// row's ids (near).  strict (backward): a row that lists
 // an id past the vocabulary does not (its loss is NaN, it has no gradient).
 __global__ __launch_bounds__(256) void flag_kernel(const RowArgs a, bool strict) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= a.m_tok) return;
   bool any = false, bad = false;
-  for (int k = threadIdx.x & 63; k < a.top; k += 64) {
-    const int64_t id = a.index[t * a.top + k];
-    any |= counts(id, a.teacher[t * a.top + k]);
+  const int wide = (a.top + 7) / 8 * 8;
+  for (int k = threadIdx.x & 63; k < wide; k += 64) {
+    const int64_t id = k < a.top ? a.index[t * a.top + k] : -1;
+    if (k < a.top) any |= counts(id, a.teacher[t * a.top + k]);
     bad |= id >= a.n_vocab;
+    if (a.near && !strict) a.near[t * wide + k] = id >= 0 && id < a.n_vocab ? (uint16_t)(id >> 8) : 0xFFFFu;
   }
   const bool in = __ballot(any) != 0 && !(strict && __ballot(bad) != 0);
   if ((threadIdx.x & 63) == 0) a.flag[t] = in;
@@ -85,8 +92,7 @@ __global__ __launch_bounds__(1024) void rows_kernel(const RowArgs a, bool backwa
   if (tid == 0) {
     for (int w = 1; w < 16; ++w) top = fmaxf(top, wave_top[w]);
     a.hdr->count = before;
-    // 1e-30: keeps up finite when every coefficient is zero (or next to it)
-    const float amax = fmaxf(top * a.tau, 1e-30f);
+    const float amax = scale_base(top, a.tau);
     a.hdr->amax = amax;
     a.hdr->up = a.up / amax;
     a.hdr->down = amax / a.up;
@@ -131,12 +137,54 @@ __device__ __forceinline__ void teacher_row(const RowArgs& a, int64_t t, int lan
   }
 }
 
-// Forward, one wave per row: joins the softmax statistics, takes the loss.
+// Forward: joins the softmax statistics, takes the loss.  kWaves waves per row
+// (one when there are rows enough to fill the chip) share the statistics; wave
+// 0 does the rest.
+template <int kWaves>
 __global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compact) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (t >= a.m_tok) return;
+  __shared__ float2 joined[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = kWaves == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  if (t >= a.m_tok) return;                        // whole workgroups where waves share a row
   const int64_t c = compact ? a.pos[t] : t;
+  const bool there = c >= 0;
+  const float scale = kLog2e / a.tau;
+  // the statistics, 4 entries of a lane at a time
+  float mx = -__builtin_inff(), sum = 0.f;
+  if (there) {
+    const float2* part = a.part + c * a.np;
+    for (int i0 = kWaves == 1 ? lane : threadIdx.x; i0 < a.np; i0 += 256 * kWaves) {
+      float2 x[4];
+      float top = mx;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + 64 * kWaves * u;
+        x[u] = i < a.np ? part[i] : float2{-__builtin_inff(), 0.f};
+        top = fmaxf(top, x[u].x);
+      }
+      const float ref = top == -__builtin_inff() ? 0.f : top;
+      sum *= __builtin_amdgcn_exp2f((mx - ref) * scale);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += x[u].y * __builtin_amdgcn_exp2f((x[u].x - ref) * scale);
+      mx = top;
+    }
+  }
+  const float own = mx;
+  mx = wave_max(mx);
+  sum = wave_sum(sum * __builtin_amdgcn_exp2f((own - (mx == -__builtin_inff() ? 0.f : mx)) * scale));
+  if constexpr (kWaves > 1) {
+    if (lane == 0) joined[wave] = float2{mx, sum};
+    __syncthreads();
+    if (wave > 0) return;
+    float2 x = joined[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) x.x = fmaxf(x.x, joined[w].x);
+    mx = x.x;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      sum += joined[w].y * __builtin_amdgcn_exp2f((joined[w].x - (mx == -__builtin_inff() ? 0.f : mx)) * scale);
+  }
   int64_t id[kPerLane];
   float p[kPerLane], logp[kPerLane];
   bool in, bad = false;
@@ -162,43 +210,92 @@ __global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compa
     }
     return;
   }
-  const float* pm = a.part_max + c * a.np;
-  const float* ps = a.part_sum + c * a.np;
-  float mx = -__builtin_inff();
-  for (int i = lane; i < a.np; i += 64) mx = fmaxf(mx, pm[i]);
-  mx = wave_max(mx);
-  float sum = 0.f;
-  for (int i = lane; i < a.np; i += 64)
-    sum += ps[i] * (pm[i] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(pm[i] - mx));
-  sum = wave_sum(sum);
-  // in base 2, the reference against the logit first: what cancels is exact
-  const float l2 = __builtin_amdgcn_logf(sum);
+  // the largest logit against the listed one first: what cancels is exact
+  const float lsum = kLn2 * __builtin_amdgcn_logf(sum);
   float loss;
   if (a.target) {
-    loss = kLn2 * ((mx - a.zlist[bad ? 0 : c]) + l2);
+    loss = bad ? 0.f : (mx - a.zlist[c]) + lsum;
   } else {
     loss = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
       if (!(p[i] == 0.f) && id[i] < a.n_vocab)             // not p > 0: a NaN teacher shows
-        loss += p[i] * (logp[i] + kLn2 * ((mx - a.zlist[c * a.top + lane + 64 * i]) + l2));
+        loss += p[i] * (logp[i] + ((mx - a.zlist[c * a.top + lane + 64 * i]) * a.inv_tau + lsum));
     loss = wave_sum(loss) * (a.tau * a.tau);
   }
   if (lane == 0) {
     a.loss[t] = bad ? __builtin_nanf("") : loss;
-    a.lse[t] = kLn2 * (mx + l2);
+    a.lse[t] = mx * a.inv_tau + lsum;
   }
 }
 
 // Backward, one workgroup per original row: the row's place among those that
 // take part gets its hidden state and coefficients; a row that does not take
-// part gets a zero gradient.
+// part gets a zero gradient.  kOwnRows: every workgroup finds its row's place
+// and the scales by itself (few rows), which saves the launches before.
+template <bool kOwnRows>
 __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   __shared__ int32_t ids[kMaxTop];
   __shared__ float ps[kMaxTop];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
-  const int c = a.pos[t];
+  int c;
+  float amax;
+  if constexpr (kOwnRows) {
+    __shared__ int32_t before[4], all[4], here[4];
+    __shared__ float tops[4];
+    int mine = 0, total = 0, self = 0;
+    float top = 0.f;
+    for (int64_t u = tid; u < a.m_tok; u += 256) {
+      bool in;
+      if (a.target) {
+        in = a.target[u] >= 0 && a.target[u] < a.n_vocab;
+      } else {
+        in = false;
+        bool bad = false;
+        for (int k = 0; k < a.top; ++k) {
+          const int64_t id = a.index[u * a.top + k];
+          in |= counts(id, a.teacher[u * a.top + k]);
+          bad |= id >= a.n_vocab;
+        }
+        in = in && !bad;
+      }
+      if (!in) continue;
+      const float g = a.dloss[u];
+      top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[u]) : 0.f));
+      ++total;
+      mine += u < t;
+      self |= u == t;
+    }
+    for (int m = 1; m < 64; m <<= 1) {
+      mine += __shfl_xor(mine, m);
+      total += __shfl_xor(total, m);
+      self |= __shfl_xor(self, m);
+    }
+    top = wave_max(top);
+    if ((tid & 63) == 0) {
+      before[tid >> 6] = mine;
+      all[tid >> 6] = total;
+      here[tid >> 6] = self;
+      tops[tid >> 6] = top;
+    }
+    __syncthreads();
+    mine = before[0] + before[1] + before[2] + before[3];
+    c = (here[0] | here[1] | here[2] | here[3]) ? mine : -1;
+    amax = scale_base(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), a.tau);
+    if (tid == 0) {
+      if (c >= 0) a.rows[c] = (int32_t)t;
+      if (t == 0) {
+        a.hdr->count = all[0] + all[1] + all[2] + all[3];
+        a.hdr->amax = amax;
+        a.hdr->up = a.up / amax;
+        a.hdr->down = amax / a.up;
+      }
+    }
+  } else {
+    c = a.pos[t];
+    amax = a.hdr->amax;
+  }
   const int vecs = a.k / 8;
   if (c < 0) {
     if (a.dh) {
@@ -210,7 +307,6 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   const u32x4* src = reinterpret_cast<const u32x4*>(a.h + t * a.h_stride);
   u32x4* dst = reinterpret_cast<u32x4*>(a.hc + (int64_t)c * a.k);
   for (int i = tid; i < vecs; i += 256) dst[i] = src[i];
-  const float amax = a.hdr->amax;
   // divided by the largest coefficient first: equal weights give exactly 1
   const float g = a.dloss[t] * a.tau / amax * a.up;
   if (tid == 0) {
@@ -236,6 +332,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
       }
   }
   __syncthreads();
+  const int wide = (a.top + 7) / 8 * 8;
   // an id listed twice is subtracted once, with both probabilities
   for (int k = tid; k < a.top; k += 256) {
     const int id = ids[k];
@@ -248,7 +345,9 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
       }
     a.index32[(int64_t)c * a.top + k] = first ? id : -1;
     a.sub[(int64_t)c * a.top + k] = g * sum;
+    if (a.near) a.near[(int64_t)c * wide + k] = first ? (uint16_t)(id >> 8) : 0xFFFFu;
   }
+  if (a.near && tid < wide - a.top) a.near[(int64_t)c * wide + a.top + tid] = 0xFFFFu;
 }
 
 }  // namespace
@@ -264,12 +363,21 @@ hipError_t launch_rows(const RowArgs& a, bool backward, hipStream_t s) {
 }
 
 hipError_t launch_finish(const RowArgs& a, bool compact, hipStream_t s) {
-  finish_kernel<<<dim3((unsigned)((a.m_tok + 3) / 4)), 256, 0, s>>>(a, compact);
+  if (a.m_tok <= 1024)
+    finish_kernel<4><<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a, compact);
+  else
+    finish_kernel<1><<<dim3((unsigned)((a.m_tok + 3) / 4)), 256, 0, s>>>(a, compact);
   return hipGetLastError();
 }
 
-hipError_t launch_gather(const RowArgs& a, hipStream_t s) {
-  gather_kernel<<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a);
+// one list entry per thread and row of a workgroup's scan, or next to it
+bool gather_alone(int32_t m_tok, int32_t top) { return m_tok <= 1024 && (int64_t)((m_tok + 255) / 256) * top <= 32; }
+
+hipError_t launch_gather(const RowArgs& a, bool own_rows, hipStream_t s) {
+  if (own_rows)
+    gather_kernel<true><<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a);
+  else
+    gather_kernel<false><<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

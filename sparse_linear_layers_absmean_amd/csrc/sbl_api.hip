@@ -666,7 +666,7 @@ namespace {
 
 constexpr int64_t kMaxHeadTokens = int64_t(1) << 22;
 constexpr int64_t kMaxHeadBytes = int64_t(1) << 31;      // one operand, 32-bit buffer offsets
-constexpr int64_t kHeadGradValues = int64_t(1) << 27;    // logit gradients held at a time (256 MB)
+constexpr int64_t kHeadGradValues = int64_t(1) << 28;    // logit gradients held at a time at most (512 MB)
 
 bool head_shape_ok(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top) {
   return m_tok >= 0 && m_tok <= kMaxHeadTokens && n_vocab >= 1 && n_vocab <= INT32_MAX - 1024 && k >= 8 && k <= kMaxK &&
@@ -676,8 +676,8 @@ bool head_shape_ok(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top) {
 
 // The workspace's parts, in bytes from its start.
 struct HeadLayout {
-  int64_t hdr, rows, pos, flag;
-  int64_t part_max, part_sum, zlist;                             // forward
+  int64_t hdr, rows, pos, flag, near;
+  int64_t stat, zlist;                                           // forward
   int64_t lse2, coef, index32, sub, hc, dz, part;                // backward
   int64_t bytes;
   int64_t np;                                                    // forward: statistics per token
@@ -696,10 +696,10 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
   l.rows = take(m_tok * 4);
   l.pos = take(m_tok * 4);
   l.flag = take(m_tok);
+  l.near = take(top > 1 ? m_tok * ((top + 7) / 8 * 8) * 2 : 0);
   if (!backward) {
     l.np = sbl::head::logits_tiles((int32_t)m_tok, (int32_t)n_vocab);
-    l.part_max = take(m_tok * l.np * 4);
-    l.part_sum = take(m_tok * l.np * 4);
+    l.stat = take(m_tok * l.np * 8);
     l.zlist = take(m_tok * top * 4);
     return l;
   }
@@ -784,6 +784,8 @@ sbl::head::RowArgs head_rows(const HeadCall& c, const HeadLayout& l) {
   r.rows = at<int32_t>(c, l.rows);
   r.pos = at<int32_t>(c, l.pos);
   r.flag = at<uint8_t>(c, l.flag);
+  // lists of more than one id, as long as block numbers fit 16 bits
+  if (c.index && c.top > 1 && c.n_vocab < 65535 * 256) r.near = at<uint16_t>(c, l.near);
   return r;
 }
 
@@ -799,8 +801,7 @@ int head_forward(const HeadCall& c, bool ce, float* loss, float* lse, hipStream_
       ranges_overlap(c.workspace, l.bytes, lse, ob))
     return SBL_ERR_SHAPE;
   sbl::head::RowArgs r = head_rows(c, l);
-  r.part_max = at<float>(c, l.part_max);
-  r.part_sum = at<float>(c, l.part_sum);
+  r.part = at<float2>(c, l.stat);
   r.np = (int32_t)l.np;
   r.zlist = at<float>(c, l.zlist);
   r.loss = loss;
@@ -821,8 +822,8 @@ int head_forward(const HeadCall& c, bool ce, float* loss, float* lse, hipStream_
   a.top = c.top;
   a.scale = sbl::head::kLog2e / c.tau;
   a.index = ce ? c.target : c.index;
-  a.part_max = at<float>(c, l.part_max);
-  a.part_sum = at<float>(c, l.part_sum);
+  a.near = compact ? r.near : nullptr;
+  a.part = at<float2>(c, l.stat);
   a.np = (int32_t)l.np;
   a.zlist = at<float>(c, l.zlist);
   st = launch_status(sbl::head::launch_logits(a, c.dtype == SBL_FP16, false, s));
@@ -864,8 +865,10 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
   r.sub = at<float>(c, l.sub);
   r.hc = at<uint16_t>(c, l.hc);
   r.dh = dh;
-  if ((st = launch_status(sbl::head::launch_rows(r, true, s))) != SBL_OK) return st;
-  if ((st = launch_status(sbl::head::launch_gather(r, s))) != SBL_OK) return st;
+  const bool own_rows = sbl::head::gather_alone(r.m_tok, r.top);
+  if (!own_rows && (st = launch_status(sbl::head::launch_rows(r, true, s))) != SBL_OK) return st;
+  if ((st = launch_status(sbl::head::launch_gather(r, own_rows, s))) != SBL_OK) return st;
+  const int64_t steps = l.range / 64;
   for (int64_t v0 = 0; v0 < c.n_vocab; v0 += l.range) {
     const int64_t n = c.n_vocab - v0 < l.range ? c.n_vocab - v0 : l.range;
     sbl::head::LogitsArgs a{};
@@ -883,20 +886,15 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
     a.lse2 = r.lse2;
     a.coef = r.coef;
     a.index32 = r.index32;
+    a.near = r.near;
     a.sub = r.sub;
     a.dz = at<uint16_t>(c, l.dz);
-    a.ldz = (int32_t)l.range;
     if ((st = launch_status(sbl::head::launch_logits(a, fp16, true, s))) != SBL_OK) return st;
-    if (dw) {
-      const sbl::head::WeightGradArgs g{a.dz, a.ldz, r.hc, r.hdr, a.m_tok, a.n_vocab, a.k, dw + v0 * c.k};
-      if ((st = launch_status(sbl::head::launch_weight_grad(g, fp16, s))) != SBL_OK) return st;
-    }
-    if (dh) {
-      const int64_t steps = (l.range + 63) / 64;
-      const sbl::head::HiddenGradArgs g{a.dz, a.ldz, a.w, r.hdr, a.m_tok, a.n_vocab, a.k, l.splits,
-                                        (int32_t)((steps + l.splits - 1) / l.splits), at<float>(c, l.part), v0 > 0};
-      if ((st = launch_status(sbl::head::launch_hidden_grad(g, fp16, s))) != SBL_OK) return st;
-    }
+    const sbl::head::WeightGradArgs gw{a.dz, r.hc, r.hdr, a.m_tok, a.n_vocab, a.k, dw ? dw + v0 * c.k : nullptr};
+    const sbl::head::HiddenGradArgs gh{a.dz, a.w, r.hdr, a.m_tok, a.n_vocab, a.k, l.splits,
+                                       (int32_t)((steps + l.splits - 1) / l.splits),
+                                       dh ? at<float>(c, l.part) : nullptr, v0 > 0};
+    if ((st = launch_status(sbl::head::launch_grads(gw, gh, fp16, s))) != SBL_OK) return st;
   }
   if (!dh) return SBL_OK;
   return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), l.splits, r.hdr, r.rows, (int32_t)c.m_tok,

@@ -33,26 +33,26 @@ struct LogitsArgs {
   int32_t k;
   int32_t top;                            // listed entries per token
   float scale;                            // log2(e) / tau
+  const uint16_t* near;                   // per row (forward: original) the 256-id blocks of its entries, 8 to a vector,
+                                          //   ~0 where there is none; or NULL
   // forward
   const int64_t* index;                   // [row][top] listed ids of the original rows
-  float* part_max;                        // [token][np] softmax statistics of 128 (or fewer) logits, base 2
-  float* part_sum;
+  float2* part;                           // [token][np] softmax statistics of a tile's ids: max logit, sum of
+                                          //   2^((z - max) scale)
   int32_t np;
-  float* zlist;                           // [token][top] scaled logits at the listed ids
+  float* zlist;                           // [token][top] logits at the listed ids
   // backward
   int64_t v0;                             // first id of this range
   const float* lse2;                      // [token] lse * log2(e)
   const float* coef;                      // [token] softmax coefficient * up
   const int32_t* index32;                 // [token][top] id, or -1 (absent, or merged into an earlier entry)
   const float* sub;                       // [token][top] what to subtract at the id
-  uint16_t* dz;                           // [token][ldz]
-  int32_t ldz;
+  uint16_t* dz;                           // [n_vocab / 256, rounded up][m_tok][256]
 };
 
 // dw[v][d] = down * sum_t dz[t][v] h[t][d] over one range of the vocabulary
 struct WeightGradArgs {
-  const uint16_t* dz;                     // [token][ldz]
-  int32_t ldz;
+  const uint16_t* dz;                     // as LogitsArgs leaves it
   const uint16_t* h;                      // [token][k], taking-part rows
   const Header* hdr;
   int32_t m_tok;
@@ -63,7 +63,6 @@ struct WeightGradArgs {
 // part[s][t][d] (+)= sum over the s-th share of this range's vocabulary of dz[t][v] w[v][d]
 struct HiddenGradArgs {
   const uint16_t* dz;
-  int32_t ldz;
   const uint16_t* w;                      // [n_vocab][k] of this range
   const Header* hdr;
   int32_t m_tok;
@@ -91,9 +90,9 @@ struct RowArgs {
   int32_t* rows;                          // [m_tok] original row of token i
   int32_t* pos;                           // [m_tok] token of an original row, or -1
   uint8_t* flag;                          // [m_tok] distillation: row takes part
+  uint16_t* near;                         // [m_tok][top, rounded up to 8], or NULL (LogitsArgs)
   // forward
-  const float* part_max;
-  const float* part_sum;
+  const float2* part;
   int32_t np;
   const float* zlist;
   float* loss;
@@ -111,11 +110,14 @@ struct RowArgs {
   uint16_t* dh;                           // nullable: rows that are taken out are zeroed
 };
 
+// Up to this many tokens both gradients run in one launch of narrow tiles.
+constexpr int kFewTokens = 64;
+
 int64_t logits_tiles(int32_t m_tok, int32_t n_vocab);     // np of a forward call
 hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStream_t s);
-hipError_t launch_weight_grad(const WeightGradArgs& a, bool fp16, hipStream_t s);
 int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k);
-hipError_t launch_hidden_grad(const HiddenGradArgs& a, bool fp16, hipStream_t s);
+// both gradients of a range (either may be absent: dw or part NULL)
+hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, bool fp16, hipStream_t s);
 // dh[rows[t]] = down * sum_s part[s][t]
 hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,
                                int32_t k, uint16_t* dh, bool fp16, hipStream_t s);
@@ -124,7 +126,10 @@ hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr,
 // as the backward needs); backward: also the header's scales
 hipError_t launch_rows(const RowArgs& a, bool backward, hipStream_t s);
 hipError_t launch_finish(const RowArgs& a, bool compact, hipStream_t s);
-hipError_t launch_gather(const RowArgs& a, hipStream_t s);
+// backward, after launch_rows: coefficients, lists and hidden states of the rows that take part.  own_rows: in place
+// of launch_rows as well (few rows and list entries: gather_alone), in the same launch
+bool gather_alone(int32_t m_tok, int32_t top);
+hipError_t launch_gather(const RowArgs& a, bool own_rows, hipStream_t s);
 
 }  // namespace head
 }  // namespace sbl

@@ -72,16 +72,19 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, ui
 // each of its 1 KB pieces (piece q = wave + waves * p), per lane.  The pieces
 // are a fixed distance apart, except when rows are picked from a list (kList).
 // kPerm (kRows only): rows are read in the order of the logits' row operand, below.
-template <Order O, int T, int WAVES, bool kPerm, bool kList = false>
+// kPanel (kRows only): the memory is panels of 256 k, [panel][row][256].
+template <Order O, int T, int WAVES, bool kPerm, bool kList = false, bool kPanel = false>
 struct Source {
   static constexpr int kPieces = T * kBK * 2 / 1024 / WAVES;
   static_assert(T * kBK * 2 % (1024 * WAVES) == 0 && WAVES % 4 == 0, "whole pieces");
-  static_assert(O == kRows || T == 256, "a 512-byte LDS row");
+  static_assert(O == kRows || T == 256 || T == 128, "LDS rows of 512 or 256 bytes");
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t off[kList ? kPieces : 1];
   uint32_t apart;                          // bytes from piece to piece
   uint32_t step;                           // bytes per 64 k
   int chunk;                               // kRows: first k of this lane's chunk
+  uint32_t panel;                          // kPanel: bytes per panel
+  int first;                               // kPanel: step 0's place, in steps from the first panel
 
   __device__ __forceinline__ int first_chunk(int wave, int lane) const {
     // f of row 8q + lane / 8 (q % 4 = wave % 4): see Reader
@@ -112,28 +115,23 @@ struct Source {
   // kCols: memory rows of `pitch` bytes, the tile's columns start at byte `col`
   __device__ __forceinline__ void init_cols(__amdgpu_buffer_rsrc_t rs, int wave, int lane, uint32_t pitch,
                                             uint32_t col) {
-    static_assert(O == kCols && (O != kCols || WAVES == 4 || WAVES == 8), "F repeats every 16 k");
+    static_assert(O == kCols, "");
     rsrc = rs;
     step = kBK * pitch;
-    const int k = 2 * wave + (lane >> 5);
-    const int F = (k & 3) | (((k >> 3) & 1) << 2);
-    if constexpr (kList) {                 // 4 waves: a piece is 8 k on, where F differs
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p)
-        off[p] = (uint32_t)(k + 2 * WAVES * p) * pitch + col +
-                 16u * ((lane & 31) ^ ((F ^ (WAVES == 4 ? 4 * (p & 1) : 0)) << 1));
-      apart = 0;
-    } else {
-      static_assert(kList || O != kCols || WAVES == 8, "pieces 16 k apart");
-      off[0] = (uint32_t)k * pitch + col + 16u * ((lane & 31) ^ (F << 1));
-      apart = 2 * WAVES * pitch;
-    }
+    constexpr int kRowLanes = T / 8, kPer = 64 / kRowLanes;     // lanes per memory row, rows per piece
+    const int k = kPer * wave + lane / kRowLanes, c = lane % kRowLanes;
+    apart = kPer * WAVES * pitch;
+    static_assert(!kList && (O != kCols || kPer * WAVES % 16 == 0), "F repeats every 16 k");
+    off[0] = (uint32_t)k * pitch + col + 16u * (c ^ (2 * unit_of(k)));
   }
+  static __device__ __forceinline__ int unit_of(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
   // piece p of step ks into `lds`; k at or past klen read zeros (an offset with
   // the top bit set is beyond every buffer, kFar rows stay so)
   __device__ __forceinline__ void piece(uint8_t* lds, int wave, int p, int ks, int klen) const {
     const bool ok = O == kRows ? ks * kBK + chunk < klen : ks * kBK < klen;
-    const uint32_t o = kList ? off[kList ? p : 0] + (uint32_t)ks * step : off[0] + ((uint32_t)ks * step + p * apart);
+    const uint32_t at = kPanel ? (uint32_t)((first + ks) >> 2) * panel + (uint32_t)((first + ks) & 3) * (kBK * 2)
+                               : (uint32_t)ks * step;
+    const uint32_t o = kList ? off[kList ? p : 0] + at : off[0] + (at + p * apart);
     dma16(rsrc, lds + 1024 * (wave + WAVES * p), o | (ok ? 0u : kFar));
   }
   __device__ __forceinline__ void fetch(uint8_t* lds, int wave, int ks, int klen) const {
@@ -201,13 +199,14 @@ __device__ __forceinline__ void wave_barrier() {
 // LDS stages are arrays of their own, picked by compile-time indexes, so that
 // the compiler can tell a stage being filled from one being read: otherwise it
 // waits for every direct load before the next LDS read.
-template <class E, Order OA, Order OB, int TM, int TN, int WM, int WN, bool kPerm, bool kListA = false, bool kListB = false>
+template <class E, Order OA, Order OB, int TM, int TN, int WM, int WN, bool kPerm, bool kListB = false,
+          bool kPanelB = false>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kMT = TM / WM / 16, kNT = TN / WN / 16;
   static constexpr int kBytesA = TM * kBK * 2, kStageBytes = (TM + TN) * kBK * 2;
-  Source<OA, TM, kWaves, kPerm, kListA> sa;
-  Source<OB, TN, kWaves, false, kListB> sb;
+  Source<OA, TM, kWaves, kPerm> sa;
+  Source<OB, TN, kWaves, false, kListB, kPanelB> sb;
   v4f acc[kMT][kNT];
 
   __device__ __forceinline__ void clear() {
@@ -215,6 +214,32 @@ struct Tile {
     for (int i = 0; i < kMT; ++i)
 #pragma unroll
       for (int j = 0; j < kNT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // One step at most: klen <= 64.
+  __device__ __forceinline__ void run_once(uint8_t* st, int wave, int lane, int klen) {
+    Reader<OA, TM, kPerm> ra;
+    Reader<OB, TN, false> rb;
+    ra.init(wave / WN * (TM / WM), lane);
+    rb.init(wave % WN * (TN / WN), lane);
+    clear();
+    sa.fetch(st, wave, 0, klen);
+    sb.fetch(st + kBytesA, wave, 0, klen);
+    wait_vm<0>();
+    wave_barrier();
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      if (32 * kk >= klen) break;
+      v8s b[kNT];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) b[j] = rb.get(st + kBytesA, j, kk);
+#pragma unroll
+      for (int i = 0; i < kMT; ++i) {
+        const v8s a = ra.get(st, i, kk);
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a, b[j], acc[i][j]);
+      }
+    }
   }
 
   // Narrow tiles (bound by memory): STAGES - 1 steps in flight, two
@@ -270,15 +295,16 @@ struct Tile {
     wait_vm<0>();                          // every direct load has landed before the workgroup can leave
   }
 
-  // 256 x 256 on 8 waves of 128 x 64, two per SIMD: half of a wave's registers
-  // hold the sums, most of the rest two sets of operands.  A step's 64 k are
-  // two halves of 32 MFMAs; while the MFMAs of one half run, the operands of
-  // the next are read and the step after next is fetched, so a wave never
-  // waits for what it has just asked for:
-  //   half 0   reads the operands of half 1; then (barrier: everyone has read
-  //            this stage) starts refilling this stage with step ks + 2
-  //   half 1   (wait: step ks + 1 has landed everywhere) reads its half 0
-  //            and sends the rest of the refill
+  // 256 x 256 on 8 waves of 128 x 64, two per SIMD, in two groups of one wave per
+  // SIMD that take turns: while one group's 32 MFMAs of a half step (32 k) run
+  // on operands it already holds, the other reads its own next operands and
+  // sends loads; a barrier ends each turn.  Step ks + 1 is fetched at the first
+  // turn of step ks into the other stage, which both groups have read by then.
+  // start() fetches step 0; what a caller loads between the two comes with it.
+  __device__ __forceinline__ void start(uint8_t* const (&st)[2], int wave, int klen) {
+    sa.fetch(st[0], wave, 0, klen);
+    sb.fetch(st[0] + kBytesA, wave, 0, klen);
+  }
   __device__ __forceinline__ void run_wide(uint8_t* const (&st)[2], int wave, int lane, int klen) {
     static_assert(TM == 256 && TN == 256 && WM == 2 && WN == 4, "eight waves of 128 x 64");
     Reader<OA, TM, kPerm> ra;
@@ -287,61 +313,46 @@ struct Tile {
     rb.init(wave % WN * (TN / WN), lane);
     clear();
     const int steps = (klen + kBK - 1) / kBK;
+    wait_vm<0>();
     if (steps <= 0) return;
-    v8s a[2][kMT], b[2][kNT];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      sa.fetch(st[s], wave, s, klen);
-      sb.fetch(st[s] + kBytesA, wave, s, klen);
-    }
-    wait_vm<8>();
     wave_barrier();
+    const bool second = wave >= 4;         // waves 4 to 7 share the SIMDs of waves 0 to 3
+    if (second) wave_barrier();            // and run one turn behind
+    v8s a[kMT], b[kNT];
+    auto read = [&](uint8_t* from, int kk) {
 #pragma unroll
-    for (int j = 0; j < kNT; ++j) b[0][j] = rb.get(st[0] + kBytesA, j, 0);
+      for (int j = 0; j < kNT; ++j) b[j] = rb.get(from + kBytesA, j, kk);
 #pragma unroll
-    for (int i = 0; i < kMT; ++i) a[0][i] = ra.get(st[0], i, 0);
-    // the 4 MFMAs of row tile i on operand set f
-    auto mma4 = [&](int f, int i) {
-#pragma unroll
-      for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a[f][i], b[f][j], acc[i][j]);
+      for (int i = 0; i < kMT; ++i) a[i] = ra.get(from, i, kk);
     };
-    // a quarter of the next operand set
-    auto load3 = [&](int f, int n, uint8_t* from, int kk) {
-      b[f][n] = rb.get(from + kBytesA, n, kk);
-      a[f][2 * n] = ra.get(from, 2 * n, kk);
-      a[f][2 * n + 1] = ra.get(from, 2 * n + 1, kk);
+    auto multiply = [&]() {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a[i], b[j], acc[i][j]);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto turn = [&]() {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      wave_barrier();
     };
     auto step = [&](int ks, int u) {
       ra.pin();
       rb.pin();
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        load3(1, n, st[u], 1);
-        mma4(0, n);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      read(st[u], 0);
+      __builtin_amdgcn_sched_barrier(0);
+      sa.fetch(st[u ^ 1], wave, ks + 1, klen);
+      sb.fetch(st[u ^ 1] + kBytesA, wave, ks + 1, klen);
+      turn();
+      multiply();
       wave_barrier();
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        sa.piece(st[u], wave, n, ks + 2, klen);
-        mma4(0, 4 + n);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      wait_vm<4>();
+      read(st[u], 1);
+      wait_vm<0>();
+      turn();
+      multiply();
       wave_barrier();
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        load3(0, n, st[u ^ 1], 0);
-        sb.piece(st[u] + kBytesA, wave, n, ks + 2, klen);
-        mma4(1, n);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int n = 4; n < 8; ++n) {
-        mma4(1, n);
-        __builtin_amdgcn_sched_barrier(0);
-      }
     };
     // an odd last step is paired with one of zeros: a branch around it costs
     // the loop its register allocation
@@ -349,6 +360,7 @@ struct Tile {
       step(ks, 0);
       step(ks + 1, 1);
     }
+    if (!second) wave_barrier();           // the second group's last turn
     wait_vm<0>();                          // every direct load has landed before the workgroup can leave
   }
 };

@@ -12,10 +12,10 @@ from oracle import head_oracle as H
 
 pytestmark = pytest.mark.gpu
 
-# tokens around the tile variants' edges (32, 64, 256), vocabularies around
+# tokens around the tile variants' edges (32, 64, 128, 256), vocabularies around
 # 32, 128 and 256, features with and without a whole last step of 64
 SHAPES = [(1, 1, 8), (1, 1000, 256), (3, 130, 72), (32, 500, 64), (33, 31, 136), (64, 1003, 128), (65, 257, 264),
-          (257, 300, 64), (300, 1003, 200), (513, 777, 328)]
+          (128, 385, 72), (129, 640, 136), (257, 300, 64), (300, 1003, 200), (513, 777, 328)]
 TYPES = ["bfloat16", "float16"]
 
 
@@ -159,11 +159,11 @@ def _rel(a, b):
 
 
 def test_several_ranges_of_the_vocabulary():
-    """More than 2^27 logits: the backward takes the vocabulary in two ranges,
+    """More than 2^28 logits: the backward takes the vocabulary in two ranges,
     and the last one is not a whole number of tiles."""
     import torch
     from sparse_linear_layers_absmean_amd import sbl
-    t, v, d = 4100, 40007, 128
+    t, v, d = 4100, 70007, 128
     say(f"head_ce ranges t={t} v={v} d={d}")
     g = torch.Generator(device="cuda").manual_seed(5)
     h = torch.randn(t, d, generator=g, device="cuda").bfloat16()

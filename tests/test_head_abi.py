@@ -122,8 +122,8 @@ def test_workspace_bytes(lib):
         fwd, bwd = f(t, v, k, 64, 0), f(t, v, k, 64, 1)
         assert 0 < fwd and f(t, v, k, 1, 0) <= fwd and 0 < bwd
         # never the logits: the forward keeps two words per 32 ids or more (and the
-        # lists); the backward 2^27 gradients of 16 bits (256 ids at least) beside
+        # lists); the backward 2^28 gradients of 16 bits (256 ids at least) beside
         # copies and partial sums of h
-        assert fwd <= t * (8 * (v // 32 + 1) + 4 * 64 + 12) + 8 * 4096
-        assert f(t, v, k, 1, 1) <= 2 * max(1 << 27, 256 * t) + 2 * t * k * (1 + 2 * 1024) + 32 * t + 16 * 4096
+        assert fwd <= t * (8 * (v // 32 + 1) + 4 * 64 + 12 + 2 * 64) + 8 * 4096
+        assert f(t, v, k, 1, 1) <= 2 * max(1 << 28, 256 * t) + 2 * t * k * (1 + 2 * 1024) + 32 * t + 16 * 4096
 
