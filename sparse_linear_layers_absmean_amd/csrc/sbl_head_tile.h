@@ -295,12 +295,19 @@ struct Tile {
     wait_vm<0>();                          // every direct load has landed before the workgroup can leave
   }
 
-  // 256 x 256 on 8 waves of 128 x 64, two per SIMD, in two groups of one wave per
-  // SIMD that take turns: while one group's 32 MFMAs of a half step (32 k) run
-  // on operands it already holds, the other reads its own next operands and
-  // sends loads; a barrier ends each turn.  Step ks + 1 is fetched at the first
-  // turn of step ks into the other stage, which both groups have read by then.
-  // start() fetches step 0; what a caller loads between the two comes with it.
+  // 256 x 256 on 8 waves of 128 x 64, two per SIMD: half of a wave's registers
+  // hold the sums, most of the rest two sets of operands.  A step's 64 k are
+  // two halves of 32 MFMAs; while the MFMAs of one half run, the operands of
+  // the next are read, so a wave never waits for what it has just asked for:
+  //   half 0   reads the operands of half 1; then (barrier: everyone has read
+  //            this stage) refilling this stage with step ks + 2 begins
+  //   half 1   (wait: step ks + 1 has landed everywhere) reads that step's
+  //            half 0; the refill goes on
+  // The 8 loads of a refill are spread over the 12 groups of 4 MFMAs that may
+  // send them (kSlots).  Sent closer together they hold up the waves: logits
+  // of 2048 x 32000 x 3200 in 314 us so, 325 with one per group from the first,
+  // 357 with all in the first four groups.  start() fetches step 0; what a
+  // caller loads between the two comes with it.
   __device__ __forceinline__ void start(uint8_t* const (&st)[2], int wave, int klen) {
     sa.fetch(st[0], wave, 0, klen);
     sb.fetch(st[0] + kBytesA, wave, 0, klen);
@@ -313,46 +320,68 @@ struct Tile {
     rb.init(wave % WN * (TN / WN), lane);
     clear();
     const int steps = (klen + kBK - 1) / kBK;
-    wait_vm<0>();
-    if (steps <= 0) return;
+    sa.fetch(st[1], wave, 1, klen);
+    sb.fetch(st[1] + kBytesA, wave, 1, klen);
+    wait_vm<8>();
     wave_barrier();
-    const bool second = wave >= 4;         // waves 4 to 7 share the SIMDs of waves 0 to 3
-    if (second) wave_barrier();            // and run one turn behind
-    v8s a[kMT], b[kNT];
-    auto read = [&](uint8_t* from, int kk) {
+    v8s a[2][kMT], b[2][kNT];
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) b[j] = rb.get(from + kBytesA, j, kk);
+    for (int j = 0; j < kNT; ++j) b[0][j] = rb.get(st[0] + kBytesA, j, 0);
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) a[i] = ra.get(from, i, kk);
-    };
-    auto multiply = [&]() {
-      __builtin_amdgcn_s_setprio(1);
+    for (int i = 0; i < kMT; ++i) a[0][i] = ra.get(st[0], i, 0);
+    // The 4 MFMAs of row tile i on operand set f.  With both operands down the
+    // k axis (twice the LDS reads) a wave that has its operands goes first:
+    // 5% there, and 1 to 2% the other way with fewer reads.
+    constexpr bool kFirst = OA == kCols && OB == kCols;
+    auto mma4 = [&](int f, int i) {
+      if constexpr (kFirst) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int i = 0; i < kMT; ++i)
-#pragma unroll
-        for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a[i], b[j], acc[i][j]);
-      __builtin_amdgcn_s_setprio(0);
+      for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a[f][i], b[f][j], acc[i][j]);
+      if constexpr (kFirst) __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto turn = [&]() {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      wave_barrier();
+    // a quarter of the next operand set
+    auto load3 = [&](int f, int n, uint8_t* from, int kk) {
+      b[f][n] = rb.get(from + kBytesA, n, kk);
+      a[f][2 * n] = ra.get(from, 2 * n, kk);
+      a[f][2 * n + 1] = ra.get(from, 2 * n + 1, kk);
+    };
+    // load q of a refill goes before group kSlots[q] of the step's 16, 3 of them
+    // before the wait
+    constexpr int kSlots[8] = {5, 6, 7, 9, 11, 12, 13, 15};
+    auto send = [&](int group, int ks, int u) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (kSlots[q] == group) {
+          if (q < 4)
+            sa.piece(st[u], wave, q, ks + 2, klen);
+          else
+            sb.piece(st[u] + kBytesA, wave, q - 4, ks + 2, klen);
+        }
     };
     auto step = [&](int ks, int u) {
       ra.pin();
       rb.pin();
-      read(st[u], 0);
-      __builtin_amdgcn_sched_barrier(0);
-      sa.fetch(st[u ^ 1], wave, ks + 1, klen);
-      sb.fetch(st[u ^ 1] + kBytesA, wave, ks + 1, klen);
-      turn();
-      multiply();
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        load3(1, n, st[u], 1);
+        mma4(0, n);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       wave_barrier();
-      read(st[u], 1);
-      wait_vm<0>();
-      turn();
-      multiply();
+#pragma unroll
+      for (int n = 4; n < 8; ++n) {
+        send(n, ks, u);
+        mma4(0, n);
+      }
+      wait_vm<3>();
       wave_barrier();
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        if (n < 4) load3(0, n, st[u ^ 1], 0);
+        send(8 + n, ks, u);
+        mma4(1, n);
+      }
     };
     // an odd last step is paired with one of zeros: a branch around it costs
     // the loop its register allocation
@@ -360,7 +389,6 @@ struct Tile {
       step(ks, 0);
       step(ks + 1, 1);
     }
-    if (!second) wave_barrier();           // the second group's last turn
     wait_vm<0>();                          // every direct load has landed before the workgroup can leave
   }
 };
