@@ -507,7 +507,8 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  * (BF16) or 2^14 (FP16): relative error 2^-8 (2^-11) of each at most, the size
  * of the outputs' own rounding.  Sums have a fixed order: results repeat bit for bit.
  * Limits: 8 <= k <= 131072, k % 8 == 0; n_vocab * k <= 2^34; m_tok <= 2^22 and
- * (m_tok + 256) * k and the span of h at most 2^30 values; 1e-4 <= tau <= 1e4.
+ * (m_tok + 256) * k and the span of h at most 2^30 values; m_tok * n_vocab below
+ * about 2^42; 1e-4 <= tau <= 1e4.
  * m_tok == 0: the forward does nothing, the backward sets dw to zero.
  * Non-finite h or w in rows that take part: results are unspecified. */
 typedef enum { SBL_BF16 = 0, SBL_FP16 = 1 } sbl_dtype;

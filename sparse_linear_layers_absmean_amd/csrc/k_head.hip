@@ -36,9 +36,9 @@ __device__ __forceinline__ uint16_t* dz_at(uint16_t* dz, int m_tok, int t, int v
 // the permuted row order 8 consecutive ids per pair of tiles, so softmax
 // statistics reduce over registers and two lane exchanges, and the gradient
 // leaves as 16-byte stores.
-template <class E, int TM, int TN, int WM, int WN, bool kBackward, class St>
+template <class E, int TM, int TN, int WM, int WN, bool kBackward, int kPolicy, class St>
 __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const St& st) {
-  using T = Tile<E, kRows, kRows, TM, TN, WM, WN, true, !kBackward>;
+  using T = Tile<E, kRows, kRows, TM, TN, WM, WN, true, !kBackward, false, kPolicy>;
   __shared__ int32_t row_of[kBackward ? 1 : TN];   // original row of each of the tile's tokens, -1: none
   __shared__ float2 stat[kBackward ? 1 : WM][kBackward ? 1 : TN];
   constexpr int kHits = TN <= 64 ? 512 : 1024;
@@ -101,7 +101,7 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
     else
       return a.index[(int64_t)row_of[tok] * a.top + ent];
   };
-  if (TN == 256 && a.near) {
+  if (a.near) {
     // 8 entries' 256-id blocks in 16 bytes, 4 loads of a thread at a time
     constexpr int kBatch = 4;
     const int per_row = (a.top + 7) / 8, units = TN * per_row;
@@ -154,7 +154,8 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
   __syncthreads();
   for (int n = tid; n < hit_count && n < kHits; n += T::kThreads) {
     const int tok = (int)(hit_at[n] >> 8 & 255), ent = (int)(hit_at[n] >> 16);
-    hit_at[n] |= (uint32_t)(id_of(tok, ent) - vt0);
+    const int64_t d = id_of(tok, ent) - vt0;     // with blocks: perhaps in the block's other tile; 255 is no row of a
+    hit_at[n] |= d >= 0 && d < TM ? (uint32_t)d : 255u;     // 128-id tile
     if constexpr (kBackward) hit_sub[n] = a.sub[(int64_t)(t0 + tok) * a.top + ent];
   }
   if constexpr (TN == 256)
@@ -307,7 +308,7 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
   }
 }
 
-template <class E, int TM, int TN, int WM, int WN, bool kBackward>
+template <class E, int TM, int TN, int WM, int WN, bool kBackward, int kPolicy = 0>
 __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArgs a) {
   constexpr int kStage = (TM + TN) * kBK * 2;
   __shared__ __align__(16) uint8_t lds0[kStage];
@@ -315,11 +316,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
   if constexpr (TN == 256) {
     uint8_t* const st[2] = {lds0, lds1};
-    logits_tile<E, TM, TN, WM, WN, kBackward>(a, tile, st);
+    logits_tile<E, TM, TN, WM, WN, kBackward, kPolicy>(a, tile, st);
   } else {
     __shared__ __align__(16) uint8_t lds2[kStage];
     uint8_t* const st[3] = {lds0, lds1, lds2};
-    logits_tile<E, TM, TN, WM, WN, kBackward>(a, tile, st);
+    logits_tile<E, TM, TN, WM, WN, kBackward, kPolicy>(a, tile, st);
   }
 }
 
@@ -327,7 +328,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
 // Rows of the tile are features (contiguous in memory, read down the k axis),
 // so a lane's 4 consecutive results are 4 consecutive features of an output row.
 
-template <class E, int TM, int TN, int WM, int WN, class St>
+template <class E, int TM, int TN, int WM, int WN, bool kOnce, class St>
 __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int tile, const St& st) {
   using T = Tile<E, kCols, kCols, TM, TN, WM, WN, false>;
   const int count = a.hdr->count;
@@ -345,8 +346,10 @@ __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int ti
   if constexpr (TN == 256) {
     tl.start(st, wave, count);
     tl.run_wide(st, wave, lane, count);
-  } else {
+  } else if constexpr (kOnce) {
     tl.run_once(st[0], wave, lane, count);
+  } else {
+    tl.template run<2>(st, wave, lane, count);
   }
   lane = lane_again();
   const int wm = wave / WN, wn = wave % WN, r = lane & 15, g = lane >> 4;
@@ -411,24 +414,25 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
     const int t = t0 + wn * (TN / WN) + 16 * j + r, d = dt * TM + wm * (TM / WM) + 16 * i + 4 * g;
     return t < count && d < a.k ? reinterpret_cast<v4f*>(a.part + ((int64_t)s * a.m_tok + t) * a.k + d) : nullptr;
   };
-  v4f old[2][T::kMT];
-  auto load = [&](int j) {
+  constexpr int kHalf = T::kMT / 2;
+  v4f old[2][kHalf];
+  auto load = [&](int n) {                 // half a column tile
 #pragma unroll
-    for (int i = 0; i < T::kMT; ++i) {
-      old[j & 1][i] = v4f{0.f, 0.f, 0.f, 0.f};
-      const v4f* p = at(j, i);
-      if (p) old[j & 1][i] = *p;
+    for (int i = 0; i < kHalf; ++i) {
+      old[n & 1][i] = v4f{0.f, 0.f, 0.f, 0.f};
+      const v4f* p = at(n / 2, (n & 1) * kHalf + i);
+      if (p) old[n & 1][i] = *p;
     }
   };
   if (a.add) load(0);
 #pragma unroll
-  for (int j = 0; j < T::kNT; ++j) {
-    if (a.add && j + 1 < T::kNT) load(j + 1);
+  for (int n = 0; n < 2 * T::kNT; ++n) {
+    if (a.add && n + 1 < 2 * T::kNT) load(n + 1);
 #pragma unroll
-    for (int i = 0; i < T::kMT; ++i) {
-      v4f x = tl.acc[i][j];
-      if (a.add) x += old[j & 1][i];
-      v4f* p = at(j, i);
+    for (int i = 0; i < kHalf; ++i) {
+      v4f x = tl.acc[(n & 1) * kHalf + i][n / 2];
+      if (a.add) x += old[n & 1][i];
+      v4f* p = at(n / 2, (n & 1) * kHalf + i);
       if (p) *p = x;
     }
   }
@@ -456,26 +460,26 @@ __global__ __launch_bounds__(512, 2) void grads_wide_kernel(const WeightGradArgs
   if (i < nh)
     hidden_grad_tile<E, 256, 256, 2, 4>(h, h0 + i, st);
   else if (i < nh + nw)
-    weight_grad_tile<E, 256, 256, 2, 4>(w, w0 + i - nh, st);
+    weight_grad_tile<E, 256, 256, 2, 4, false>(w, w0 + i - nh, st);
 }
 
-// 65 to 128 tokens
+// One of the gradients on smaller tiles.
 template <class E>
-__global__ __launch_bounds__(512, 2) void weight_grad_kernel(const WeightGradArgs a) {
-  __shared__ __align__(16) uint8_t lds0[512 * kBK * 2];
-  __shared__ __align__(16) uint8_t lds1[512 * kBK * 2];
+__global__ __launch_bounds__(256, 2) void weight_grad_kernel(const WeightGradArgs a) {
+  __shared__ __align__(16) uint8_t lds0[256 * kBK * 2];
+  __shared__ __align__(16) uint8_t lds1[256 * kBK * 2];
   uint8_t* const st[2] = {lds0, lds1};
-  weight_grad_tile<E, 256, 256, 2, 4>(a, xcd_tile(blockIdx.x, gridDim.x), st);
+  weight_grad_tile<E, 128, 128, 2, 2, false>(a, xcd_tile(blockIdx.x, gridDim.x), st);
 }
 
-template <class E>
-__global__ __launch_bounds__(512, 2) void hidden_grad_kernel(const HiddenGradArgs a) {
-  constexpr int kStage = (256 + 128) * kBK * 2;
+template <class E, int TM, int TN>
+__global__ __launch_bounds__(TM == 256 ? 512 : 256, 2) void hidden_grad_kernel(const HiddenGradArgs a) {
+  constexpr int kStage = (TM + TN) * kBK * 2;
   __shared__ __align__(16) uint8_t lds0[kStage];
   __shared__ __align__(16) uint8_t lds1[kStage];
   __shared__ __align__(16) uint8_t lds2[kStage];
   uint8_t* const st[3] = {lds0, lds1, lds2};
-  hidden_grad_tile<E, 256, 128, 4, 2>(a, xcd_tile(blockIdx.x, gridDim.x), st);
+  hidden_grad_tile<E, TM, TN, TM / 64, 2>(a, xcd_tile(blockIdx.x, gridDim.x), st);
 }
 
 // Few tokens: dw is bound by its writes, dh by its reads of w, so both go in one
@@ -491,7 +495,7 @@ __global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, c
   const int tile = b < both ? b >> 1 : b - (both >> 1);
   uint8_t* const st[3] = {lds0, lds1, lds2};
   if (is_dw)
-    weight_grad_tile<E, 128, 128, 2, 2>(w, tile, st);
+    weight_grad_tile<E, 128, 128, 2, 2, true>(w, tile, st);
   else
     hidden_grad_tile<E, 128, kFewTokens, 2, 2>(h, tile, st);
 }
@@ -522,49 +526,166 @@ __global__ __launch_bounds__(256) void hidden_final_kernel(const float* part, in
   *reinterpret_cast<uint2*>(dh + (int64_t)rows[t] * k + d) = uint2{E::pack2(x[0], x[1]), E::pack2(x[2], x[3])};
 }
 
-// ids per tile of the logits kernel, and tokens per tile of every kernel
-int vocab_tile(int m_tok) { return m_tok <= kFewTokens ? 128 : 256; }
-int token_tile(int m_tok) { return m_tok <= 32 ? 32 : m_tok <= 64 ? 64 : m_tok <= 128 ? 128 : 256; }
+// ---------------------------------------------------------------- variants
+// Which tiles a product runs on.  Wide tiles (256 x 256) do most per byte moved,
+// but a chip of 256 CUs wants as many tiles; small ones fill it from small
+// products, fit ragged sizes, and share a CU two at a time.  The cost of a
+// variant, in microseconds: rounds of its workgroups (one or two per CU) times
+// its steps of 64 k and what it spends before and after them.  Steps as
+// measured with every CU at work: logits 256 x 256 1.5, 256 x 128 1.0, 128 x 64
+// 0.75 (two per CU; 0.52 alone), 128 x 32 0.5 (0.44); so 512 x 32000 x 3200
+// takes 94 us on the first and 101, 129 and 190 on the others, 559 x 1500 x
+// 6264 takes 134, 101, 50 and 43.
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct LogitsTile {
+  int tm, tn;
+};
+
+LogitsTile logits_variant(int64_t m_tok, int64_t n_vocab, int64_t k) {
+  const struct {
+    LogitsTile tile;
+    int per_cu;
+    float step, alone, more;
+  } all[] = {{{256, 256}, 1, 1.5f, 1.5f, 5.0f},
+             {{256, 128}, 1, 1.0f, 1.0f, 3.5f},
+             {{128, 64}, 2, 0.75f, 0.52f, 3.0f},
+             {{128, 32}, 2, 0.5f, 0.44f, 2.5f}};
+  LogitsTile best = all[0].tile;
+  float least = 1e30f;
+  for (const auto& v : all) {
+    const int64_t tiles = ceil_div(n_vocab, v.tile.tm) * ceil_div(m_tok, v.tile.tn);
+    const float steps = (float)ceil_div(k, kBK);
+    const float cost = tiles <= 256 ? steps * v.alone + v.more
+                                    : (float)ceil_div(tiles, 256 * v.per_cu) * (steps * v.step + v.more);
+    if (cost < least) {
+      least = cost;
+      best = v.tile;
+    }
+  }
+  return best;
+}
+
+// The gradients of one range: tiles of dw (256 x 256 or 128 x 128), of dh
+// (features x tokens), and shares of the vocabulary per dh tile.  A share's
+// partial sums are written and read once more (8 bytes per value, 4.5 TB/s).
+// Wide tiles of both go in one launch, whose last rounds then fill each other:
+// half a tile is lost at its end, not two.  Measured at 2048 x 32000 x 3200:
+// dw 362 us wide, 435 narrow; dh 433 wide, 424 on 256 x 128, 632 on 128 x 64;
+// both wide together 703.  At 263 x 867 x 352: dw 11.8 and 5.5; dh 16.9, 9.1
+// and 5.1.
+struct GradPlan {
+  bool few;                                // at most kFewTokens: grads_kernel
+  bool wide_w;
+  int hd, ht;                              // dh tile
+  int splits;
+};
+
+GradPlan grad_plan(int64_t m_tok, int64_t n_vocab, int64_t k) {
+  const int64_t steps_w = ceil_div(m_tok, kBK), steps_h = ceil_div(n_vocab, kBK);
+  GradPlan p{};
+  if (m_tok <= kFewTokens) {
+    // two workgroups per CU or so, 4 steps each at least
+    const int64_t tiles = ceil_div(k, 128);
+    int64_t s = ceil_div(512, tiles);
+    if (s > steps_h / 4) s = steps_h / 4;
+    return GradPlan{true, false, 128, kFewTokens, s < 1 ? 1 : (int)s};
+  }
+  auto sums = [&](int64_t s) { return (float)(s * m_tok * k) * 8 / 4.5e6f; };
+  const int64_t tiles_w = ceil_div(k, 256) * ceil_div(n_vocab, 256);
+  const float wide_w = (float)ceil_div(tiles_w, 256) * (steps_w * 1.45f + 7);
+  const float narrow_w = (float)ceil_div(ceil_div(k, 128) * ceil_div(n_vocab, 128), 512) * (steps_w * 0.95f + 3.5f);
+  const struct {
+    int hd, ht, slots;
+    float step, more;
+  } all[] = {{256, 256, 256, 1.45f, 8}, {256, 128, 256, 0.82f, 4}, {128, 64, 512, 0.65f, 4}};
+  float least = 1e30f;
+  for (const auto& v : all) {
+    const int64_t tiles = ceil_div(k, v.hd) * ceil_div(m_tok, v.ht);
+    for (int64_t s = 1; s <= 256 && (s == 1 || s * 4 <= steps_h); ++s) {
+      const float each = ceil_div(steps_h, s) * v.step + v.more;
+      const float alone = (float)ceil_div(tiles * s, v.slots) * each + sums(s);
+      const float w = wide_w < narrow_w ? wide_w : narrow_w;
+      if (alone + w + 3 < least) {         // 3: one launch more
+        least = alone + w + 3;
+        p = GradPlan{false, wide_w < narrow_w, v.hd, v.ht, (int)s};
+      }
+      if (v.ht == 256) {
+        const float each_w = steps_w * 1.45f + 7, longest = each > each_w ? each : each_w;
+        float both = (tiles_w * each_w + tiles * s * each) / 256 + (tiles * s < 256 ? longest : each_w) / 2;
+        both = (both > longest ? both : longest) + sums(s) + 3;   // 3: the larger kernel's start
+        if (both < least) {
+          least = both;
+          p = GradPlan{false, true, v.hd, v.ht, (int)s};
+        }
+      }
+    }
+  }
+  return p;
+}
 
 template <class E, bool kBackward>
 hipError_t logits(const LogitsArgs& a, hipStream_t s) {
-  const int tm = vocab_tile(a.m_tok), tn = token_tile(a.m_tok);
-  const dim3 grid((unsigned)(((int64_t)a.n_vocab + tm - 1) / tm * ((a.m_tok + tn - 1) / tn)));
-  if (tn == 32)
+  const LogitsTile t = logits_variant(a.m_tok, a.n_vocab, a.k);
+  const dim3 grid((unsigned)(ceil_div(a.n_vocab, t.tm) * ceil_div(a.m_tok, t.tn)));
+  // one token tile of a forward reads the weights once: with more of them than
+  // stay cached (256 MB in all), past the cache (205 MB: 42 -> 37 us at one
+  // token; 88 MB read again and again from the cache: 21 -> 27 us)
+  const bool once = !kBackward && a.m_tok <= t.tn && (int64_t)a.n_vocab * a.k * 2 > (int64_t(128) << 20);
+  if (t.tn == 32 && once)
+    logits_kernel<E, 128, 32, 4, 1, false, kNt><<<grid, 256, 0, s>>>(a);
+  else if (t.tn == 64 && once)
+    logits_kernel<E, 128, 64, 4, 1, false, kNt><<<grid, 256, 0, s>>>(a);
+  else if (t.tn == 32)
     logits_kernel<E, 128, 32, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
-  else if (tn == 64)
+  else if (t.tn == 64)
     logits_kernel<E, 128, 64, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
-  else if (tn == 128)
+  else if (t.tn == 128)
     logits_kernel<E, 256, 128, 4, 2, kBackward><<<grid, 512, 0, s>>>(a);
   else
     logits_kernel<E, 256, 256, 2, 4, kBackward><<<grid, 512, 0, s>>>(a);
   return hipGetLastError();
 }
 
+// n_vocab of w and h is this range's; the plan is that of a whole range
 template <class E>
-hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, hipStream_t s) {
-  const int tn = token_tile(h.m_tok);
-  const int td = tn <= kFewTokens ? 128 : 256;
-  const int n_w = w.dw ? (w.k + td - 1) / td * ((w.n_vocab + td - 1) / td) : 0;
-  const int n_h = h.part ? (h.k + td - 1) / td * ((h.m_tok + tn - 1) / tn) * h.splits : 0;
-  if (tn <= kFewTokens) {
-    grads_kernel<E><<<dim3((unsigned)(n_w + n_h)), 256, 0, s>>>(w, h, n_w, n_h);
-  } else if (tn == 256) {
-    grads_wide_kernel<E><<<dim3((unsigned)(8 * ((n_w + 7) / 8 + (n_h + 7) / 8))), 512, 0, s>>>(w, h, n_w, n_h);
-  } else {
-    if (n_w > 0) weight_grad_kernel<E><<<dim3((unsigned)n_w), 512, 0, s>>>(w);
+hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, const GradPlan& p, hipStream_t s) {
+  const int tw = p.few || !p.wide_w ? 128 : 256;
+  const unsigned n_w = w.dw ? (unsigned)(ceil_div(w.k, tw) * ceil_div(w.n_vocab, tw)) : 0;
+  const unsigned n_h = h.part ? (unsigned)(ceil_div(h.k, p.hd) * ceil_div(h.m_tok, p.ht) * p.splits) : 0;
+  if (p.few) {
+    grads_kernel<E><<<dim3(n_w + n_h), 256, 0, s>>>(w, h, n_w, n_h);
+    return hipGetLastError();
+  }
+  if (p.ht == 256 && (p.wide_w || n_w == 0)) {
+    grads_wide_kernel<E><<<dim3(8 * ((n_w + 7) / 8 + (n_h + 7) / 8)), 512, 0, s>>>(w, h, n_w, n_h);
+    return hipGetLastError();
+  }
+  if (n_w > 0) {
+    const HiddenGradArgs none{};
+    if (p.wide_w)
+      grads_wide_kernel<E><<<dim3(8 * ((n_w + 7) / 8)), 512, 0, s>>>(w, none, n_w, 0);
+    else
+      weight_grad_kernel<E><<<dim3(n_w), 256, 0, s>>>(w);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (n_h > 0) hidden_grad_kernel<E><<<dim3((unsigned)n_h), 512, 0, s>>>(h);
+  }
+  if (n_h > 0) {
+    const WeightGradArgs none{};
+    if (p.ht == 256)
+      grads_wide_kernel<E><<<dim3(8 * ((n_h + 7) / 8)), 512, 0, s>>>(none, h, 0, n_h);
+    else if (p.ht == 128)
+      hidden_grad_kernel<E, 256, 128><<<dim3(n_h), 512, 0, s>>>(h);
+    else
+      hidden_grad_kernel<E, 128, 64><<<dim3(n_h), 256, 0, s>>>(h);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t logits_tiles(int32_t m_tok, int32_t n_vocab) {
-  const int tm = vocab_tile(m_tok);
-  return ((int64_t)n_vocab + tm - 1) / tm;
+int64_t logits_tiles(int32_t m_tok, int32_t n_vocab, int32_t k) {
+  return m_tok < 1 ? 1 : ceil_div(n_vocab, logits_variant(m_tok, n_vocab, k).tm);
 }
 
 hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStream_t s) {
@@ -572,22 +693,13 @@ hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStrea
   return backward ? logits<Bf16, true>(a, s) : logits<Bf16, false>(a, s);
 }
 
-hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, bool fp16, hipStream_t s) {
-  return fp16 ? grads<Fp16>(w, h, s) : grads<Bf16>(w, h, s);
+int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k) {
+  return m_tok < 1 ? 1 : grad_plan(m_tok, n_vocab, k).splits;
 }
 
-// Shares of a range per hidden-gradient tile.  Few tokens: two workgroups per
-// CU or so, 4 steps each at least.  More: short enough to go round with the
-// launch's weight-gradient tiles, a third of a CU's work at most.
-int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k) {
-  if (m_tok < 1) return 1;
-  const int tn = token_tile(m_tok), td = m_tok <= kFewTokens ? 128 : 256;
-  const int64_t tiles = (int64_t)((k + td - 1) / td) * ((m_tok + tn - 1) / tn);
-  const int64_t steps = ((int64_t)n_vocab + kBK - 1) / kBK;
-  const int64_t want = m_tok <= 128 ? 512 : 427;
-  int64_t s = (want + tiles - 1) / tiles;
-  if (s > steps / 4) s = steps / 4;
-  return s < 1 ? 1 : (int)s;
+hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t range, bool fp16, hipStream_t s) {
+  const GradPlan p = grad_plan(w.m_tok, range, w.k);
+  return fp16 ? grads<Fp16>(w, h, p, s) : grads<Bf16>(w, h, p, s);
 }
 
 hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,

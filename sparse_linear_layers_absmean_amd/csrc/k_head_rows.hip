@@ -149,6 +149,28 @@ __global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compa
   const int64_t c = compact ? a.pos[t] : t;
   const bool there = c >= 0;
   const float scale = kLog2e / a.tau;
+  // what does not depend on the statistics comes first: its loads overlap theirs
+  int64_t id[kPerLane];
+  float p[kPerLane], logp[kPerLane], zl[kPerLane];
+  bool in, bad = false;
+  if (a.target) {
+    const int64_t y = a.target[t];
+    in = y >= 0;
+    bad = y >= a.n_vocab;
+    zl[0] = in && !bad && there ? a.zlist[c] : 0.f;
+  } else {
+    if (kWaves == 1 || wave == 0) teacher_row(a, t, lane, id, p, logp);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      const bool mine = (kWaves == 1 || wave == 0) && id[i] >= 0;
+      any |= mine;
+      bad |= mine && id[i] >= a.n_vocab;
+      zl[i] = mine && id[i] < a.n_vocab && there ? a.zlist[c * a.top + lane + 64 * i] : 0.f;
+    }
+    in = __ballot(any) != 0;
+    bad = __ballot(bad) != 0;
+  }
   // the statistics, 4 entries of a lane at a time
   float mx = -__builtin_inff(), sum = 0.f;
   if (there) {
@@ -185,24 +207,6 @@ __global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compa
     for (int w = 0; w < kWaves; ++w)
       sum += joined[w].y * __builtin_amdgcn_exp2f((joined[w].x - (mx == -__builtin_inff() ? 0.f : mx)) * scale);
   }
-  int64_t id[kPerLane];
-  float p[kPerLane], logp[kPerLane];
-  bool in, bad = false;
-  if (a.target) {
-    const int64_t y = a.target[t];
-    in = y >= 0;
-    bad = y >= a.n_vocab;
-  } else {
-    teacher_row(a, t, lane, id, p, logp);
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      any |= id[i] >= 0;
-      bad |= id[i] >= a.n_vocab;
-    }
-    in = __ballot(any) != 0;
-    bad = __ballot(bad) != 0;
-  }
   if (!in) {
     if (lane == 0) {
       a.loss[t] = 0.f;
@@ -214,13 +218,13 @@ __global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compa
   const float lsum = kLn2 * __builtin_amdgcn_logf(sum);
   float loss;
   if (a.target) {
-    loss = bad ? 0.f : (mx - a.zlist[c]) + lsum;
+    loss = bad ? 0.f : (mx - zl[0]) + lsum;
   } else {
     loss = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
       if (!(p[i] == 0.f) && id[i] < a.n_vocab)             // not p > 0: a NaN teacher shows
-        loss += p[i] * (logp[i] + ((mx - a.zlist[c * a.top + lane + 64 * i]) * a.inv_tau + lsum));
+        loss += p[i] * (logp[i] + ((mx - zl[i]) * a.inv_tau + lsum));
     loss = wave_sum(loss) * (a.tau * a.tau);
   }
   if (lane == 0) {
@@ -233,6 +237,8 @@ __global__ __launch_bounds__(256) void finish_kernel(const RowArgs a, bool compa
 // take part gets its hidden state and coefficients; a row that does not take
 // part gets a zero gradient.  kOwnRows: every workgroup finds its row's place
 // and the scales by itself (few rows), which saves the launches before.
+constexpr int kAloneRows = 1024;
+
 template <bool kOwnRows>
 __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   __shared__ int32_t ids[kMaxTop];
@@ -244,22 +250,23 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   if constexpr (kOwnRows) {
     __shared__ int32_t before[4], all[4], here[4];
     __shared__ float tops[4];
+    __shared__ int32_t any[kAloneRows], wrong[kAloneRows];
+    if (!a.target) {                       // a thread per list entry
+      for (int u = tid; u < a.m_tok; u += 256) any[u] = wrong[u] = 0;
+      __syncthreads();
+      const int entries = a.m_tok * a.top;
+#pragma unroll 4
+      for (int e = tid; e < entries; e += 256) {
+        const int64_t id = a.index[e];
+        if (counts(id, a.teacher[e])) any[e / a.top] = 1;
+        if (id >= a.n_vocab) wrong[e / a.top] = 1;
+      }
+      __syncthreads();
+    }
     int mine = 0, total = 0, self = 0;
     float top = 0.f;
     for (int64_t u = tid; u < a.m_tok; u += 256) {
-      bool in;
-      if (a.target) {
-        in = a.target[u] >= 0 && a.target[u] < a.n_vocab;
-      } else {
-        in = false;
-        bool bad = false;
-        for (int k = 0; k < a.top; ++k) {
-          const int64_t id = a.index[u * a.top + k];
-          in |= counts(id, a.teacher[u * a.top + k]);
-          bad |= id >= a.n_vocab;
-        }
-        in = in && !bad;
-      }
+      const bool in = a.target ? a.target[u] >= 0 && a.target[u] < a.n_vocab : any[u] && !wrong[u];
       if (!in) continue;
       const float g = a.dloss[u];
       top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[u]) : 0.f));
@@ -370,8 +377,8 @@ hipError_t launch_finish(const RowArgs& a, bool compact, hipStream_t s) {
   return hipGetLastError();
 }
 
-// one list entry per thread and row of a workgroup's scan, or next to it
-bool gather_alone(int32_t m_tok, int32_t top) { return m_tok <= 1024 && (int64_t)((m_tok + 255) / 256) * top <= 32; }
+// few enough list entries for every workgroup to read them all
+bool gather_alone(int32_t m_tok, int32_t top) { return m_tok <= kAloneRows && m_tok * top <= 8 * 1024; }
 
 hipError_t launch_gather(const RowArgs& a, bool own_rows, hipStream_t s) {
   if (own_rows)

@@ -670,7 +670,8 @@ constexpr int64_t kHeadGradValues = int64_t(1) << 28;    // logit gradients held
 
 bool head_shape_ok(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top) {
   return m_tok >= 0 && m_tok <= kMaxHeadTokens && n_vocab >= 1 && n_vocab <= INT32_MAX - 1024 && k >= 8 && k <= kMaxK &&
-         k % 8 == 0 && n_vocab * k <= kMaxElems && (m_tok + 256) * k * 2 <= kMaxHeadBytes && top >= 1 &&
+         k % 8 == 0 && n_vocab * k <= kMaxElems && (m_tok + 256) * k * 2 <= kMaxHeadBytes &&
+         (n_vocab / 128 + 1) * (m_tok / 32 + 1) < int64_t(1) << 30 && top >= 1 &&
          top <= sbl::head::kMaxTop;
 }
 
@@ -698,7 +699,7 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
   l.flag = take(m_tok);
   l.near = take(top > 1 ? m_tok * ((top + 7) / 8 * 8) * 2 : 0);
   if (!backward) {
-    l.np = sbl::head::logits_tiles((int32_t)m_tok, (int32_t)n_vocab);
+    l.np = sbl::head::logits_tiles((int32_t)m_tok, (int32_t)n_vocab, (int32_t)k);
     l.stat = take(m_tok * l.np * 8);
     l.zlist = take(m_tok * top * 4);
     return l;
@@ -894,7 +895,7 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
     const sbl::head::HiddenGradArgs gh{a.dz, a.w, r.hdr, a.m_tok, a.n_vocab, a.k, l.splits,
                                        (int32_t)((steps + l.splits - 1) / l.splits),
                                        dh ? at<float>(c, l.part) : nullptr, v0 > 0};
-    if ((st = launch_status(sbl::head::launch_grads(gw, gh, fp16, s))) != SBL_OK) return st;
+    if ((st = launch_status(sbl::head::launch_grads(gw, gh, (int32_t)l.range, fp16, s))) != SBL_OK) return st;
   }
   if (!dh) return SBL_OK;
   return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), l.splits, r.hdr, r.rows, (int32_t)c.m_tok,

@@ -113,11 +113,12 @@ struct RowArgs {
 // Up to this many tokens both gradients run in one launch of narrow tiles.
 constexpr int kFewTokens = 64;
 
-int64_t logits_tiles(int32_t m_tok, int32_t n_vocab);     // np of a forward call
+int64_t logits_tiles(int32_t m_tok, int32_t n_vocab, int32_t k);     // np of a forward call
 hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStream_t s);
+// shares per dh tile, for ranges of n_vocab ids
 int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k);
-// both gradients of a range (either may be absent: dw or part NULL)
-hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, bool fp16, hipStream_t s);
+// both gradients of a range (either may be absent: dw or part NULL); `range`: ids of a whole range
+hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t range, bool fp16, hipStream_t s);
 // dh[rows[t]] = down * sum_s part[s][t]
 hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,
                                int32_t k, uint16_t* dh, bool fp16, hipStream_t s);

@@ -64,16 +64,20 @@ constexpr uint32_t kFar = 0x80000000u;    // a buffer offset beyond every buffer
 
 enum Order { kRows, kCols };
 
+constexpr int kNt = 2;                    // cache-policy bit "nt" of a buffer load: read once
+
+template <int kPolicy>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, kPolicy);
 }
 
 // Where one wave's share of an operand tile comes from: the byte offset of
 // each of its 1 KB pieces (piece q = wave + waves * p), per lane.  The pieces
 // are a fixed distance apart, except when rows are picked from a list (kList).
 // kPerm (kRows only): rows are read in the order of the logits' row operand, below.
-// kPanel (kRows only): the memory is panels of 256 k, [panel][row][256].
-template <Order O, int T, int WAVES, bool kPerm, bool kList = false, bool kPanel = false>
+// kPanel (kRows only): the memory is panels of 256 k, [panel][row][256], with
+// zeros from klen to the end of its panel.
+template <Order O, int T, int WAVES, bool kPerm, bool kList = false, bool kPanel = false, int kPolicy = 0>
 struct Source {
   static constexpr int kPieces = T * kBK * 2 / 1024 / WAVES;
   static_assert(T * kBK * 2 % (1024 * WAVES) == 0 && WAVES % 4 == 0, "whole pieces");
@@ -128,11 +132,11 @@ struct Source {
   // piece p of step ks into `lds`; k at or past klen read zeros (an offset with
   // the top bit set is beyond every buffer, kFar rows stay so)
   __device__ __forceinline__ void piece(uint8_t* lds, int wave, int p, int ks, int klen) const {
-    const bool ok = O == kRows ? ks * kBK + chunk < klen : ks * kBK < klen;
+    const bool ok = O == kRows && !kPanel ? ks * kBK + chunk < klen : ks * kBK < klen;
     const uint32_t at = kPanel ? (uint32_t)((first + ks) >> 2) * panel + (uint32_t)((first + ks) & 3) * (kBK * 2)
                                : (uint32_t)ks * step;
     const uint32_t o = kList ? off[kList ? p : 0] + at : off[0] + (at + p * apart);
-    dma16(rsrc, lds + 1024 * (wave + WAVES * p), o | (ok ? 0u : kFar));
+    dma16<kPolicy>(rsrc, lds + 1024 * (wave + WAVES * p), o | (ok ? 0u : kFar));
   }
   __device__ __forceinline__ void fetch(uint8_t* lds, int wave, int ks, int klen) const {
 #pragma unroll
@@ -200,12 +204,12 @@ __device__ __forceinline__ void wave_barrier() {
 // the compiler can tell a stage being filled from one being read: otherwise it
 // waits for every direct load before the next LDS read.
 template <class E, Order OA, Order OB, int TM, int TN, int WM, int WN, bool kPerm, bool kListB = false,
-          bool kPanelB = false>
+          bool kPanelB = false, int kPolicyA = 0>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kMT = TM / WM / 16, kNT = TN / WN / 16;
   static constexpr int kBytesA = TM * kBK * 2, kStageBytes = (TM + TN) * kBK * 2;
-  Source<OA, TM, kWaves, kPerm> sa;
+  Source<OA, TM, kWaves, kPerm, false, false, kPolicyA> sa;
   Source<OB, TN, kWaves, false, kListB, kPanelB> sb;
   v4f acc[kMT][kNT];
 
@@ -340,15 +344,20 @@ struct Tile {
       if constexpr (kFirst) __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     };
-    // a quarter of the next operand set
-    auto load3 = [&](int f, int n, uint8_t* from, int kk) {
-      b[f][n] = rb.get(from + kBytesA, n, kk);
-      a[f][2 * n] = ra.get(from, 2 * n, kk);
-      a[f][2 * n + 1] = ra.get(from, 2 * n + 1, kk);
+    // two of the next 12 operands
+    auto load2 = [&](int f, int n, uint8_t* from, int kk) {
+#pragma unroll
+      for (int q = 2 * n; q < 2 * n + 2; ++q) {
+        constexpr int kOrder[12] = {0,4,5,1,6,7,2,8,9,3,10,11};   // 0 to 3: column tiles, 4 on: row tiles
+        if (kOrder[q] < 4)
+          b[f][kOrder[q] & 3] = rb.get(from + kBytesA, kOrder[q] & 3, kk);
+        else
+          a[f][kOrder[q] - 4] = ra.get(from, kOrder[q] - 4, kk);
+      }
     };
     // load q of a refill goes before group kSlots[q] of the step's 16, 3 of them
     // before the wait
-    constexpr int kSlots[8] = {5, 6, 7, 9, 11, 12, 13, 15};
+    constexpr int kSlots[8] = {6, 7, 9, 11, 12, 13, 14, 15};
     auto send = [&](int group, int ks, int u) {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -363,22 +372,22 @@ struct Tile {
       ra.pin();
       rb.pin();
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        load3(1, n, st[u], 1);
+      for (int n = 0; n < 6; ++n) {
+        if (n < 6) load2(1, n, st[u], 1);
         mma4(0, n);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       wave_barrier();
 #pragma unroll
-      for (int n = 4; n < 8; ++n) {
+      for (int n = 6; n < 8; ++n) {
         send(n, ks, u);
         mma4(0, n);
       }
-      wait_vm<3>();
+      wait_vm<2>();
       wave_barrier();
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        if (n < 4) load3(0, n, st[u ^ 1], 0);
+        if (n < 6) load2(0, n, st[u ^ 1], 0);
         send(8 + n, ks, u);
         mma4(1, n);
       }

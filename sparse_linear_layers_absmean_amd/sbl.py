@@ -169,8 +169,8 @@ def _ptr(t, dtype, nbytes: int, name: str):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:                               # torch.cuda.current_stream().cuda_stream, without the object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -508,29 +508,29 @@ def sbl_head_workspace_bytes(m_tok: int, n_vocab: int, k: int, top: int = 1, bac
 def _head_args(h, w):
     """(h pointer, row stride, w pointer, dtype, m_tok, n_vocab, k): h [m_tok][k] with rows of
     contiguous values (any row stride that is a multiple of 8), w [n_vocab][k] contiguous, both
-    bfloat16 (or its 16-bit patterns as int16/uint16) or both float16."""
-    for t, name in ((h, "h"), (w, "w")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != 2:
-            raise ValueError(f"{name} must have two dimensions")
+    bfloat16 (or its 16-bit patterns as int16/uint16) or both float16, on the current GPU."""
+    if not isinstance(h, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise TypeError("h and w must be torch.Tensors")
+    if h.dim() != 2 or w.dim() != 2:
+        raise ValueError("h and w must have two dimensions")
     fp16 = h.dtype == torch.float16
     types = (torch.float16,) if fp16 else _W16
     if h.dtype not in types or w.dtype not in types:
         raise TypeError(f"h and w have dtypes {h.dtype} and {w.dtype}, expected two of {types}")
     m_tok, k = h.shape
-    n_vocab = w.shape[0]
-    if w.shape[1] != k:
-        raise ValueError(f"h has {k} features, w {w.shape[1]}")
-    if not h.is_cuda:
-        raise ValueError("h must be a GPU tensor")
-    if h.device != w.device:
-        raise ValueError("h and w must be on one device")
-    if h.stride(1) != 1 and k > 1 or (m_tok > 1 and h.stride(0) < k):
+    n_vocab, kw = w.shape
+    if kw != k:
+        raise ValueError(f"h has {k} features, w {kw}")
+    if not h.is_cuda or h.device != w.device or h.get_device() != torch.cuda.current_device():
+        raise ValueError("h and w must be on the current GPU")
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    stride, step = h.stride()
+    if m_tok <= 1:
+        stride = k
+    if step != 1 and k > 1 or stride < k:
         raise ValueError("h must have rows of contiguous values")
-    stride = h.stride(0) if m_tok > 1 else k
-    return (h.data_ptr() if m_tok else None, stride, _ptr(w, types, n_vocab * k * 2, "w"),
-            SBL_FP16 if fp16 else SBL_BF16, m_tok, n_vocab, k)
+    return (h.data_ptr() if m_tok else None, stride, w.data_ptr(), SBL_FP16 if fp16 else SBL_BF16, m_tok, n_vocab, k)
 
 
 def _teacher_args(index, teacher, m_tok: int):
@@ -544,53 +544,48 @@ def _teacher_args(index, teacher, m_tok: int):
 def sbl_head_ce_forward(h, w, target, loss, lse, workspace, stream=None):
     """Cross entropy of the output head: h [m_tok][k], w [n_vocab][k] (16-bit), target int64
     [m_tok] (negative: row taken out) -> loss, lse fp32 [m_tok].  The logits are never stored."""
-    lib = load()
-    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
-    st = lib.sbl_head_ce_forward(hp, stride, wp, dtype, _ptr(target, torch.int64, m_tok * 8, "target"), m_tok, n_vocab,
-                                 k, _ptr(loss, torch.float32, m_tok * 4, "loss"),
-                                 _ptr(lse, torch.float32, m_tok * 4, "lse"), _ptr(workspace, None, 0, "workspace"),
-                                 _nbytes(workspace), _stream(stream))
-    _check("sbl_head_ce_forward", st)
+    head = _head_args(h, w)
+    n = head[4] * 4
+    _check("sbl_head_ce_forward", load().sbl_head_ce_forward(
+        *head[:4], _ptr(target, torch.int64, 2 * n, "target"), *head[4:], _ptr(loss, torch.float32, n, "loss"),
+        _ptr(lse, torch.float32, n, "lse"), _ptr(workspace, None, 0, "workspace"), _nbytes(workspace),
+        _stream(stream)))
 
 
 def sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw, workspace, dlse=None, stream=None):
     """Gradients of the cross entropy: dloss (and dlse) fp32 [m_tok] -> dh [m_tok][k] and dw
     [n_vocab][k] in the type of h and w (either may be None)."""
-    lib = load()
-    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
-    st = lib.sbl_head_ce_backward(hp, stride, wp, dtype, _ptr(target, torch.int64, m_tok * 8, "target"),
-                                  _ptr(lse, torch.float32, m_tok * 4, "lse"),
-                                  _ptr(dloss, torch.float32, m_tok * 4, "dloss"),
-                                  _ptr(dlse, torch.float32, m_tok * 4, "dlse"), m_tok, n_vocab, k,
-                                  _ptr(dh, h.dtype, m_tok * k * 2, "dh"), _ptr(dw, w.dtype, n_vocab * k * 2, "dw"),
-                                  _ptr(workspace, None, 0, "workspace"), _nbytes(workspace), _stream(stream))
-    _check("sbl_head_ce_backward", st)
+    head = _head_args(h, w)
+    m_tok, n_vocab, k = head[4:]
+    n = m_tok * 4
+    _check("sbl_head_ce_backward", load().sbl_head_ce_backward(
+        *head[:4], _ptr(target, torch.int64, 2 * n, "target"), _ptr(lse, torch.float32, n, "lse"),
+        _ptr(dloss, torch.float32, n, "dloss"), _ptr(dlse, torch.float32, n, "dlse"), m_tok, n_vocab, k,
+        _ptr(dh, h.dtype, m_tok * k * 2, "dh"), _ptr(dw, w.dtype, n_vocab * k * 2, "dw"),
+        _ptr(workspace, None, 0, "workspace"), _nbytes(workspace), _stream(stream)))
 
 
 def sbl_head_kd_forward(h, w, index, teacher, tau: float, loss, lse, workspace, stream=None):
     """Distillation from a teacher's top logits: index int64, teacher fp32 [m_tok][top]
     (negative index: no entry), tau the temperature -> loss, lse fp32 [m_tok]."""
-    lib = load()
-    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
-    ip, tp, top = _teacher_args(index, teacher, m_tok)
-    st = lib.sbl_head_kd_forward(hp, stride, wp, dtype, ip, tp, top, tau, m_tok, n_vocab, k,
-                                 _ptr(loss, torch.float32, m_tok * 4, "loss"),
-                                 _ptr(lse, torch.float32, m_tok * 4, "lse"), _ptr(workspace, None, 0, "workspace"),
-                                 _nbytes(workspace), _stream(stream))
-    _check("sbl_head_kd_forward", st)
+    head = _head_args(h, w)
+    n = head[4] * 4
+    _check("sbl_head_kd_forward", load().sbl_head_kd_forward(
+        *head[:4], *_teacher_args(index, teacher, head[4]), tau, *head[4:], _ptr(loss, torch.float32, n, "loss"),
+        _ptr(lse, torch.float32, n, "lse"), _ptr(workspace, None, 0, "workspace"), _nbytes(workspace),
+        _stream(stream)))
 
 
 def sbl_head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, dh, dw, workspace, stream=None):
     """Gradients of the distillation loss: dloss fp32 [m_tok] -> dh [m_tok][k] and dw
     [n_vocab][k] in the type of h and w (either may be None)."""
-    lib = load()
-    hp, stride, wp, dtype, m_tok, n_vocab, k = _head_args(h, w)
-    ip, tp, top = _teacher_args(index, teacher, m_tok)
-    st = lib.sbl_head_kd_backward(hp, stride, wp, dtype, ip, tp, top, tau, _ptr(lse, torch.float32, m_tok * 4, "lse"),
-                                  _ptr(dloss, torch.float32, m_tok * 4, "dloss"), m_tok, n_vocab, k,
-                                  _ptr(dh, h.dtype, m_tok * k * 2, "dh"), _ptr(dw, w.dtype, n_vocab * k * 2, "dw"),
-                                  _ptr(workspace, None, 0, "workspace"), _nbytes(workspace), _stream(stream))
-    _check("sbl_head_kd_backward", st)
+    head = _head_args(h, w)
+    m_tok, n_vocab, k = head[4:]
+    _check("sbl_head_kd_backward", load().sbl_head_kd_backward(
+        *head[:4], *_teacher_args(index, teacher, m_tok), tau, _ptr(lse, torch.float32, m_tok * 4, "lse"),
+        _ptr(dloss, torch.float32, m_tok * 4, "dloss"), m_tok, n_vocab, k, _ptr(dh, h.dtype, m_tok * k * 2, "dh"),
+        _ptr(dw, w.dtype, n_vocab * k * 2, "dw"), _ptr(workspace, None, 0, "workspace"), _nbytes(workspace),
+        _stream(stream)))
 
 
 # ---------------------------------------------------------------- allocating conveniences
@@ -646,25 +641,33 @@ def new_head_workspace(m_tok: int, n_vocab: int, k: int, top: int = 1, backward:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _head_workspace(workspace, h, w, top: int, backward: bool, stream):
-    if workspace is None:
-        workspace = new_head_workspace(h.shape[0], w.shape[0], h.shape[1], top, backward, h.device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)      # freed on return, still in use there
-    return workspace
+def _new_scratch(lib, head, top: int, backward: int, device, stream):
+    """A workspace of the caching allocator, for one call on `stream`."""
+    nbytes = lib.sbl_head_workspace_bytes(*head[4:], top, backward)
+    scratch = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        scratch.record_stream(stream)                # freed on return, still in use there
+    return scratch, nbytes
 
 
 def head_ce(h, w, target, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_ce_forward; returns (loss, lse)."""
-    workspace = _head_workspace(workspace, h, w, 1, False, stream)
-    loss, lse = torch.empty((2, h.shape[0]), dtype=torch.float32, device=h.device).unbind(0)
-    sbl_head_ce_forward(h, w, target, loss, lse, workspace, stream=stream)
+    lib, head = load(), _head_args(h, w)
+    m_tok, device = head[4], h.device
+    scratch, nbytes = (workspace, _nbytes(workspace)) if workspace is not None else \
+        _new_scratch(lib, head, 1, 0, device, stream)
+    loss = torch.empty(m_tok, dtype=torch.float32, device=device)
+    lse = torch.empty(m_tok, dtype=torch.float32, device=device)
+    _check("sbl_head_ce_forward", lib.sbl_head_ce_forward(
+        *head[:4], _ptr(target, torch.int64, 8 * m_tok, "target"), *head[4:], loss.data_ptr(), lse.data_ptr(),
+        _ptr(scratch, None, 0, "workspace"), nbytes, _stream(stream)))
     return loss, lse
 
 
 def head_ce_backward(h, w, target, lse, dloss, dlse=None, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_ce_backward; returns (dh, dw)."""
-    workspace = _head_workspace(workspace, h, w, 1, True, stream)
+    if workspace is None:
+        workspace, _ = _new_scratch(load(), _head_args(h, w), 1, 1, h.device, stream)
     dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
     sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw, workspace, dlse=dlse, stream=stream)
     return dh, dw
@@ -672,15 +675,23 @@ def head_ce_backward(h, w, target, lse, dloss, dlse=None, workspace=None, stream
 
 def head_kd(h, w, index, teacher, tau: float, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_kd_forward; returns (loss, lse)."""
-    workspace = _head_workspace(workspace, h, w, index.shape[1], False, stream)
-    loss, lse = torch.empty((2, h.shape[0]), dtype=torch.float32, device=h.device).unbind(0)
-    sbl_head_kd_forward(h, w, index, teacher, tau, loss, lse, workspace, stream=stream)
+    lib, head = load(), _head_args(h, w)
+    m_tok, device = head[4], h.device
+    entries = _teacher_args(index, teacher, m_tok)
+    scratch, nbytes = (workspace, _nbytes(workspace)) if workspace is not None else \
+        _new_scratch(lib, head, entries[2], 0, device, stream)
+    loss = torch.empty(m_tok, dtype=torch.float32, device=device)
+    lse = torch.empty(m_tok, dtype=torch.float32, device=device)
+    _check("sbl_head_kd_forward", lib.sbl_head_kd_forward(
+        *head[:4], *entries, tau, *head[4:], loss.data_ptr(), lse.data_ptr(), _ptr(scratch, None, 0, "workspace"),
+        nbytes, _stream(stream)))
     return loss, lse
 
 
 def head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_kd_backward; returns (dh, dw)."""
-    workspace = _head_workspace(workspace, h, w, index.shape[1], True, stream)
+    if workspace is None:
+        workspace, _ = _new_scratch(load(), _head_args(h, w), index.shape[1], 1, h.device, stream)
     dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
     sbl_head_kd_backward(h, w, index, teacher, tau, lse, dloss, dh, dw, workspace, stream=stream)
     return dh, dw

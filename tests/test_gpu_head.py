@@ -15,7 +15,9 @@ pytestmark = pytest.mark.gpu
 # tokens around the tile variants' edges (32, 64, 128, 256), vocabularies around
 # 32, 128 and 256, features with and without a whole last step of 64
 SHAPES = [(1, 1, 8), (1, 1000, 256), (3, 130, 72), (32, 500, 64), (33, 31, 136), (64, 1003, 128), (65, 257, 264),
-          (128, 385, 72), (129, 640, 136), (257, 300, 64), (300, 1003, 200), (513, 777, 328)]
+          (128, 385, 72), (129, 640, 136), (257, 300, 64), (300, 1003, 200), (513, 777, 328),
+          # vocabularies large enough for the larger tiles of each product
+          (70, 33001, 136), (500, 32700, 72), (600, 9001, 1032)]
 TYPES = ["bfloat16", "float16"]
 
 
@@ -113,7 +115,8 @@ def test_cross_entropy_matches_oracle(t, v, d, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("top,tau", [(1, 1.0), (5, 2.0), (64, 4.0), (200, 0.5)])
-@pytest.mark.parametrize("t,v,d", [(1, 1, 8), (3, 130, 72), (40, 1003, 128), (65, 257, 264), (300, 1003, 200)])
+@pytest.mark.parametrize("t,v,d", [(1, 1, 8), (3, 130, 72), (40, 1003, 128), (65, 257, 264), (300, 1003, 200),
+                                   (500, 32700, 72)])
 def test_distillation_matches_oracle(t, v, d, top, tau, dtype):
     import torch
     from sparse_linear_layers_absmean_amd import sbl

@@ -68,6 +68,7 @@ CALLS = {"ce_fwd": _ce_fwd, "ce_bwd": _ce_bwd, "kd_fwd": _kd_fwd, "kd_bwd": _kd_
     (dict(k=0, hs=0), SHAPE), (dict(k=60), SHAPE), (dict(k=131080, hs=131080), SHAPE),
     (dict(v=(1 << 34) // 64 + 1), SHAPE),                       # n_vocab * k
     (dict(m=1 << 18, k=4096, hs=4096), SHAPE),                  # (m_tok + 256) * k
+    (dict(m=1 << 22, v=1 << 24), SHAPE),                        # m_tok * n_vocab
     (dict(hs=56), SHAPE), (dict(hs=68), SHAPE), (dict(m=9, hs=1 << 27), SHAPE),
     (dict(dtype=2), UNSUPPORTED), (dict(dtype=-1), UNSUPPORTED),
     (dict(h=None), NULL), (dict(w=None), NULL), (dict(ws=None), WORKSPACE), (dict(wsb=0), WORKSPACE),
