@@ -22,12 +22,12 @@ namespace {
 // the thread index occupies a register during the products.
 __device__ __forceinline__ int lane_again() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0)); }
 
-// The logit gradients of a range, in panels of 256 ids: [panel][m_tok][256].  A
+// The logit gradients of a range, in panels of 256 ids: [panel][rows][256].  A
 // 256 x 256 tile is one run of 128 KB, wherever it is written or read, and rows
 // are 512 bytes apart (rows of the whole range, 64 or 128 KB apart, would touch
 // a page each).
-__device__ __forceinline__ uint16_t* dz_at(uint16_t* dz, int m_tok, int t, int v) {
-  return dz + ((int64_t)(v >> 8) * m_tok + t) * 256 + (v & 255);
+__device__ __forceinline__ uint16_t* dz_at(uint16_t* dz, int rows, int t, int v) {
+  return dz + ((int64_t)(v >> 8) * rows + t) * 256 + (v & 255);
 }
 
 // ---------------------------------------------------------------- logits
@@ -53,7 +53,9 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
   const int gv = nvt - group * kGroup < kGroup ? nvt - group * kGroup : kGroup;
   const int vt = group * kGroup + in_group % gv, tt = in_group / gv;
   const int t0 = tt * TN;
-  if (t0 >= count) return;
+  // few tokens, backward: rows without a token are written too, as zeros
+  const int half = kBackward ? a.half : 0;
+  if (t0 >= count && half == 0) return;
   const int64_t vt0 = (int64_t)vt * TM;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int lane = tid & 63;
@@ -61,7 +63,8 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
   const int64_t wrows = a.n_vocab - vt0 < TM ? a.n_vocab - vt0 : TM;
   tl.sa.init_rows(make_rsrc(a.w + vt0 * a.k, wrows * a.k * 2), wave, lane, 2 * a.k);
   if constexpr (kBackward) {
-    tl.sb.init_rows(make_rsrc(a.h + (int64_t)t0 * a.k, (int64_t)(count - t0) * a.k * 2), wave, lane, 2 * a.k);
+    const int left = count > t0 ? count - t0 : 0;
+    tl.sb.init_rows(make_rsrc(a.h + (int64_t)t0 * a.k, (int64_t)left * a.k * 2), wave, lane, 2 * a.k);
   } else {
     for (int i = tid; i < TN; i += T::kThreads) {
       const int t = t0 + i;
@@ -209,13 +212,17 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           tl.acc[i][j][e] = coef[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(tl.acc[i][j][e], a.scale, -lse2[j]));
-      if (t < count) {
-        uint16_t* o = dz_at(a.dz, a.m_tok, t, vw) + 8 * g;
+      if (t < (half > 0 ? half : count)) {
+        uint16_t* o = dz_at(a.dz, a.dz_rows, t, vw) + 8 * g;
 #pragma unroll
         for (int i = 0; i < kMT; i += 2) {
           const v4f x = tl.acc[i][j], y = tl.acc[i + 1][j];
-          *reinterpret_cast<u32x4*>(o + 16 * i) =
-              u32x4{E::pack2(x[0], x[1]), E::pack2(x[2], x[3]), E::pack2(y[0], y[1]), E::pack2(y[2], y[3])};
+          const u32x4 v = u32x4{E::pack2(x[0], x[1]), E::pack2(x[2], x[3]), E::pack2(y[0], y[1]), E::pack2(y[2], y[3])};
+          *reinterpret_cast<u32x4*>(o + 16 * i) = v;
+          if (half > 0)                    // what the rounding left, to rows of its own
+            *reinterpret_cast<u32x4*>(o + 256 * half + 16 * i) =
+                u32x4{E::rest2(x[0], x[1], v[0]), E::rest2(x[2], x[3], v[1]), E::rest2(y[0], y[1], v[2]),
+                      E::rest2(y[2], y[3], v[3])};
         }
       }
     }
@@ -266,7 +273,12 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
         if (mine) a.zlist[t * a.top + hk] = val;
       } else {
         const float hsub = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sub), src));
-        if (mine) *dz_at(a.dz, a.m_tok, (int)t, vw + hr) = (uint16_t)E::pack2(val - hsub, 0.f);
+        if (mine) {
+          uint16_t* o = dz_at(a.dz, a.dz_rows, (int)t, vw + hr);
+          const uint32_t v = E::pack2(val - hsub, 0.f);
+          *o = (uint16_t)v;
+          if (half > 0) o[256 * half] = (uint16_t)E::rest2(val - hsub, 0.f, v);
+        }
       }
     }
   };
@@ -328,10 +340,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
 // Rows of the tile are features (contiguous in memory, read down the k axis),
 // so a lane's 4 consecutive results are 4 consecutive features of an output row.
 
-template <class E, int TM, int TN, int WM, int WN, bool kOnce, class St>
+template <class E, int TM, int TN, int WM, int WN, bool kShort, class St>
 __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int tile, const St& st) {
   using T = Tile<E, kCols, kCols, TM, TN, WM, WN, false>;
-  const int count = a.hdr->count;
+  const int count = a.rows > 0 ? a.rows : a.hdr->count;
   const int ndt = (a.k + TM - 1) / TM, nvt = (a.n_vocab + TN - 1) / TN;
   constexpr int kGroup = 4;
   const int group = tile / (kGroup * ndt), in_group = tile % (kGroup * ndt);
@@ -346,8 +358,8 @@ __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int ti
   if constexpr (TN == 256) {
     tl.start(st, wave, count);
     tl.run_wide(st, wave, lane, count);
-  } else if constexpr (kOnce) {
-    tl.run_once(st[0], wave, lane, count);
+  } else if constexpr (kShort) {
+    tl.run_short(st[0], wave, lane, count);
   } else {
     tl.template run<2>(st, wave, lane, count);
   }
@@ -377,7 +389,7 @@ __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int ti
 template <class E, int TM, int TN, int WM, int WN, class St>
 __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int tile, const St& st) {
   using T = Tile<E, kCols, kRows, TM, TN, WM, WN, false, false, true>;
-  const int count = a.hdr->count;
+  const int count = a.rows > 0 ? a.rows : a.hdr->count;
   const int ndt = (a.k + TM - 1) / TM, ntt = (a.m_tok + TN - 1) / TN;
   // a share's tiles together: they read the same rows of w
   const int s = tile / (ndt * ntt), in = tile % (ndt * ntt);
@@ -697,8 +709,9 @@ int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k) {
   return m_tok < 1 ? 1 : grad_plan(m_tok, n_vocab, k).splits;
 }
 
-hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t range, bool fp16, hipStream_t s) {
-  const GradPlan p = grad_plan(w.m_tok, range, w.k);
+hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t m_tok, int32_t range, bool fp16,
+                        hipStream_t s) {
+  const GradPlan p = grad_plan(m_tok, range, w.k);
   return fp16 ? grads<Fp16>(w, h, p, s) : grads<Bf16>(w, h, p, s);
 }
 

@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   __shared__ float ps[kMaxTop];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
-  int c;
+  int c, pad = 0;                          // pad: the half's row that this workgroup zeroes if c < 0
   float amax;
   if constexpr (kOwnRows) {
     __shared__ int32_t before[4], all[4], here[4];
@@ -289,6 +289,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
     __syncthreads();
     mine = before[0] + before[1] + before[2] + before[3];
     c = (here[0] | here[1] | here[2] | here[3]) ? mine : -1;
+    pad = all[0] + all[1] + all[2] + all[3] + (int)(t - mine);
     amax = scale_base(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), a.tau);
     if (tid == 0) {
       if (c >= 0) a.rows[c] = (int32_t)t;
@@ -305,7 +306,11 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   }
   const int vecs = a.k / 8;
   if (c < 0) {
-    if (a.dh) {
+    if (kOwnRows && a.half > 0)
+      for (int i = tid; i < 2 * vecs; i += 256)
+        reinterpret_cast<u32x4*>(a.hc + (int64_t)(i < vecs ? pad : pad + a.half) * a.k)[i < vecs ? i : i - vecs] =
+            u32x4{0, 0, 0, 0};
+    if (a.dh && t < a.m_tok) {
       u32x4* o = reinterpret_cast<u32x4*>(a.dh + t * a.k);
       for (int i = tid; i < vecs; i += 256) o[i] = u32x4{0, 0, 0, 0};
     }
@@ -313,7 +318,10 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   }
   const u32x4* src = reinterpret_cast<const u32x4*>(a.h + t * a.h_stride);
   u32x4* dst = reinterpret_cast<u32x4*>(a.hc + (int64_t)c * a.k);
-  for (int i = tid; i < vecs; i += 256) dst[i] = src[i];
+  for (int i = tid; i < vecs; i += 256) {
+    dst[i] = src[i];
+    if (kOwnRows && a.half > 0) dst[i + (int64_t)a.half * vecs] = src[i];
+  }
   // divided by the largest coefficient first: equal weights give exactly 1
   const float g = a.dloss[t] * a.tau / amax * a.up;
   if (tid == 0) {
@@ -378,11 +386,13 @@ hipError_t launch_finish(const RowArgs& a, bool compact, hipStream_t s) {
 }
 
 // few enough list entries for every workgroup to read them all
-bool gather_alone(int32_t m_tok, int32_t top) { return m_tok <= kAloneRows && m_tok * top <= 8 * 1024; }
+bool gather_alone(int32_t m_tok, int32_t top) {
+  return m_tok <= kFewTokens || (m_tok <= kAloneRows && m_tok * top <= 8 * 1024);
+}
 
 hipError_t launch_gather(const RowArgs& a, bool own_rows, hipStream_t s) {
   if (own_rows)
-    gather_kernel<true><<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a);
+    gather_kernel<true><<<dim3((unsigned)(a.half > 0 ? a.half : a.m_tok)), 256, 0, s>>>(a);
   else
     gather_kernel<false><<<dim3((unsigned)a.m_tok), 256, 0, s>>>(a);
   return hipGetLastError();

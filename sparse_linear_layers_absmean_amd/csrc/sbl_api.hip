@@ -717,9 +717,11 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
   l.coef = take(m_tok * 4);
   l.index32 = take(m_tok * top * 4);
   l.sub = take(m_tok * top * 4);
-  l.hc = take(m_tok * k * 2);
-  l.dz = take(m_tok * l.range * 2);
-  l.part = take((int64_t)l.splits * m_tok * k * 4);
+  // few tokens: two rows each (LogitsArgs::half)
+  const int64_t rows = m_tok > sbl::head::kFewTokens ? m_tok : 2 * sbl::head::few_half(m_tok);
+  l.hc = take(rows * k * 2);
+  l.dz = take(rows * l.range * 2);
+  l.part = take((int64_t)l.splits * rows * k * 4);
   return l;
 }
 
@@ -866,6 +868,8 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
   r.sub = at<float>(c, l.sub);
   r.hc = at<uint16_t>(c, l.hc);
   r.dh = dh;
+  const int32_t half = sbl::head::few_half(c.m_tok), rows = half > 0 ? 2 * half : 0;
+  r.half = half;
   const bool own_rows = sbl::head::gather_alone(r.m_tok, r.top);
   if (!own_rows && (st = launch_status(sbl::head::launch_rows(r, true, s))) != SBL_OK) return st;
   if ((st = launch_status(sbl::head::launch_gather(r, own_rows, s))) != SBL_OK) return st;
@@ -890,16 +894,19 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
     a.near = r.near;
     a.sub = r.sub;
     a.dz = at<uint16_t>(c, l.dz);
+    a.dz_rows = half > 0 ? rows : a.m_tok;
+    a.half = half;
     if ((st = launch_status(sbl::head::launch_logits(a, fp16, true, s))) != SBL_OK) return st;
-    const sbl::head::WeightGradArgs gw{a.dz, r.hc, r.hdr, a.m_tok, a.n_vocab, a.k, dw ? dw + v0 * c.k : nullptr};
-    const sbl::head::HiddenGradArgs gh{a.dz, a.w, r.hdr, a.m_tok, a.n_vocab, a.k, l.splits,
+    const sbl::head::WeightGradArgs gw{a.dz, r.hc, r.hdr, rows, a.dz_rows, a.n_vocab, a.k, dw ? dw + v0 * c.k : nullptr};
+    const sbl::head::HiddenGradArgs gh{a.dz, a.w, r.hdr, rows, a.dz_rows, a.n_vocab, a.k, l.splits,
                                        (int32_t)((steps + l.splits - 1) / l.splits),
                                        dh ? at<float>(c, l.part) : nullptr, v0 > 0};
-    if ((st = launch_status(sbl::head::launch_grads(gw, gh, (int32_t)l.range, fp16, s))) != SBL_OK) return st;
+    if ((st = launch_status(sbl::head::launch_grads(gw, gh, a.m_tok, (int32_t)l.range, fp16, s))) != SBL_OK) return st;
   }
   if (!dh) return SBL_OK;
-  return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), l.splits, r.hdr, r.rows, (int32_t)c.m_tok,
-                                                      (int32_t)c.k, dh, fp16, s));
+  return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), half > 0 ? 2 * l.splits : l.splits, r.hdr,
+                                                      r.rows, half > 0 ? half : (int32_t)c.m_tok, (int32_t)c.k, dh,
+                                                      fp16, s));
 }
 
 }  // namespace

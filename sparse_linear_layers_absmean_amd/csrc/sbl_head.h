@@ -47,7 +47,10 @@ struct LogitsArgs {
   const float* coef;                      // [token] softmax coefficient * up
   const int32_t* index32;                 // [token][top] id, or -1 (absent, or merged into an earlier entry)
   const float* sub;                       // [token][top] what to subtract at the id
-  uint16_t* dz;                           // [n_vocab / 256, rounded up][m_tok][256]
+  uint16_t* dz;                           // [n_vocab / 256, rounded up][dz_rows][256]
+  int32_t dz_rows;
+  int32_t half;                           // 0, or (few tokens) rows of dz: half for the tokens' gradients, as many again
+                                          //   for what their rounding to 16 bits left
 };
 
 // dw[v][d] = down * sum_t dz[t][v] h[t][d] over one range of the vocabulary
@@ -55,6 +58,7 @@ struct WeightGradArgs {
   const uint16_t* dz;                     // as LogitsArgs leaves it
   const uint16_t* h;                      // [token][k], taking-part rows
   const Header* hdr;
+  int32_t rows;                           // tokens, or 0: the header's count
   int32_t m_tok;
   int32_t n_vocab, k;                     // of this range
   uint16_t* dw;                           // [n_vocab][k]
@@ -65,6 +69,7 @@ struct HiddenGradArgs {
   const uint16_t* dz;
   const uint16_t* w;                      // [n_vocab][k] of this range
   const Header* hdr;
+  int32_t rows;                           // as above
   int32_t m_tok;
   int32_t n_vocab, k;
   int32_t splits, split_steps;            // steps of 64 ids per share
@@ -106,19 +111,26 @@ struct RowArgs {
   float* coef;
   int32_t* index32;
   float* sub;
-  uint16_t* hc;                           // [token][k] copy of the taking-part rows
+  uint16_t* hc;                           // [token][k] copy of the taking-part rows; with `half`, 2 half rows: zeros after
+                                          //   the last token, and all of it twice
+  int32_t half;
   uint16_t* dh;                           // nullable: rows that are taken out are zeroed
 };
 
-// Up to this many tokens both gradients run in one launch of narrow tiles.
+// Up to this many tokens both gradients run in one launch of narrow tiles, bound
+// by reading w and writing dw.  The products cost nothing then, so the logit
+// gradients are carried in two 16-bit parts (16 or more bits of precision):
+// the second half of 2 few_half(m_tok) rows holds what rounding left.
 constexpr int kFewTokens = 64;
+inline int few_half(int64_t m_tok) { return m_tok > kFewTokens ? 0 : m_tok <= 32 ? 32 : 64; }
 
 int64_t logits_tiles(int32_t m_tok, int32_t n_vocab, int32_t k);     // np of a forward call
 hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStream_t s);
 // shares per dh tile, for ranges of n_vocab ids
 int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k);
 // both gradients of a range (either may be absent: dw or part NULL); `range`: ids of a whole range
-hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t range, bool fp16, hipStream_t s);
+hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t m_tok, int32_t range, bool fp16,
+                        hipStream_t s);
 // dh[rows[t]] = down * sum_s part[s][t]
 hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,
                                int32_t k, uint16_t* dh, bool fp16, hipStream_t s);

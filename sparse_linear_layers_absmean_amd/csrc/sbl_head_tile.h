@@ -48,6 +48,11 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, v2b{(__bf16)a, (__bf16)b});
   }
+  // what rounding a and b to `v` = pack2(a, b) left, rounded itself
+  static __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t v) {
+    const v2b x = __builtin_bit_cast(v2b, v);
+    return pack2(a - (float)x[0], b - (float)x[1]);
+  }
 };
 struct Fp16 {
   static constexpr float kUp = 16384.0f;
@@ -56,6 +61,10 @@ struct Fp16 {
   }
   static __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, v2h{(_Float16)a, (_Float16)b});
+  }
+  static __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t v) {
+    const v2h x = __builtin_bit_cast(v2h, v);
+    return pack2(a - (float)x[0], b - (float)x[1]);
   }
 };
 
@@ -220,29 +229,34 @@ struct Tile {
       for (int j = 0; j < kNT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  // One step at most: klen <= 64.
-  __device__ __forceinline__ void run_once(uint8_t* st, int wave, int lane, int klen) {
+  // One stage, nothing in flight beside the products: a step or two of a tile
+  // that is bound by what it writes, several workgroups per CU.
+  __device__ __forceinline__ void run_short(uint8_t* st, int wave, int lane, int klen) {
     Reader<OA, TM, kPerm> ra;
     Reader<OB, TN, false> rb;
     ra.init(wave / WN * (TM / WM), lane);
     rb.init(wave % WN * (TN / WN), lane);
     clear();
-    sa.fetch(st, wave, 0, klen);
-    sb.fetch(st + kBytesA, wave, 0, klen);
-    wait_vm<0>();
-    wave_barrier();
+    const int steps = (klen + kBK - 1) / kBK;
+    for (int ks = 0; ks < steps; ++ks) {
+      if (ks > 0) wave_barrier();          // every wave has read the last step
+      sa.fetch(st, wave, ks, klen);
+      sb.fetch(st + kBytesA, wave, ks, klen);
+      wait_vm<0>();
+      wave_barrier();
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      if (32 * kk >= klen) break;
-      v8s b[kNT];
+      for (int kk = 0; kk < 2; ++kk) {
+        v8s b[kNT];
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) b[j] = rb.get(st + kBytesA, j, kk);
+        for (int j = 0; j < kNT; ++j) b[j] = rb.get(st + kBytesA, j, kk);
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        const v8s a = ra.get(st, i, kk);
+        for (int i = 0; i < kMT; ++i) {
+          const v8s a = ra.get(st, i, kk);
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a, b[j], acc[i][j]);
+          for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a, b[j], acc[i][j]);
+        }
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
   }
 
@@ -288,13 +302,34 @@ struct Tile {
     // whole turns of the stages, then the rest (no path leads from a skipped
     // step to another: the compiler would wait for every load there)
     int k0 = 0;
+    // few sums per lane: kept in two levels, so that a long k rounds no more than a short one
+    constexpr bool kTwoLevels = kMT * kNT <= 8;
+    v4f done[kTwoLevels ? kMT : 1][kTwoLevels ? kNT : 1];
+    auto carry = [&](bool first) {
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+          if constexpr (kTwoLevels) done[i][j] = first ? v4f{0.f, 0.f, 0.f, 0.f} : done[i][j] + acc[i][j];
+          if (!first) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+    };
+    if constexpr (kTwoLevels) carry(true);
     for (; k0 + STAGES <= steps; k0 += STAGES) {
+      if constexpr (kTwoLevels)
+        if (k0 % (4 * STAGES) == 0 && k0 > 0) carry(false);
 #pragma unroll
       for (int u = 0; u < STAGES; ++u) step(k0 + u, u);
     }
     if (k0 < steps) step(k0, 0);
     if constexpr (STAGES > 2) {
       if (k0 + 1 < steps) step(k0 + 1, 1);
+    }
+    if constexpr (kTwoLevels) {
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) acc[i][j] += done[i][j];
     }
     wait_vm<0>();                          // every direct load has landed before the workgroup can leave
   }
