@@ -416,7 +416,7 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
     tl.start(st, wave, (int)vs);
     tl.run_wide(st, wave, lane, (int)vs);
   } else {
-    tl.template run<3>(st, wave, lane, (int)vs);
+    tl.template run<TN == 128 && TM == 128 ? 2 : 3>(st, wave, lane, (int)vs);
   }
   lane = lane_again();
   const int wm = wave / WN, wn = wave % WN, r = lane & 15, g = lane >> 4;
@@ -496,20 +496,31 @@ __global__ __launch_bounds__(TM == 256 ? 512 : 256, 2) void hidden_grad_kernel(c
 
 // Few tokens: dw is bound by its writes, dh by its reads of w, so both go in one
 // launch, on alternating workgroups while both last (n_dw and n_dh of them).
-template <class E>
+// One tile of 2 kHalf token rows holds both parts of every logit gradient, so w
+// is read once; two workgroups per CU.
+template <class E, int kHalf>
 __global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, const HiddenGradArgs h, int n_dw, int n_dh) {
-  constexpr int kStage = (128 + kFewTokens) * kBK * 2;   // of dh; dw's only one is smaller than two of them
-  __shared__ __align__(16) uint8_t lds0[kStage < 256 * kBK * 2 ? 256 * kBK * 2 : kStage];
-  __shared__ __align__(16) uint8_t lds1[kStage];
-  __shared__ __align__(16) uint8_t lds2[kStage];
+  constexpr int kStage = 256 * kBK * 2;    // one of dw, and of dh at 64 tokens
+  constexpr int kThird = kHalf == 32 ? (128 + 64) * kBK * 2 : 16;
+  __shared__ __align__(16) uint8_t lds0[kStage];
+  __shared__ __align__(16) uint8_t lds1[kHalf == 32 ? kThird : kStage];
+  __shared__ __align__(16) uint8_t lds2[kThird];
   const int b = blockIdx.x, both = 2 * (n_dw < n_dh ? n_dw : n_dh);
   const bool is_dw = b < both ? (b & 1) != 0 : n_dw > n_dh;
   const int tile = b < both ? b >> 1 : b - (both >> 1);
-  uint8_t* const st[3] = {lds0, lds1, lds2};
-  if (is_dw)
-    weight_grad_tile<E, 128, 128, 2, 2, true>(w, tile, st);
-  else
-    hidden_grad_tile<E, 128, kFewTokens, 2, 2>(h, tile, st);
+  if constexpr (kHalf == 32) {
+    uint8_t* const st[3] = {lds0, lds1, lds2};
+    if (is_dw)
+      weight_grad_tile<E, 128, 128, 2, 2, true>(w, tile, st);
+    else
+      hidden_grad_tile<E, 128, 64, 2, 2>(h, tile, st);
+  } else {
+    uint8_t* const st[2] = {lds0, lds1};
+    if (is_dw)
+      weight_grad_tile<E, 128, 128, 2, 2, false>(w, tile, st);
+    else
+      hidden_grad_tile<E, 128, 128, 2, 2>(h, tile, st);
+  }
 }
 
 // One workgroup per token and 256 features: 64 threads of 4 features x 4 groups
@@ -601,7 +612,7 @@ GradPlan grad_plan(int64_t m_tok, int64_t n_vocab, int64_t k) {
     const int64_t tiles = ceil_div(k, 128);
     int64_t s = ceil_div(512, tiles);
     if (s > steps_h / 4) s = steps_h / 4;
-    return GradPlan{true, false, 128, kFewTokens, s < 1 ? 1 : (int)s};
+    return GradPlan{true, false, 128, 2 * few_half(m_tok), s < 1 ? 1 : (int)s};
   }
   auto sums = [&](int64_t s) { return (float)(s * m_tok * k) * 8 / 4.5e6f; };
   const int64_t tiles_w = ceil_div(k, 256) * ceil_div(n_vocab, 256);
@@ -666,7 +677,10 @@ hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, const GradPla
   const unsigned n_w = w.dw ? (unsigned)(ceil_div(w.k, tw) * ceil_div(w.n_vocab, tw)) : 0;
   const unsigned n_h = h.part ? (unsigned)(ceil_div(h.k, p.hd) * ceil_div(h.m_tok, p.ht) * p.splits) : 0;
   if (p.few) {
-    grads_kernel<E><<<dim3(n_w + n_h), 256, 0, s>>>(w, h, n_w, n_h);
+    if (p.ht == 64)
+      grads_kernel<E, 32><<<dim3(n_w + n_h), 256, 0, s>>>(w, h, n_w, n_h);
+    else
+      grads_kernel<E, 64><<<dim3(n_w + n_h), 256, 0, s>>>(w, h, n_w, n_h);
     return hipGetLastError();
   }
   if (p.ht == 256 && (p.wide_w || n_w == 0)) {
