@@ -216,7 +216,8 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
         uint16_t* o = dz_at(a.dz, a.dz_rows, t, vw) + 8 * g;
 #pragma unroll
         for (int i = 0; i < kMT; i += 2) {
-          const v4f x = tl.acc[i][j], y = tl.acc[i + 1][j];
+          v4f x = tl.acc[i][j], y = tl.acc[i + 1][j];
+          if (t >= count) x = y = v4f{0.f, 0.f, 0.f, 0.f};     // no token: also where the weights are not finite
           const u32x4 v = u32x4{E::pack2(x[0], x[1]), E::pack2(x[2], x[3]), E::pack2(y[0], y[1]), E::pack2(y[2], y[3])};
           *reinterpret_cast<u32x4*>(o + 16 * i) = v;
           if (half > 0)                    // what the rounding left, to rows of its own

@@ -1,5 +1,5 @@
 // Internal declarations of the output head's losses (k_head.hip,
-// k_head_rows.hip, sbl_head_api.hip).
+// k_head_rows.hip, sbl_api.hip).
 #pragma once
 
 #include "sbl_internal.h"

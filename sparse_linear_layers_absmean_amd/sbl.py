@@ -641,57 +641,74 @@ def new_head_workspace(m_tok: int, n_vocab: int, k: int, top: int = 1, backward:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _new_scratch(lib, head, top: int, backward: int, device, stream):
-    """A workspace of the caching allocator, for one call on `stream`."""
-    nbytes = lib.sbl_head_workspace_bytes(*head[4:], top, backward)
-    scratch = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=device)
+def _torch_stream(stream):
+    """A caller's stream as torch knows it: what a call allocates under it comes from, and
+    goes back to, that stream's memory."""
     if isinstance(stream, torch.cuda.Stream):
-        scratch.record_stream(stream)                # freed on return, still in use there
-    return scratch, nbytes
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) != 0 else torch.cuda.default_stream()
+
+
+def _new_scratch(lib, head, top: int, backward: int, device):
+    """A workspace for one call on the current stream."""
+    nbytes = lib.sbl_head_workspace_bytes(*head[4:], top, backward)
+    return torch.empty(max(nbytes, 0), dtype=torch.uint8, device=device), nbytes
 
 
 def head_ce(h, w, target, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_ce_forward; returns (loss, lse)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return head_ce(h, w, target, workspace)
     lib, head = load(), _head_args(h, w)
     m_tok, device = head[4], h.device
     scratch, nbytes = (workspace, _nbytes(workspace)) if workspace is not None else \
-        _new_scratch(lib, head, 1, 0, device, stream)
+        _new_scratch(lib, head, 1, 0, device)
     loss = torch.empty(m_tok, dtype=torch.float32, device=device)
     lse = torch.empty(m_tok, dtype=torch.float32, device=device)
     _check("sbl_head_ce_forward", lib.sbl_head_ce_forward(
         *head[:4], _ptr(target, torch.int64, 8 * m_tok, "target"), *head[4:], loss.data_ptr(), lse.data_ptr(),
-        _ptr(scratch, None, 0, "workspace"), nbytes, _stream(stream)))
+        _ptr(scratch, None, 0, "workspace"), nbytes, _stream(None)))
     return loss, lse
 
 
 def head_ce_backward(h, w, target, lse, dloss, dlse=None, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_ce_backward; returns (dh, dw)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return head_ce_backward(h, w, target, lse, dloss, dlse, workspace)
     if workspace is None:
-        workspace, _ = _new_scratch(load(), _head_args(h, w), 1, 1, h.device, stream)
+        workspace, _ = _new_scratch(load(), _head_args(h, w), 1, 1, h.device)
     dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
-    sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw, workspace, dlse=dlse, stream=stream)
+    sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw, workspace, dlse=dlse)
     return dh, dw
 
 
 def head_kd(h, w, index, teacher, tau: float, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_kd_forward; returns (loss, lse)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return head_kd(h, w, index, teacher, tau, workspace)
     lib, head = load(), _head_args(h, w)
     m_tok, device = head[4], h.device
     entries = _teacher_args(index, teacher, m_tok)
     scratch, nbytes = (workspace, _nbytes(workspace)) if workspace is not None else \
-        _new_scratch(lib, head, entries[2], 0, device, stream)
+        _new_scratch(lib, head, entries[2], 0, device)
     loss = torch.empty(m_tok, dtype=torch.float32, device=device)
     lse = torch.empty(m_tok, dtype=torch.float32, device=device)
     _check("sbl_head_kd_forward", lib.sbl_head_kd_forward(
         *head[:4], *entries, tau, *head[4:], loss.data_ptr(), lse.data_ptr(), _ptr(scratch, None, 0, "workspace"),
-        nbytes, _stream(stream)))
+        nbytes, _stream(None)))
     return loss, lse
 
 
 def head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, workspace=None, stream=None):
     """Allocate outputs (and a workspace) and run sbl_head_kd_backward; returns (dh, dw)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return head_kd_backward(h, w, index, teacher, tau, lse, dloss, workspace)
     if workspace is None:
-        workspace, _ = _new_scratch(load(), _head_args(h, w), index.shape[1], 1, h.device, stream)
+        workspace, _ = _new_scratch(load(), _head_args(h, w), index.shape[1], 1, h.device)
     dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
-    sbl_head_kd_backward(h, w, index, teacher, tau, lse, dloss, dh, dw, workspace, stream=stream)
+    sbl_head_kd_backward(h, w, index, teacher, tau, lse, dloss, dh, dw, workspace)
     return dh, dw

@@ -419,3 +419,115 @@ def test_refusals_of_the_binding():
     with pytest.raises(sbl.SblError):                 # a workspace one byte short
         n = sbl.sbl_head_workspace_bytes(4, 10, 64)
         sbl.head_ce(h, w, target, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+
+
+def _grid(rng, shape, step, top):
+    """Multiples of `step` up to `top`: exact in 16 bits, and so is a step from them."""
+    return np.clip(np.round(rng.standard_normal(shape) / step * 0.5), -top / step, top / step) * step
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("t", [7, 40, 150])
+@pytest.mark.parametrize("kind,tau", [("ce", 1.0), ("kd", 1.0), ("kd", 2.0)])
+def test_gradients_are_the_forwards_differences(kind, tau, t, dtype):
+    """dh and dw along a direction against the central difference of the forward's
+    own losses, whose inputs (the point and both steps from it) are exact in 16
+    bits.  Allowed: the forward's bound twice, the gradients' bounds along the
+    direction, and what a central difference leaves out, which is the same
+    difference and derivative taken in 64 bits."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    say(f"head differences {kind} tau={tau} t={t} {dtype}")
+    v, d, top = 300, 64, 6
+    rng = np.random.default_rng([72, t, int(2 * tau)])
+    step_h, step_w = 2.0 ** -5, 2.0 ** -7
+    hv, wv = _grid(rng, (t, d), step_h, 3.0), _grid(rng, (v, d), step_w, 0.75) * 0.5
+    gone = rng.random(t) < 0.2
+    gone[0] = False
+    dloss = (rng.integers(1, 9, t) / 8.0).astype(np.float32)
+    if kind == "ce":
+        target = np.where(gone, -1, rng.integers(0, v, t))
+        want, row = H.wanted_ce(target, v)
+        entropy, slack = np.zeros(t), np.zeros(t)
+        forward = lambda h, w: sbl.head_ce(h, w, _i64(target))
+        backward = lambda h, w, lse: sbl.head_ce_backward(h, w, _i64(target), lse, _f32(dloss))
+    else:
+        index, teacher = _teacher(rng, t, v, top, gone)
+        p, logp = H.teacher_probabilities(index, teacher, tau)
+        want, row = H.wanted_kd(index, p, v)
+        entropy = H.entropy_of(p, logp)
+        slack = 64 * H.U32 * (1 + np.abs(np.where(p > 0, logp, 0.0)).max(axis=1))
+        forward = lambda h, w: sbl.head_kd(h, w, _i64(index), _f32(teacher), tau)
+        backward = lambda h, w, lse: sbl.head_kd_backward(h, w, _i64(index), _f32(teacher), tau, lse, _f32(dloss))
+    put = lambda x: _half(x, dtype)[0]
+    h, w = put(hv), put(wv)
+    assert np.array_equal(_half(hv, dtype)[1], hv) and np.array_equal(_half(wv, dtype)[1], wv)
+    lse = forward(h, w)[1]
+    dh, dw = (_np(x).astype(np.float64) for x in backward(h, w, lse))
+    rh, rw, eh, ew = H.backward(hv, wv, want, row, _np(lse), dloss, tau=tau, dtype=dtype)
+    rounded = (tau * np.abs(dloss) * row * slack)[:, None] * want
+    eh = eh + 2 * rounded @ np.abs(wv)
+    ew = ew + 2 * rounded.T @ np.where(row[:, None], np.abs(hv), 0.0)
+
+    def total(hx, wx):
+        loss64, _, bound = H.forward(hx, wx, want, row, entropy, tau)
+        loss = _np(forward(put(hx), put(wx))[0]).astype(np.float64)
+        return (dloss * loss).sum(), (dloss * loss64 * row).sum(), (dloss * row * (tau * tau) * (bound + slack)).sum()
+
+    for grad, exact, err, step, at in ((dh, rh, eh, step_h, "h"), (dw, rw, ew, step_w / 2, "w")):
+        e = np.sign(exact) * step                    # the steepest direction: every difference has one sign
+        up = total(hv + e, wv) if at == "h" else total(hv, wv + e)
+        down = total(hv - e, wv) if at == "h" else total(hv, wv - e)
+        left_out = abs((up[1] - down[1]) / 2 - (exact * e).sum())
+        allowed = left_out + (up[2] + down[2]) / 2 + (err * np.abs(e)).sum()
+        got, slope = (up[0] - down[0]) / 2, (grad * e).sum()
+        assert abs(got - slope) <= allowed, (at, got, slope, allowed)
+        assert allowed < 0.1 * abs(slope), (at, slope, allowed)        # the comparison says something
+
+
+@pytest.mark.parametrize("t,v,d", [(20, 700, 64), (64, 33000, 128), (300, 9000, 64), (520, 33000, 72)])
+def test_many_listed_ids_in_one_tile(t, v, d):
+    """Every token lists 40 ids of the same 128: more than a tile keeps apart."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    say(f"head_kd crowded t={t} v={v} d={d}")
+    top, tau, dtype = 40, 2.0, "bfloat16"
+    rng, h, hv, w, wv, gone = _inputs(t, v, d, dtype, [73, t])
+    index = np.stack([512 + rng.permutation(128)[:top] for _ in range(t)])
+    teacher = rng.standard_normal((t, top)).astype(np.float32)
+    index[gone] = -1
+    p, logp = H.teacher_probabilities(index, teacher, tau)
+    want, row = H.wanted_kd(index, p, v)
+    loss, lse = sbl.head_kd(h, w, _i64(index), _f32(teacher), tau)
+    rl, rs, bound = H.forward(hv, wv, want, row, H.entropy_of(p, logp), tau)
+    spread = np.abs(np.where(p > 0, logp, 0.0)).max(axis=1)
+    _near(_np(loss), rl, tau * tau * (bound + 64 * H.U32 * (1 + spread)) * row, "loss")
+    dloss = (rng.random(t) + 0.5) / t
+    dh, dw = sbl.head_kd_backward(h, w, _i64(index), _f32(teacher), tau, lse, _f32(dloss))
+    rh, rw, eh, ew = H.backward(hv, wv, want, row, _np(lse), dloss.astype(np.float32), tau=tau, dtype=dtype)
+    s = (tau * np.abs(dloss) * row * 64 * H.U32 * (1 + spread))[:, None] * want
+    _near(_np(dh), rh, eh + 2 * s @ np.abs(wv), "dh")
+    _near(_np(dw), rw, ew + 2 * s.T @ np.where(row[:, None], np.abs(hv), 0.0), "dw")
+
+
+@pytest.mark.parametrize("t", [1, 20, 40, 70, 300])
+def test_an_id_of_no_probability(t):
+    """A weight of -infinity on a feature that is positive in every token: its id
+    has probability 0, and its row of dw is exactly zero, at every token count."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    v, d = 300, 64
+    g = torch.Generator(device="cuda").manual_seed(11)
+    h, w = torch.randn(t, d, generator=g, device="cuda"), torch.randn(v, d, generator=g, device="cuda") * 0.2
+    h[:, 5] = h[:, 5].abs() + 0.5
+    w[17, 5] = -float("inf")
+    h, w = h.bfloat16(), w.bfloat16()
+    target = torch.full((t,), 20, device="cuda")
+    loss, lse = sbl.head_ce(h, w, target)
+    z = h.double() @ w.double().t()
+    assert float((lse.double() - torch.logsumexp(z, 1)).abs().max()) < 1e-4
+    assert float((loss.double() - (torch.logsumexp(z, 1) - z[:, 20])).abs().max()) < 1e-4
+    dw = torch.empty_like(w)
+    sbl.sbl_head_ce_backward(h, w, target, lse, torch.ones(t, device="cuda"), None, dw,
+                             _dirty(sbl.sbl_head_workspace_bytes(t, v, d, backward=True)))
+    assert dw.isfinite().all() and not dw[17].any()
