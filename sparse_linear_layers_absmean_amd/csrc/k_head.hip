@@ -451,6 +451,13 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
   }
 }
 
+// This XCD's run of n tiles (workgroups go to the 8 XCDs in turn).
+__device__ __forceinline__ int xcd_share(int n, int& first) {
+  const int x = blockIdx.x & 7, per = (n + 7) / 8;
+  first = x * per < n ? x * per : n;
+  return n - first < per ? n - first : per;
+}
+
 // More than 128 tokens: both gradients of a range in one launch (either may be
 // absent), so that one's last, part empty round is filled by the other.  Each
 // XCD takes a contiguous run of each kind's tiles, the hidden gradient's, the
@@ -462,14 +469,9 @@ __global__ __launch_bounds__(512, 2) void grads_wide_kernel(const WeightGradArgs
   __shared__ __align__(16) uint8_t lds0[512 * kBK * 2];
   __shared__ __align__(16) uint8_t lds1[512 * kBK * 2];
   uint8_t* const st[2] = {lds0, lds1};
-  const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
-  auto share = [&](int n, int& first) {    // this XCD's run of n tiles
-    const int per = (n + 7) / 8;
-    first = x * per < n ? x * per : n;
-    return n - first < per ? n - first : per;
-  };
+  const int i = blockIdx.x >> 3;
   int w0, h0;
-  const int nw = share(n_w, w0), nh = share(n_h, h0);
+  const int nw = xcd_share(n_w, w0), nh = xcd_share(n_h, h0);
   if (i < nh)
     hidden_grad_tile<E, 256, 256, 2, 4>(h, h0 + i, st);
   else if (i < nh + nw)
@@ -506,9 +508,13 @@ __global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, c
   __shared__ __align__(16) uint8_t lds0[kStage];
   __shared__ __align__(16) uint8_t lds1[kHalf == 32 ? kThird : kStage];
   __shared__ __align__(16) uint8_t lds2[kThird];
-  const int b = blockIdx.x, both = 2 * (n_dw < n_dh ? n_dw : n_dh);
-  const bool is_dw = b < both ? (b & 1) != 0 : n_dw > n_dh;
-  const int tile = b < both ? b >> 1 : b - (both >> 1);
+  const int i = blockIdx.x >> 3;
+  int w0, h0;
+  const int nw = xcd_share(n_dw, w0), nh = xcd_share(n_dh, h0);
+  const int both = 2 * (nw < nh ? nw : nh);
+  if (i >= nw + nh) return;
+  const bool is_dw = i < both ? (i & 1) != 0 : nw > nh;
+  const int tile = (is_dw ? w0 : h0) + (i < both ? i >> 1 : i - (both >> 1));
   if constexpr (kHalf == 32) {
     uint8_t* const st[3] = {lds0, lds1, lds2};
     if (is_dw)
@@ -678,10 +684,11 @@ hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, const GradPla
   const unsigned n_w = w.dw ? (unsigned)(ceil_div(w.k, tw) * ceil_div(w.n_vocab, tw)) : 0;
   const unsigned n_h = h.part ? (unsigned)(ceil_div(h.k, p.hd) * ceil_div(h.m_tok, p.ht) * p.splits) : 0;
   if (p.few) {
+    const dim3 grid(8 * ((n_w + 7) / 8 + (n_h + 7) / 8));
     if (p.ht == 64)
-      grads_kernel<E, 32><<<dim3(n_w + n_h), 256, 0, s>>>(w, h, n_w, n_h);
+      grads_kernel<E, 32><<<grid, 256, 0, s>>>(w, h, n_w, n_h);
     else
-      grads_kernel<E, 64><<<dim3(n_w + n_h), 256, 0, s>>>(w, h, n_w, n_h);
+      grads_kernel<E, 64><<<grid, 256, 0, s>>>(w, h, n_w, n_h);
     return hipGetLastError();
   }
   if (p.ht == 256 && (p.wide_w || n_w == 0)) {
