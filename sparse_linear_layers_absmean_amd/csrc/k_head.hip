@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
 // Rows of the tile are features (contiguous in memory, read down the k axis),
 // so a lane's 4 consecutive results are 4 consecutive features of an output row.
 
-template <class E, int TM, int TN, int WM, int WN, bool kShort, class St>
+template <class E, int TM, int TN, int WM, int WN, class St>
 __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int tile, const St& st) {
   using T = Tile<E, kCols, kCols, TM, TN, WM, WN, false>;
   const int count = a.rows > 0 ? a.rows : a.hdr->count;
@@ -359,8 +359,6 @@ __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int ti
   if constexpr (TN == 256) {
     tl.start(st, wave, count);
     tl.run_wide(st, wave, lane, count);
-  } else if constexpr (kShort) {
-    tl.run_short(st[0], wave, lane, count);
   } else {
     tl.template run<2>(st, wave, lane, count);
   }
@@ -475,7 +473,7 @@ __global__ __launch_bounds__(512, 2) void grads_wide_kernel(const WeightGradArgs
   if (i < nh)
     hidden_grad_tile<E, 256, 256, 2, 4>(h, h0 + i, st);
   else if (i < nh + nw)
-    weight_grad_tile<E, 256, 256, 2, 4, false>(w, w0 + i - nh, st);
+    weight_grad_tile<E, 256, 256, 2, 4>(w, w0 + i - nh, st);
 }
 
 // One of the gradients on smaller tiles.
@@ -484,7 +482,7 @@ __global__ __launch_bounds__(256, 2) void weight_grad_kernel(const WeightGradArg
   __shared__ __align__(16) uint8_t lds0[256 * kBK * 2];
   __shared__ __align__(16) uint8_t lds1[256 * kBK * 2];
   uint8_t* const st[2] = {lds0, lds1};
-  weight_grad_tile<E, 128, 128, 2, 2, false>(a, xcd_tile(blockIdx.x, gridDim.x), st);
+  weight_grad_tile<E, 128, 128, 2, 2>(a, xcd_tile(blockIdx.x, gridDim.x), st);
 }
 
 template <class E, int TM, int TN>
@@ -497,36 +495,89 @@ __global__ __launch_bounds__(TM == 256 ? 512 : 256, 2) void hidden_grad_kernel(c
   hidden_grad_tile<E, TM, TN, TM / 64, 2>(a, xcd_tile(blockIdx.x, gridDim.x), st);
 }
 
-// Few tokens: dw is bound by its writes, dh by its reads of w, so both go in one
-// launch, on alternating workgroups while both last (n_dw and n_dh of them).
-// One tile of 2 kHalf token rows holds both parts of every logit gradient, so w
-// is read once; two workgroups per CU.
-template <class E, int kHalf>
-__global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, const HiddenGradArgs h, int n_dw, int n_dh) {
-  constexpr int kStage = 256 * kBK * 2;    // one of dw, and of dh at 64 tokens
-  constexpr int kThird = kHalf == 32 ? (128 + 64) * kBK * 2 : 16;
+// Few tokens: dw of 128 features and `run` tiles of 128 ids.  All of its k, the
+// 2 kHalf token rows, lies in LDS: the hidden states for the whole run, the logit
+// gradients of one tile.  The next tile's are asked for before this one's dw is
+// stored, so that stores are under way all the time.
+template <class E, int kHalf, int kPolicy>
+__device__ __forceinline__ void weight_grad_run(const WeightGradArgs& a, int tile, int run, uint8_t* la, uint8_t* lb) {
+  using T = Tile<E, kCols, kCols, 128, 128, 2, 2, false>;
+  constexpr int kSteps = 2 * kHalf / kBK;
+  const int ndt = (a.k + 127) / 128, nvt = (a.n_vocab + 127) / 128;
+  const int dt = tile % ndt, v0 = tile / ndt * run, v1 = v0 + run < nvt ? v0 + run : nvt;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave / 2, wn = wave % 2, r = lane & 15, g = lane >> 4;
+  const float down = a.hdr->down;
+  T tl;
+  tl.sa.init_cols(make_rsrc(a.h, (int64_t)a.rows * a.k * 2), wave, lane, 2 * a.k, 256 * dt);
+  auto fetch_dz = [&](int vt) {
+    tl.sb.init_cols(make_rsrc(a.dz + (int64_t)(vt / 2) * a.m_tok * 256, (int64_t)a.rows * 512), wave, lane, 512,
+                    256 * (vt & 1));
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) tl.sb.fetch(lb + s * 128 * kBK * 2, wave, s, a.rows);
+  };
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) tl.sa.fetch(la + s * T::kBytesA, wave, s, a.rows);
+  fetch_dz(v0);
+  wait_vm<0>();
+  wave_barrier();
+  const int d0 = dt * 128 + wm * 64 + ((g & 1) ? 16 + 4 * (g - 1) : 4 * g);   // as in weight_grad_tile
+  for (int vt = v0; vt < v1; ++vt) {
+    tl.template products<kSteps>(la, lb, wave, lane);
+    wave_barrier();                        // every wave has read this tile's gradients
+    if (vt + 1 < v1) fetch_dz(vt + 1);
+    const int64_t left = a.n_vocab - (int64_t)vt * 128;
+    const __amdgpu_buffer_rsrc_t out = make_rsrc(a.dw + (int64_t)vt * 128 * a.k, (left < 128 ? left : 128) * a.k * 2);
+    // exactly 8 stores, those past an end dropped: the wait below counts them
+#pragma unroll
+    for (int j = 0; j < T::kNT; ++j)
+#pragma unroll
+      for (int i = 0; i < T::kMT; i += 2) {
+        const v4f x = tl.acc[i][j] * down, y = tl.acc[i + 1][j] * down;
+        const auto lo = __builtin_amdgcn_permlane16_swap(E::pack2(x[0], x[1]), E::pack2(y[0], y[1]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(E::pack2(x[2], x[3]), E::pack2(y[2], y[3]), false, false);
+        const int d = d0 + 16 * i;
+        const uint32_t at = (uint32_t)(wn * 64 + 16 * j + r) * (2u * a.k) + 2u * d;
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, out, d < a.k ? at : kFar, 0, kPolicy);
+      }
+    if (vt + 1 < v1) {
+      wait_vm<8>();                        // the next tile's gradients, asked for before the 8 stores
+      wave_barrier();
+    }
+  }
+}
+
+// Both gradients of few tokens, bound by memory: dh by its reads of w, dw by its
+// writes.  One dh tile of 2 kHalf token rows holds both parts of every logit
+// gradient, so w is read once; two workgroups per CU.  Each XCD takes a contiguous
+// run of dh's tiles, then one of dw's: reads and writes at the same time cost more
+// than one after the other (30 x 128256 x 4096: 193 us and 283, 565 on
+// alternating workgroups; 37 x 32003 x 1536 in all 90 -> 76).
+template <class E, int kHalf, int kPolicy>
+__global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, const HiddenGradArgs h, int n_dw, int n_dh,
+                                                       int run) {
+  constexpr int kStage = (128 + 2 * kHalf) * kBK * 2;      // of dh, and at least either operand of dw
   __shared__ __align__(16) uint8_t lds0[kStage];
-  __shared__ __align__(16) uint8_t lds1[kHalf == 32 ? kThird : kStage];
-  __shared__ __align__(16) uint8_t lds2[kThird];
+  __shared__ __align__(16) uint8_t lds1[kStage];
   const int i = blockIdx.x >> 3;
   int w0, h0;
   const int nw = xcd_share(n_dw, w0), nh = xcd_share(n_dh, h0);
-  const int both = 2 * (nw < nh ? nw : nh);
-  if (i >= nw + nh) return;
-  const bool is_dw = i < both ? (i & 1) != 0 : nw > nh;
-  const int tile = (is_dw ? w0 : h0) + (i < both ? i >> 1 : i - (both >> 1));
+  if (i >= nh + nw) return;
+  const bool is_dw = i >= nh;
+  const int tile = is_dw ? w0 + i - nh : h0 + i;
   if constexpr (kHalf == 32) {
+    __shared__ __align__(16) uint8_t lds2[kStage];
     uint8_t* const st[3] = {lds0, lds1, lds2};
     if (is_dw)
-      weight_grad_tile<E, 128, 128, 2, 2, true>(w, tile, st);
+      weight_grad_run<E, kHalf, kPolicy>(w, tile, run, lds0, lds1);
     else
-      hidden_grad_tile<E, 128, 64, 2, 2>(h, tile, st);
+      hidden_grad_tile<E, 128, 2 * kHalf, 2, 2>(h, tile, st);
   } else {
     uint8_t* const st[2] = {lds0, lds1};
     if (is_dw)
-      weight_grad_tile<E, 128, 128, 2, 2, false>(w, tile, st);
+      weight_grad_run<E, kHalf, kPolicy>(w, tile, run, lds0, lds1);
     else
-      hidden_grad_tile<E, 128, 128, 2, 2>(h, tile, st);
+      hidden_grad_tile<E, 128, 2 * kHalf, 2, 2>(h, tile, st);
   }
 }
 
@@ -654,18 +705,21 @@ GradPlan grad_plan(int64_t m_tok, int64_t n_vocab, int64_t k) {
   return p;
 }
 
+// Whether an array of the weights' size is more than stays in the caches (256 MB
+// in all): then what is used once goes past them.  One token's forward over 205 MB
+// 42 -> 37 us; 88 MB read again and again from the cache 21 -> 27 us.  dw of 1.05 GB
+// from 30 tokens 524 -> 469 us with its logits, of 98 MB 41 -> 50.
+bool past_cache(int64_t n_vocab, int64_t k) { return n_vocab * k * 2 > (int64_t(128) << 20); }
+
 template <class E, bool kBackward>
 hipError_t logits(const LogitsArgs& a, hipStream_t s) {
   const LogitsTile t = logits_variant(a.m_tok, a.n_vocab, a.k);
   const dim3 grid((unsigned)(ceil_div(a.n_vocab, t.tm) * ceil_div(a.m_tok, t.tn)));
-  // one token tile of a forward reads the weights once: with more of them than
-  // stay cached (256 MB in all), past the cache (205 MB: 42 -> 37 us at one
-  // token; 88 MB read again and again from the cache: 21 -> 27 us)
-  const bool once = !kBackward && a.m_tok <= t.tn && (int64_t)a.n_vocab * a.k * 2 > (int64_t(128) << 20);
+  const bool once = a.m_tok <= t.tn && (kBackward ? past_cache(a.n_vocab / 2, a.k) : past_cache(a.n_vocab, a.k));
   if (t.tn == 32 && once)
-    logits_kernel<E, 128, 32, 4, 1, false, kNt><<<grid, 256, 0, s>>>(a);
+    logits_kernel<E, 128, 32, 4, 1, kBackward, kNt><<<grid, 256, 0, s>>>(a);
   else if (t.tn == 64 && once)
-    logits_kernel<E, 128, 64, 4, 1, false, kNt><<<grid, 256, 0, s>>>(a);
+    logits_kernel<E, 128, 64, 4, 1, kBackward, kNt><<<grid, 256, 0, s>>>(a);
   else if (t.tn == 32)
     logits_kernel<E, 128, 32, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
   else if (t.tn == 64)
@@ -677,6 +731,8 @@ hipError_t logits(const LogitsArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+constexpr int64_t kRunMax = 8;
+
 // n_vocab of w and h is this range's; the plan is that of a whole range
 template <class E>
 hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, const GradPlan& p, hipStream_t s) {
@@ -684,11 +740,20 @@ hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, const GradPla
   const unsigned n_w = w.dw ? (unsigned)(ceil_div(w.k, tw) * ceil_div(w.n_vocab, tw)) : 0;
   const unsigned n_h = h.part ? (unsigned)(ceil_div(h.k, p.hd) * ceil_div(h.m_tok, p.ht) * p.splits) : 0;
   if (p.few) {
-    const dim3 grid(8 * ((n_w + 7) / 8 + (n_h + 7) / 8));
-    if (p.ht == 64)
-      grads_kernel<E, 32><<<grid, 256, 0, s>>>(w, h, n_w, n_h);
+    // tiles of dw that a workgroup takes one after the other: a launch of few tiles takes them side by side
+    int64_t run = n_w / 1024;
+    run = run < 1 ? 1 : run > kRunMax ? kRunMax : run;
+    const int64_t runs = w.dw ? ceil_div(w.k, 128) * ceil_div(ceil_div(w.n_vocab, 128), run) : 0;
+    const dim3 grid((unsigned)(8 * (ceil_div(runs, 8) + ceil_div(n_h, 8))));
+    const bool once = past_cache(w.n_vocab, w.k);
+    if (p.ht == 64 && once)
+      grads_kernel<E, 32, kNt><<<grid, 256, 0, s>>>(w, h, (int)runs, (int)n_h, (int)run);
+    else if (p.ht == 64)
+      grads_kernel<E, 32, 0><<<grid, 256, 0, s>>>(w, h, (int)runs, (int)n_h, (int)run);
+    else if (once)
+      grads_kernel<E, 64, kNt><<<grid, 256, 0, s>>>(w, h, (int)runs, (int)n_h, (int)run);
     else
-      grads_kernel<E, 64><<<grid, 256, 0, s>>>(w, h, n_w, n_h);
+      grads_kernel<E, 64, 0><<<grid, 256, 0, s>>>(w, h, (int)runs, (int)n_h, (int)run);
     return hipGetLastError();
   }
   if (p.ht == 256 && (p.wide_w || n_w == 0)) {

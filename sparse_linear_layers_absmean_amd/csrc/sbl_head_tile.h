@@ -229,35 +229,27 @@ struct Tile {
       for (int j = 0; j < kNT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  // One stage, nothing in flight beside the products: a step or two of a tile
-  // that is bound by what it writes, several workgroups per CU.
-  __device__ __forceinline__ void run_short(uint8_t* st, int wave, int lane, int klen) {
+  // The products of STEPS steps that lie in LDS, step by step: A at `la`, B at `lb`.
+  template <int STEPS>
+  __device__ __forceinline__ void products(const uint8_t* la, const uint8_t* lb, int wave, int lane) {
     Reader<OA, TM, kPerm> ra;
     Reader<OB, TN, false> rb;
     ra.init(wave / WN * (TM / WM), lane);
     rb.init(wave % WN * (TN / WN), lane);
     clear();
-    const int steps = (klen + kBK - 1) / kBK;
-    for (int ks = 0; ks < steps; ++ks) {
-      if (ks > 0) wave_barrier();          // every wave has read the last step
-      sa.fetch(st, wave, ks, klen);
-      sb.fetch(st + kBytesA, wave, ks, klen);
-      wait_vm<0>();
-      wave_barrier();
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        v8s b[kNT];
+    for (int kk = 0; kk < 2 * STEPS; ++kk) {
+      v8s b[kNT];
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) b[j] = rb.get(st + kBytesA, j, kk);
+      for (int j = 0; j < kNT; ++j) b[j] = rb.get(lb + kk / 2 * (TN * kBK * 2), j, kk & 1);
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-          const v8s a = ra.get(st, i, kk);
+      for (int i = 0; i < kMT; ++i) {
+        const v8s a = ra.get(la + kk / 2 * kBytesA, i, kk & 1);
 #pragma unroll
-          for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a, b[j], acc[i][j]);
-        }
+        for (int j = 0; j < kNT; ++j) acc[i][j] = E::mma(a, b[j], acc[i][j]);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
   // Narrow tiles (bound by memory): STAGES - 1 steps in flight, two
@@ -408,7 +400,7 @@ struct Tile {
       rb.pin();
 #pragma unroll
       for (int n = 0; n < 6; ++n) {
-        if (n < 6) load2(1, n, st[u], 1);
+        load2(1, n, st[u], 1);
         mma4(0, n);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
