@@ -500,12 +500,15 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  *              (top = 1 for cross entropy), 256-byte aligned, any contents; calls
  *              in flight at the same time need their own.  Backward: the
  *              gradient of at most 2^28 logits at a time (256 ids at least), a
- *              copy of h and fp32 partial sums of dh.
+ *              copy of h and fp32 partial sums of dh; up to 64 tokens, two rows
+ *              of each per token, in 64 or 128 rows.
  * Products are exact and summed in fp32; softmax statistics and the loss are
  * fp32.  The backward rounds dz once to the 16-bit type before the two
  * products that read it, scaled so that the largest coefficient becomes 1
  * (BF16) or 2^14 (FP16): relative error 2^-8 (2^-11) of each at most, the size
- * of the outputs' own rounding.  Sums have a fixed order: results repeat bit for bit.
+ * of the outputs' own rounding.  Up to 64 tokens it is held in two 16-bit parts,
+ * which leaves the outputs' rounding alone.  Sums have a fixed order: results
+ * repeat bit for bit.
  * Limits: 8 <= k <= 131072, k % 8 == 0; n_vocab * k <= 2^34; m_tok <= 2^22 and
  * (m_tok + 256) * k and the span of h at most 2^30 values; m_tok * n_vocab below
  * about 2^42; 1e-4 <= tau <= 1e4.
