@@ -390,11 +390,29 @@ __device__ __forceinline__ void weight_grad_tile(const WeightGradArgs& a, int ti
   }
 }
 
+// The shares of dh when `count` of the m_tok rows take part: the tiles that the
+// others would have taken share the vocabulary instead.  They fill the grid and
+// the partial sums' rows that all m_tok would (n tiles of tn rows in all).
+struct Shares {
+  int splits, steps, tiles;                // steps of a share; token tiles
+  int64_t rows;                            // rows of a share's partial sums
+};
+__device__ __forceinline__ Shares hidden_shares(int splits, int range_steps, int m_tok, int tn, int count) {
+  const int n = count < 1 ? 1 : count, tiles = (n + tn - 1) / tn;
+  int64_t s = (int64_t)splits * ((m_tok + tn - 1) / tn) / tiles;
+  const int64_t fit = (int64_t)splits * m_tok / n;
+  s = s < fit ? s : fit;
+  s = s < range_steps / 4 ? s : range_steps / 4;
+  s = s > splits ? s : splits;
+  const int steps = (int)((range_steps + s - 1) / s);
+  return Shares{(range_steps + steps - 1) / steps, steps, tiles, n};
+}
+
 template <class E, int TM, int TN, int WM, int WN, class St>
-__device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int tile, const St& st) {
+__device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, const Shares& sh, int tile, const St& st) {
   using T = Tile<E, kCols, kRows, TM, TN, WM, WN, false, false, true>;
   const int count = a.rows > 0 ? a.rows : a.hdr->count;
-  const int ndt = (a.k + TM - 1) / TM, ntt = (a.m_tok + TN - 1) / TN;
+  const int ndt = (a.k + TM - 1) / TM, ntt = sh.tiles;
   // a share's tiles together: they read the same rows of w
   const int s = tile / (ndt * ntt), in = tile % (ndt * ntt);
   // groups of kGroup token tiles x every feature tile
@@ -405,9 +423,9 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
   if (t0 >= count) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int lane = threadIdx.x & 63;
-  const int64_t v0 = (int64_t)s * a.split_steps * kBK;
+  const int64_t v0 = (int64_t)s * sh.steps * kBK;
   int64_t vs = a.n_vocab - v0;
-  if (vs > (int64_t)a.split_steps * kBK) vs = (int64_t)a.split_steps * kBK;
+  if (vs > (int64_t)sh.steps * kBK) vs = (int64_t)sh.steps * kBK;
   if (vs < 0) vs = 0;
   T tl;
   tl.sa.init_cols(make_rsrc(a.w + v0 * a.k, vs * a.k * 2), wave, lane, 2 * a.k, 2 * TM * dt);
@@ -415,7 +433,7 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
   tl.sb.init_rows(make_rsrc(a.dz + (int64_t)t0 * 256, ((int64_t)(a.n_vocab + 255) / 256 * a.m_tok - t0) * 512), wave, lane,
                   512);
   tl.sb.panel = (uint32_t)a.m_tok * 512;
-  tl.sb.first = s * a.split_steps;
+  tl.sb.first = s * sh.steps;
   if constexpr (TN == 256) {
     tl.start(st, wave, (int)vs);
     tl.run_wide(st, wave, lane, (int)vs);
@@ -428,7 +446,7 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
   // load waits for every store before it)
   auto at = [&](int j, int i) -> v4f* {
     const int t = t0 + wn * (TN / WN) + 16 * j + r, d = dt * TM + wm * (TM / WM) + 16 * i + 4 * g;
-    return t < count && d < a.k ? reinterpret_cast<v4f*>(a.part + ((int64_t)s * a.m_tok + t) * a.k + d) : nullptr;
+    return t < count && d < a.k ? reinterpret_cast<v4f*>(a.part + (s * sh.rows + t) * a.k + d) : nullptr;
   };
   constexpr int kHalf = T::kMT / 2;
   v4f old[2][kHalf];
@@ -454,6 +472,10 @@ __device__ __forceinline__ void hidden_grad_tile(const HiddenGradArgs& a, int ti
   }
 }
 
+__device__ __forceinline__ Shares all_rows(const HiddenGradArgs& a, int tn) {
+  return Shares{a.splits, a.split_steps, (a.m_tok + tn - 1) / tn, a.m_tok};
+}
+
 // This XCD's run of n tiles (workgroups go to the 8 XCDs in turn).
 __device__ __forceinline__ int xcd_share(int n, int& first) {
   const int x = blockIdx.x & 7, per = (n + 7) / 8;
@@ -476,7 +498,7 @@ __global__ __launch_bounds__(512, 2) void grads_wide_kernel(const WeightGradArgs
   int w0, h0;
   const int nw = xcd_share(n_w, w0), nh = xcd_share(n_h, h0);
   if (i < nh)
-    hidden_grad_tile<E, 256, 256, 2, 4>(h, h0 + i, st);
+    hidden_grad_tile<E, 256, 256, 2, 4>(h, all_rows(h, 256), h0 + i, st);
   else if (i < nh + nw)
     weight_grad_tile<E, 256, 256, 2, 4>(w, w0 + i - nh, st);
 }
@@ -497,7 +519,9 @@ __global__ __launch_bounds__(TM == 256 ? 512 : 256, 2) void hidden_grad_kernel(c
   __shared__ __align__(16) uint8_t lds1[kStage];
   __shared__ __align__(16) uint8_t lds2[kStage];
   uint8_t* const st[3] = {lds0, lds1, lds2};
-  hidden_grad_tile<E, TM, TN, TM / 64, 2>(a, xcd_tile(blockIdx.x, gridDim.x), st);
+  const Shares sh = hidden_shares(a.splits, a.range_steps, a.m_tok, TN, a.hdr->count);
+  const int n = sh.splits * sh.tiles * ((a.k + TM - 1) / TM);      // at most the grid's
+  if (blockIdx.x < n) hidden_grad_tile<E, TM, TN, TM / 64, 2>(a, sh, xcd_tile(blockIdx.x, n), st);
 }
 
 // Few tokens: dw of 128 features and `run` tiles of 128 ids.  All of its k, the
@@ -576,31 +600,39 @@ __global__ __launch_bounds__(256, 2) void grads_kernel(const WeightGradArgs w, c
     if (is_dw)
       weight_grad_run<E, kHalf, kPolicy>(w, tile, run, lds0, lds1);
     else
-      hidden_grad_tile<E, 128, 2 * kHalf, 2, 2>(h, tile, st);
+      hidden_grad_tile<E, 128, 2 * kHalf, 2, 2>(h, all_rows(h, 2 * kHalf), tile, st);
   } else {
     uint8_t* const st[2] = {lds0, lds1};
     if (is_dw)
       weight_grad_run<E, kHalf, kPolicy>(w, tile, run, lds0, lds1);
     else
-      hidden_grad_tile<E, 128, 2 * kHalf, 2, 2>(h, tile, st);
+      hidden_grad_tile<E, 128, 2 * kHalf, 2, 2>(h, all_rows(h, 2 * kHalf), tile, st);
   }
 }
 
 // One workgroup per token and 256 features: 64 threads of 4 features x 4 groups
 // of shares.
 template <class E>
-__global__ __launch_bounds__(256) void hidden_final_kernel(const float* part, int splits, const Header* hdr,
-                                                           const int32_t* rows, int32_t m_tok, int32_t k,
-                                                           uint16_t* dh) {
+__global__ __launch_bounds__(256) void hidden_final_kernel(const float* part, const HiddenPlan plan, int range_steps,
+                                                           const Header* hdr, const int32_t* rows, int32_t m_tok,
+                                                           int32_t k, uint16_t* dh) {
   __shared__ v4f joined[4][64];
   const int t = blockIdx.x;
-  if (t >= hdr->count) return;
+  const int count = hdr->count;
+  if (t >= count) return;
+  int splits = plan.splits;
+  int64_t each = m_tok;
+  if (plan.token_tile > 0) {
+    const Shares sh = hidden_shares(splits, range_steps, m_tok, plan.token_tile, count);
+    splits = sh.splits;
+    each = sh.rows;
+  }
   const int q = threadIdx.x >> 6, lane = threadIdx.x & 63, d = 4 * (blockIdx.y * 64 + lane);
   const bool in = d < k;
   v4f x = v4f{0.f, 0.f, 0.f, 0.f};
   if (in) {
     const float* p = part + (int64_t)t * k + d;
-    const int64_t next = (int64_t)m_tok * k;
+    const int64_t next = each * k;
 #pragma unroll 4
     for (int s = q; s < splits; s += 4) x += *reinterpret_cast<const v4f*>(p + s * next);
   }
@@ -750,7 +782,9 @@ hipError_t grads(const WeightGradArgs& w, const HiddenGradArgs& h, const GradPla
     run = run < 1 ? 1 : run > kRunMax ? kRunMax : run;
     const int64_t runs = w.dw ? ceil_div(w.k, 128) * ceil_div(ceil_div(w.n_vocab, 128), run) : 0;
     const dim3 grid((unsigned)(8 * (ceil_div(runs, 8) + ceil_div(n_h, 8))));
-    const bool once = past_cache(w.n_vocab, w.k);
+    // stores go past the caches only as whole 128-byte lines: parts of lines from two
+    // workgroups would reach memory one by one (1 x 124987 x 2312: 508 -> 711 us)
+    const bool once = past_cache(w.n_vocab, w.k) && w.k % 64 == 0;
     if (p.ht == 64 && once)
       grads_kernel<E, 32, kNt><<<grid, 256, 0, s>>>(w, h, (int)runs, (int)n_h, (int)run);
     else if (p.ht == 64)
@@ -797,8 +831,10 @@ hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStrea
   return backward ? logits<Bf16, true>(a, s) : logits<Bf16, false>(a, s);
 }
 
-int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k) {
-  return m_tok < 1 ? 1 : grad_plan(m_tok, n_vocab, k).splits;
+HiddenPlan hidden_plan(int32_t m_tok, int32_t n_vocab, int32_t k) {
+  if (m_tok < 1) return HiddenPlan{1, 0};
+  const GradPlan p = grad_plan(m_tok, n_vocab, k);
+  return HiddenPlan{p.splits, p.few || p.ht == 256 ? 0 : p.ht};
 }
 
 hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t m_tok, int32_t range, bool fp16,
@@ -807,13 +843,13 @@ hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_
   return fp16 ? grads<Fp16>(w, h, p, s) : grads<Bf16>(w, h, p, s);
 }
 
-hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,
-                               int32_t k, uint16_t* dh, bool fp16, hipStream_t s) {
+hipError_t launch_hidden_final(const float* part, const HiddenPlan& plan, int32_t range_steps, const Header* hdr,
+                               const int32_t* rows, int32_t m_tok, int32_t k, uint16_t* dh, bool fp16, hipStream_t s) {
   const dim3 grid((unsigned)m_tok, (unsigned)((k + 255) / 256));
   if (fp16)
-    hidden_final_kernel<Fp16><<<grid, 256, 0, s>>>(part, splits, hdr, rows, m_tok, k, dh);
+    hidden_final_kernel<Fp16><<<grid, 256, 0, s>>>(part, plan, range_steps, hdr, rows, m_tok, k, dh);
   else
-    hidden_final_kernel<Bf16><<<grid, 256, 0, s>>>(part, splits, hdr, rows, m_tok, k, dh);
+    hidden_final_kernel<Bf16><<<grid, 256, 0, s>>>(part, plan, range_steps, hdr, rows, m_tok, k, dh);
   return hipGetLastError();
 }
 

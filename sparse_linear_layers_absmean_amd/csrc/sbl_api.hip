@@ -683,7 +683,7 @@ struct HeadLayout {
   int64_t bytes;
   int64_t np;                                                    // forward: statistics per token
   int64_t range;                                                 // backward: ids per range of the vocabulary
-  int splits;
+  sbl::head::HiddenPlan dh;
 };
 
 HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, bool backward) {
@@ -712,7 +712,7 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
   most = most < 256 ? 256 : most / 256 * 256;
   const int64_t ranges = (n_vocab + most - 1) / most;
   l.range = ((n_vocab + ranges - 1) / ranges + 255) / 256 * 256;
-  l.splits = sbl::head::hidden_splits((int32_t)m_tok, (int32_t)l.range, (int32_t)k);
+  l.dh = sbl::head::hidden_plan((int32_t)m_tok, (int32_t)l.range, (int32_t)k);
   l.lse2 = take(m_tok * 4);
   l.coef = take(m_tok * 4);
   l.index32 = take(m_tok * top * 4);
@@ -721,7 +721,7 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
   const int64_t rows = m_tok > sbl::head::kFewTokens ? m_tok : 2 * sbl::head::few_half(m_tok);
   l.hc = take(rows * k * 2);
   l.dz = take(rows * l.range * 2);
-  l.part = take((int64_t)l.splits * rows * k * 4);
+  l.part = take((int64_t)l.dh.splits * rows * k * 4);
   return l;
 }
 
@@ -898,15 +898,16 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
     a.half = half;
     if ((st = launch_status(sbl::head::launch_logits(a, fp16, true, s))) != SBL_OK) return st;
     const sbl::head::WeightGradArgs gw{a.dz, r.hc, r.hdr, rows, a.dz_rows, a.n_vocab, a.k, dw ? dw + v0 * c.k : nullptr};
-    const sbl::head::HiddenGradArgs gh{a.dz, a.w, r.hdr, rows, a.dz_rows, a.n_vocab, a.k, l.splits,
-                                       (int32_t)((steps + l.splits - 1) / l.splits),
+    const sbl::head::HiddenGradArgs gh{a.dz, a.w, r.hdr, rows, a.dz_rows, a.n_vocab, a.k, l.dh.splits,
+                                       (int32_t)((steps + l.dh.splits - 1) / l.dh.splits), (int32_t)steps,
                                        dh ? at<float>(c, l.part) : nullptr, v0 > 0};
     if ((st = launch_status(sbl::head::launch_grads(gw, gh, a.m_tok, (int32_t)l.range, fp16, s))) != SBL_OK) return st;
   }
   if (!dh) return SBL_OK;
-  return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), half > 0 ? 2 * l.splits : l.splits, r.hdr,
-                                                      r.rows, half > 0 ? half : (int32_t)c.m_tok, (int32_t)c.k, dh,
-                                                      fp16, s));
+  sbl::head::HiddenPlan plan = l.dh;
+  if (half > 0) plan.splits *= 2;                                // the second part's rows are shares of their own
+  return launch_status(sbl::head::launch_hidden_final(at<float>(c, l.part), plan, (int32_t)steps, r.hdr, r.rows,
+                                                      half > 0 ? half : (int32_t)c.m_tok, (int32_t)c.k, dh, fp16, s));
 }
 
 }  // namespace

@@ -73,7 +73,8 @@ struct HiddenGradArgs {
   int32_t m_tok;
   int32_t n_vocab, k;
   int32_t splits, split_steps;            // steps of 64 ids per share
-  float* part;                            // [splits][m_tok][k]
+  int32_t range_steps;                    // steps of a whole range
+  float* part;                            // [splits][m_tok][k], or as many rows
   int32_t add;                            // add to what earlier ranges left there
 };
 
@@ -126,14 +127,19 @@ inline int few_half(int64_t m_tok) { return m_tok > kFewTokens ? 0 : m_tok <= 32
 
 int64_t logits_tiles(int32_t m_tok, int32_t n_vocab, int32_t k);     // np of a forward call
 hipError_t launch_logits(const LogitsArgs& a, bool fp16, bool backward, hipStream_t s);
-// shares per dh tile, for ranges of n_vocab ids
-int hidden_splits(int32_t m_tok, int32_t n_vocab, int32_t k);
+// How dh is split over a range of n_vocab ids: shares per tile; token_tile > 0: the
+// shares are that many if all m_tok rows take part, more in proportion if fewer
+// do (tiles of token_tile rows), worked out on the GPU where the count is known.
+struct HiddenPlan {
+  int splits, token_tile;
+};
+HiddenPlan hidden_plan(int32_t m_tok, int32_t n_vocab, int32_t k);
 // both gradients of a range (either may be absent: dw or part NULL); `range`: ids of a whole range
 hipError_t launch_grads(const WeightGradArgs& w, const HiddenGradArgs& h, int32_t m_tok, int32_t range, bool fp16,
                         hipStream_t s);
 // dh[rows[t]] = down * sum_s part[s][t]
-hipError_t launch_hidden_final(const float* part, int splits, const Header* hdr, const int32_t* rows, int32_t m_tok,
-                               int32_t k, uint16_t* dh, bool fp16, hipStream_t s);
+hipError_t launch_hidden_final(const float* part, const HiddenPlan& plan, int32_t range_steps, const Header* hdr,
+                               const int32_t* rows, int32_t m_tok, int32_t k, uint16_t* dh, bool fp16, hipStream_t s);
 
 // which rows take part (strict: ids past the vocabulary take their row out,
 // as the backward needs); backward: also the header's scales

@@ -531,3 +531,41 @@ def test_an_id_of_no_probability(t):
     sbl.sbl_head_ce_backward(h, w, target, lse, torch.ones(t, device="cuda"), None, dw,
                              _dirty(sbl.sbl_head_workspace_bytes(t, v, d, backward=True)))
     assert dw.isfinite().all() and not dw[17].any()
+
+
+@pytest.mark.parametrize("t,v,d,kept", [(100, 70001, 256, 0.5), (200, 33001, 520, 0.1), (777, 20011, 392, 0.25),
+                                        (777, 20011, 392, 1.0), (130, 70001, 72, 0.01), (100, 140001, 8192, 0.3)])
+def test_dh_where_many_rows_are_taken_out(t, v, d, kept):
+    """dh is shared over the vocabulary by how many rows take part: few of many,
+    all, one; and (the last) in two ranges of the vocabulary."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    say(f"head_ce kept={kept} t={t} v={v} d={d}")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    h = torch.randn(t, d, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(v, d, generator=g, device="cuda") * (2.0 / d ** 0.5)).bfloat16()
+    target = torch.randint(0, v, (t,), generator=g, device="cuda")
+    gone = torch.rand(t, generator=g, device="cuda") >= kept
+    gone[t // 2] = False
+    target[gone] = -1
+    h[gone] = float("nan")
+    lse = sbl.head_ce(h, w, target)[1]
+    dloss = torch.rand(t, generator=g, device="cuda") + 0.5
+    dh, dw = torch.full_like(h, 7.0), torch.empty_like(w)
+    sbl.sbl_head_ce_backward(h, w, target, lse, dloss, dh, dw,
+                             _dirty(sbl.sbl_head_workspace_bytes(t, v, d, backward=True)))
+    torch.cuda.synchronize()
+    keep = ~gone
+    n, hk = int(keep.sum()), h[keep].double()
+    rh = torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    for i in range(0, v, 16384):
+        wi = w[i:i + 16384].double()
+        dz = dloss[keep].double()[:, None] * torch.exp(hk @ wi.t() - lse[keep].double()[:, None])
+        here = (target[keep] >= i) & (target[keep] < i + len(wi))
+        rows = torch.nonzero(here)[:, 0]
+        dz[rows, target[keep][rows] - i] -= dloss[keep].double()[rows]
+        rh += dz @ wi
+        # one rounding of dz and one of the result, each 2^-8 relative at most and never all at once
+        assert _rel(dw[i:i + 16384], dz.t() @ hk) < 2.0 ** -8
+    assert _rel(dh[keep], rh) < 2.0 ** -8
+    assert not dh[gone].any()
