@@ -163,6 +163,9 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
     hit_at[n] |= d >= 0 && d < TM ? (uint32_t)d : 255u;     // 128-id tile
     if constexpr (kBackward) hit_sub[n] = a.sub[(int64_t)(t0 + tok) * a.top + ent];
   }
+  // the other waves read the list after the products, whose first barrier waits
+  // for no LDS write (and may be the only one: a single step)
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   if constexpr (TN == 256)
     tl.run_wide(st, wave, lane, a.k);
   else
@@ -285,7 +288,7 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
       }
     }
   };
-  const int found = hit_count;             // written before the products' first barrier
+  const int found = hit_count;             // complete, as the list is, since the products' first barrier
   if (found <= kHits) {
     for (int n0 = 0; n0 < found; n0 += 64) {
       int rel = -1, et = 0, ek = 0;
