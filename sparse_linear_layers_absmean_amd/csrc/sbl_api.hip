@@ -704,9 +704,11 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
     l.zlist = take(m_tok * top * 4);
     return l;
   }
+  // few tokens: two rows of gradients and hidden states each (LogitsArgs::half)
+  const int64_t rows = m_tok > sbl::head::kFewTokens ? m_tok : 2 * sbl::head::few_half(m_tok);
   // ranges of equal width (a multiple of 256 ids), as few as hold
   // kHeadGradValues gradients (256 ids at least) and 2 GiB of weights
-  int64_t most = kHeadGradValues / (m_tok < 1 ? 1 : m_tok);
+  int64_t most = kHeadGradValues / rows;
   const int64_t by_w = kMaxHeadBytes / (2 * k) - 512;
   if (most > by_w) most = by_w;
   most = most < 256 ? 256 : most / 256 * 256;
@@ -717,8 +719,6 @@ HeadLayout head_layout(int64_t m_tok, int64_t n_vocab, int64_t k, int64_t top, b
   l.coef = take(m_tok * 4);
   l.index32 = take(m_tok * top * 4);
   l.sub = take(m_tok * top * 4);
-  // few tokens: two rows each (LogitsArgs::half)
-  const int64_t rows = m_tok > sbl::head::kFewTokens ? m_tok : 2 * sbl::head::few_half(m_tok);
   l.hc = take(rows * k * 2);
   l.dz = take(rows * l.range * 2);
   l.part = take((int64_t)l.dh.splits * rows * k * 4);

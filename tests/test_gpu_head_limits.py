@@ -1,0 +1,46 @@
+"""Losses of the output head on the GPU where their sizes end: vocabularies of
+tens of millions of ids, launches of more workgroups than one grid holds, and
+the gradients of an empty batch."""
+
+import pytest
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+def test_gradients_of_a_vocabulary_of_tens_of_millions():
+    """One token, 40 million ids.  Every id but the target has features 0 or 1/2
+    (the target none), so each feature of dh is a sum of positive terms: in fp32,
+    of fewer than 1000 roundings one after the other, with logit gradients of
+    2^-16 or better, it is off by less than 2^-12, and its rounding to BF16 by 2^-9."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    t, v, d, y = 1, 40000000, 8, 17
+    say(f"head_ce wide vocabulary t={t} v={v} d={d}")
+    g = torch.Generator(device="cuda").manual_seed(21)
+    w = torch.randint(0, 2, (v, d), generator=g, device="cuda", dtype=torch.int8).bfloat16() * 0.5
+    n = torch.arange(v, device="cuda")
+    w[:, 5] = (n >= (1 << 25)) * 0.5                 # where features of the first ids say nothing
+    w[:, 6] = (n < 512) * 0.5
+    w[:, 7] = (n >= v - 100) * 0.5
+    w[y] = 0
+    h = torch.tensor([[1.0, -2.0, 0.5, 3.0, -1.0, 2.0, 1.5, -0.5]], device="cuda").bfloat16()
+    target = torch.tensor([y], device="cuda")
+    loss, lse = sbl.head_ce(h, w, target)
+    dloss = torch.ones(1, device="cuda")
+    dh, dw = sbl.head_ce_backward(h, w, target, lse, dloss)
+    torch.cuda.synchronize()
+    z = torch.zeros(v, dtype=torch.float64, device="cuda")
+    for i in range(d):
+        z += w[:, i].double() * h[0, i].double()
+    ref = torch.logsumexp(z, 0)
+    assert abs(float(lse[0].double() - ref)) < 1e-4 and abs(float(loss[0].double() - ref)) < 1e-4
+    q = torch.exp(z - lse[0].double())
+    for i in range(d):
+        want = (q * w[:, i].double()).sum()
+        assert abs(float(dh[0, i].double() - want)) <= 2.0 ** -8 * float(want), (i, float(dh[0, i]), float(want))
+    q[y] -= 1
+    for i in range(d):
+        want = q * h[0, i].double()
+        assert bool(((dw[:, i].double() - want).abs() <= 2.0 ** -8 * want.abs()).all()), i

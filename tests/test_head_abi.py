@@ -128,3 +128,14 @@ def test_workspace_bytes(lib):
         assert fwd <= t * (8 * (v // 32 + 1) + 4 * 64 + 12 + 2 * 64) + 8 * 4096
         assert f(t, v, k, 1, 1) <= 2 * max(1 << 28, 256 * t) + 2 * t * k * (1 + 2 * 1024) + 32 * t + 16 * 4096
 
+
+
+@pytest.mark.parametrize("t,v,k", [(1, 40000000, 8), (7, 44000000, 24), (33, 1 << 26, 16), (64, 1 << 27, 8),
+                                   (65, 1 << 27, 8), (1, (1 << 31) - 1025, 8)])
+def test_gradients_held_at_a_time(lib, t, v, k):
+    """2^28 logit gradients at most, counting the two rows of each of up to 64 tokens
+    (64 or 128 rows in all): products read them within 32-bit offsets."""
+    splits = 1024                                   # more shares of dh than any plan takes
+    rows = t if t > 64 else 64 if t <= 32 else 128
+    rest = rows * k * (2 + 4 * splits) + t * 64 + 16 * 4096
+    assert lib.sbl_head_workspace_bytes(t, v, k, 1, 1) <= 2 * (1 << 28) + rest
