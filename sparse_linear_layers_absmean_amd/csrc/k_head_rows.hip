@@ -36,8 +36,8 @@ __device__ __forceinline__ bool counts(int64_t id, float teacher) {
 __device__ __forceinline__ float scale_base(float top, float tau) { return fmaxf(top * tau, 1e-30f); }
 
 // Distillation: one wave per row, flag = takes part; forward: the blocks of the
-// row's ids (near).  strict (backward): a row that lists
-// an id past the vocabulary does not (its loss is NaN, it has no gradient).
+// row's ids (near).  strict (backward): a row with an entry that counts and
+// whose id is past the vocabulary does not (its loss is NaN, it has no gradient).
 __global__ __launch_bounds__(256) void flag_kernel(const RowArgs a, bool strict) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= a.m_tok) return;
@@ -45,8 +45,9 @@ __global__ __launch_bounds__(256) void flag_kernel(const RowArgs a, bool strict)
   const int wide = (a.top + 7) / 8 * 8;
   for (int k = threadIdx.x & 63; k < wide; k += 64) {
     const int64_t id = k < a.top ? a.index[t * a.top + k] : -1;
-    if (k < a.top) any |= counts(id, a.teacher[t * a.top + k]);
-    bad |= id >= a.n_vocab;
+    const bool here = k < a.top && counts(id, a.teacher[t * a.top + k]);
+    any |= here;
+    bad |= here && id >= a.n_vocab;
     if (a.near && !strict) a.near[t * wide + k] = id >= 0 && id < a.n_vocab ? (uint16_t)(id >> 8) : 0xFFFFu;
   }
   const bool in = __ballot(any) != 0 && !(strict && __ballot(bad) != 0);
@@ -258,7 +259,8 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
 #pragma unroll 4
       for (int e = tid; e < entries; e += 256) {
         const int64_t id = a.index[e];
-        if (counts(id, a.teacher[e])) any[e / a.top] = 1;
+        if (!counts(id, a.teacher[e])) continue;
+        any[e / a.top] = 1;
         if (id >= a.n_vocab) wrong[e / a.top] = 1;
       }
       __syncthreads();

@@ -569,3 +569,31 @@ def test_dh_where_many_rows_are_taken_out(t, v, d, kept):
         assert _rel(dw[i:i + 16384], dz.t() @ hk) < 2.0 ** -8
     assert _rel(dh[keep], rh) < 2.0 ** -8
     assert not dh[gone].any()
+
+
+@pytest.mark.parametrize("t,top", [(7, 4), (60, 20), (300, 4), (300, 40), (1500, 12)])
+def test_absent_entries_hold_any_id(t, top):
+    """A teacher logit of -infinity makes its entry absent whatever its id, past the
+    vocabulary too (lists padded with the vocabulary's size, say), in both directions."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    v, d = 300, 64
+    g = torch.Generator(device="cuda").manual_seed(13)
+    h = torch.randn(t, d, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(v, d, generator=g, device="cuda") * 0.2).bfloat16()
+    index = torch.randint(0, v, (t, top), generator=g, device="cuda")
+    teacher = torch.randn(t, top, generator=g, device="cuda")
+    absent = torch.rand(t, top, generator=g, device="cuda") < 0.4
+    absent[:, 0] = False
+    absent[t // 2] = True                            # nothing left of this row
+    dloss = torch.rand(t, generator=g, device="cuda") + 0.5
+    results = []
+    for far in (-1, v, 2 ** 40):
+        i = torch.where(absent, torch.full_like(index, far), index)
+        x = torch.where(absent, torch.full_like(teacher, -float("inf")), teacher)
+        loss, lse = sbl.head_kd(h, w, i, x, 2.0)
+        results.append((loss, lse, *sbl.head_kd_backward(h, w, i, x, 2.0, lse, dloss)))
+    torch.cuda.synchronize()
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+    assert bool(results[0][2].any(dim=1).sum() == t - 1)
