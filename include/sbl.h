@@ -504,7 +504,7 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  *              of each per token, in 64 or 128 rows.
  * Products are exact and summed in fp32; softmax statistics and the loss are
  * fp32.  The backward rounds dz once to the 16-bit type before the two
- * products that read it, scaled so that the largest coefficient becomes 1
+ * products that read it, scaled so that the largest finite coefficient becomes 1
  * (BF16) or 2^14 (FP16): relative error 2^-8 (2^-11) of each at most, the size
  * of the outputs' own rounding.  Up to 64 tokens it is held in two 16-bit parts,
  * which leaves the outputs' rounding alone.  Sums have a fixed order: results
@@ -513,7 +513,8 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  * (m_tok + 256) * k and the span of h at most 2^30 values; m_tok * n_vocab below
  * about 2^42; 1e-4 <= tau <= 1e4.
  * m_tok == 0: the forward does nothing, the backward sets dw to zero.
- * Non-finite h or w in rows that take part: results are unspecified. */
+ * Non-finite h or w in rows that take part: results are unspecified.  A dloss
+ * or dlse that is not finite spoils its row of dh, and dw, but no other row of dh. */
 typedef enum { SBL_BF16 = 0, SBL_FP16 = 1 } sbl_dtype;
 
 /* Bytes of workspace of a head call; -1 for invalid sizes. */

@@ -31,9 +31,16 @@ __device__ __forceinline__ bool counts(int64_t id, float teacher) {
   return id >= 0 && teacher != -__builtin_inff();
 }
 
-// What the logit gradients are divided by: the largest coefficient; 1e-30
-// keeps the quotient finite when every one is zero (or next to it).
-__device__ __forceinline__ float scale_base(float top, float tau) { return fmaxf(top * tau, 1e-30f); }
+// What the logit gradients are divided by: the largest finite coefficient of any
+// row; 1e-30 keeps the quotient finite when every one is zero (or next to it).
+// A row whose coefficient is not finite (loss scaling that overflowed) has such
+// gradients itself, and dw has, but it scales no other row.
+__device__ __forceinline__ float scale_base(float top) { return fmaxf(top, 1e-30f); }
+__device__ __forceinline__ float finite_size(float x) { return fabsf(x) < __builtin_inff() ? fabsf(x) : 0.f; }
+__device__ __forceinline__ float row_size(const RowArgs& a, int64_t t) {
+  const float g = a.dloss[t], top = finite_size(g * a.tau);
+  return a.dlse ? fmaxf(top, finite_size((g + a.dlse[t]) * a.tau)) : top;
+}
 
 // Distillation: one wave per row, flag = takes part; forward: the blocks of the
 // row's ids (near).  strict (backward): a row with an entry that counts and
@@ -79,10 +86,7 @@ __global__ __launch_bounds__(1024) void rows_kernel(const RowArgs a, bool backwa
     if (t < a.m_tok) a.pos[t] = in ? at : -1;
     if (in) {
       a.rows[at] = (int32_t)t;
-      if (backward) {
-        const float g = a.dloss[t];
-        top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[t]) : 0.f));
-      }
+      if (backward) top = fmaxf(top, row_size(a, t));
     }
     before += all;
     __syncthreads();
@@ -93,7 +97,7 @@ __global__ __launch_bounds__(1024) void rows_kernel(const RowArgs a, bool backwa
   if (tid == 0) {
     for (int w = 1; w < 16; ++w) top = fmaxf(top, wave_top[w]);
     a.hdr->count = before;
-    const float amax = scale_base(top, a.tau);
+    const float amax = scale_base(top);
     a.hdr->amax = amax;
     a.hdr->up = a.up / amax;
     a.hdr->down = amax / a.up;
@@ -270,8 +274,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
     for (int64_t u = tid; u < a.m_tok; u += 256) {
       const bool in = a.target ? a.target[u] >= 0 && a.target[u] < a.n_vocab : any[u] && !wrong[u];
       if (!in) continue;
-      const float g = a.dloss[u];
-      top = fmaxf(top, fmaxf(fabsf(g), a.dlse ? fabsf(g + a.dlse[u]) : 0.f));
+      top = fmaxf(top, row_size(a, u));
       ++total;
       mine += u < t;
       self |= u == t;
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
     mine = before[0] + before[1] + before[2] + before[3];
     c = (here[0] | here[1] | here[2] | here[3]) ? mine : -1;
     pad = all[0] + all[1] + all[2] + all[3] + (int)(t - mine);
-    amax = scale_base(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), a.tau);
+    amax = scale_base(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
     if (tid == 0) {
       if (c >= 0) a.rows[c] = (int32_t)t;
       if (t == 0) {
@@ -324,7 +327,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
     dst[i] = src[i];
     if (kOwnRows && a.half > 0) dst[i + (int64_t)a.half * vecs] = src[i];
   }
-  // divided by the largest coefficient first: equal weights give exactly 1
+  // divided by the largest finite coefficient first: equal weights give exactly 1
   const float g = a.dloss[t] * a.tau / amax * a.up;
   if (tid == 0) {
     a.lse2[c] = a.lse_in[t] * kLog2e;

@@ -597,3 +597,37 @@ def test_absent_entries_hold_any_id(t, top):
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
     assert bool(results[0][2].any(dim=1).sum() == t - 1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", ["inf", "-inf", "nan"])
+@pytest.mark.parametrize("t,top", [(7, 4), (300, 4), (1500, 12)])
+def test_a_gradient_that_is_not_finite_stays_in_its_row(t, top, bad, dtype):
+    """dloss or dlse of one row infinite or NaN (an overflow under loss scaling): every
+    other row of dh is what it is with an ordinary value there."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    v, d, row = 300, 64, t // 2
+    g = torch.Generator(device="cuda").manual_seed(14)
+    h = torch.randn(t, d, generator=g, device="cuda").to(getattr(torch, dtype))
+    w = (torch.randn(v, d, generator=g, device="cuda") * 0.2).to(getattr(torch, dtype))
+    target = torch.randint(0, v, (t,), generator=g, device="cuda")
+    index = torch.randint(0, v, (t, top), generator=g, device="cuda")
+    teacher = torch.randn(t, top, generator=g, device="cuda")
+    dloss = torch.rand(t, generator=g, device="cuda") + 0.5
+    dlse = torch.randn(t, generator=g, device="cuda").clamp(-1, 1) * 0.25
+    dloss[0] = 2.0                                   # the largest coefficient is another row's
+    spoilt = dloss.clone()
+    spoilt[row] = float(bad)
+    spoilt_lse = dlse.clone()
+    spoilt_lse[row] = float(bad)
+    others = torch.arange(t, device="cuda") != row
+    lse = sbl.head_ce(h, w, target)[1]
+    want = sbl.head_ce_backward(h, w, target, lse, dloss, dlse=dlse)[0]
+    for a, b in ((spoilt, dlse), (dloss, spoilt_lse)):
+        dh = sbl.head_ce_backward(h, w, target, lse, a, dlse=b)[0]
+        assert torch.equal(dh[others], want[others]) and not dh[row].isfinite().any()
+    lse = sbl.head_kd(h, w, index, teacher, 2.0)[1]
+    want = sbl.head_kd_backward(h, w, index, teacher, 2.0, lse, dloss)[0]
+    dh = sbl.head_kd_backward(h, w, index, teacher, 2.0, lse, spoilt)[0]
+    assert torch.equal(dh[others], want[others]) and not dh[row].isfinite().any()
