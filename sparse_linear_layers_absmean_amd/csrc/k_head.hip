@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
   constexpr int kStage = (TM + TN) * kBK * 2;
   __shared__ __align__(16) uint8_t lds0[kStage];
   __shared__ __align__(16) uint8_t lds1[kStage];
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int tile = a.tile0 + xcd_tile(blockIdx.x, gridDim.x);
   if constexpr (TN == 256) {
     uint8_t* const st[2] = {lds0, lds1};
     logits_tile<E, TM, TN, WM, WN, kBackward, kPolicy>(a, tile, st);
@@ -751,24 +751,33 @@ GradPlan grad_plan(int64_t m_tok, int64_t n_vocab, int64_t k) {
 // from 30 tokens 524 -> 469 us with its logits, of 98 MB 41 -> 50.
 bool past_cache(int64_t n_vocab, int64_t k) { return n_vocab * k * 2 > (int64_t(128) << 20); }
 
+// Threads of one launch stay below 2^32; a product of more takes several.
+constexpr int64_t kLaunchTiles = int64_t(1) << 22;
+
 template <class E, bool kBackward>
-hipError_t logits(const LogitsArgs& a, hipStream_t s) {
+hipError_t logits(LogitsArgs a, hipStream_t s) {
   const LogitsTile t = logits_variant(a.m_tok, a.n_vocab, a.k);
-  const dim3 grid((unsigned)(ceil_div(a.n_vocab, t.tm) * ceil_div(a.m_tok, t.tn)));
+  const int64_t tiles = ceil_div(a.n_vocab, t.tm) * ceil_div(a.m_tok, t.tn);
   const bool once = a.m_tok <= t.tn && (kBackward ? past_cache(a.n_vocab / 2, a.k) : past_cache(a.n_vocab, a.k));
-  if (t.tn == 32 && once)
-    logits_kernel<E, 128, 32, 4, 1, kBackward, kNt><<<grid, 256, 0, s>>>(a);
-  else if (t.tn == 64 && once)
-    logits_kernel<E, 128, 64, 4, 1, kBackward, kNt><<<grid, 256, 0, s>>>(a);
-  else if (t.tn == 32)
-    logits_kernel<E, 128, 32, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
-  else if (t.tn == 64)
-    logits_kernel<E, 128, 64, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
-  else if (t.tn == 128)
-    logits_kernel<E, 256, 128, 4, 2, kBackward><<<grid, 512, 0, s>>>(a);
-  else
-    logits_kernel<E, 256, 256, 2, 4, kBackward><<<grid, 512, 0, s>>>(a);
-  return hipGetLastError();
+  for (int64_t first = 0; first < tiles; first += kLaunchTiles) {
+    const dim3 grid((unsigned)(tiles - first < kLaunchTiles ? tiles - first : kLaunchTiles));
+    a.tile0 = (int32_t)first;
+    if (t.tn == 32 && once)
+      logits_kernel<E, 128, 32, 4, 1, kBackward, kNt><<<grid, 256, 0, s>>>(a);
+    else if (t.tn == 64 && once)
+      logits_kernel<E, 128, 64, 4, 1, kBackward, kNt><<<grid, 256, 0, s>>>(a);
+    else if (t.tn == 32)
+      logits_kernel<E, 128, 32, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
+    else if (t.tn == 64)
+      logits_kernel<E, 128, 64, 4, 1, kBackward><<<grid, 256, 0, s>>>(a);
+    else if (t.tn == 128)
+      logits_kernel<E, 256, 128, 4, 2, kBackward><<<grid, 512, 0, s>>>(a);
+    else
+      logits_kernel<E, 256, 256, 2, 4, kBackward><<<grid, 512, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 constexpr int64_t kRunMax = 8;

@@ -33,6 +33,7 @@ struct LogitsArgs {
   int32_t k;
   int32_t top;                            // listed entries per token
   float scale;                            // log2(e) / tau
+  int32_t tile0;                          // first tile of this launch
   const uint16_t* near;                   // per row (forward: original) the 256-id blocks of its entries, 8 to a vector,
                                           //   ~0 where there is none; or NULL
   // forward

@@ -44,3 +44,31 @@ def test_gradients_of_a_vocabulary_of_tens_of_millions():
     for i in range(d):
         want = q * h[0, i].double()
         assert bool(((dw[:, i].double() - want).abs() <= 2.0 ** -8 * want.abs()).all()), i
+
+
+def test_a_product_of_more_workgroups_than_one_grid():
+    """2^18 tokens over more than 2^21 ids: over 2^32 threads in all.  64 of the rows
+    against 64 bits, within the oracle's bound of a 32-bit evaluation."""
+    import torch
+    from oracle import head_oracle as H
+    from sparse_linear_layers_absmean_amd import sbl
+    t, v, d = 1 << 18, (1 << 21) + 77, 8
+    say(f"head_ce many tiles t={t} v={v} d={d}")
+    g = torch.Generator(device="cuda").manual_seed(22)
+    h = torch.randn(t, d, generator=g, device="cuda").bfloat16()
+    w = torch.randn(v, d, generator=g, device="cuda").bfloat16()
+    target = torch.randint(0, v, (t,), generator=g, device="cuda")
+    rows = torch.cat([torch.tensor([0, 1, t - 2, t - 1], device="cuda"),
+                      torch.randint(0, t, (60,), generator=g, device="cuda")])
+    target[rows[:4]] = torch.tensor([0, v - 1, v - 77, v - 78], device="cuda")
+    loss, lse = sbl.head_ce(h, w, target)
+    torch.cuda.synchronize()
+    assert bool(lse.isfinite().all()) and bool(loss.isfinite().all())
+    hr, wd = h[rows].double(), w.double()
+    z = hr @ wd.t()
+    ref = torch.logsumexp(z, 1)
+    picked = z.gather(1, target[rows][:, None])[:, 0]
+    ez = (d + 1) * H.U32 * (hr.abs() @ wd.abs().t()).max(dim=1).values
+    bound = 2 * ez + 64 * H.U32 * (1 + ref.abs() + z.abs().max(dim=1).values)
+    assert bool(((lse[rows].double() - ref).abs() <= bound).all())
+    assert bool(((loss[rows].double() - (ref - picked)).abs() <= bound).all())
