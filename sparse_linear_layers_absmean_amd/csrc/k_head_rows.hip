@@ -370,7 +370,20 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
   if (a.near && tid < wide - a.top) a.near[(int64_t)c * wide + a.top + tid] = 0xFFFFu;
 }
 
+// dw of no tokens: a store of 16 bytes per thread and turn, the chip filled once.
+// (One of the launches that a graph may hold: no memory-set node.)
+__global__ __launch_bounds__(256) void zero_kernel(u32x4* out, int64_t vecs) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * 256)
+    out[i] = u32x4{0, 0, 0, 0};
+}
+
 }  // namespace
+
+hipError_t launch_zero(uint16_t* out, int64_t values, hipStream_t s) {
+  const int64_t vecs = values / 8, blocks = (vecs + 255) / 256;
+  zero_kernel<<<dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, s>>>(reinterpret_cast<u32x4*>(out), vecs);
+  return hipGetLastError();
+}
 
 hipError_t launch_rows(const RowArgs& a, bool backward, hipStream_t s) {
   if (!a.target) {

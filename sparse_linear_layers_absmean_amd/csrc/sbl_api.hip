@@ -842,7 +842,7 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
   if (c.m_tok == 0) {                                            // no token: dw = 0
     if (!dw) return SBL_OK;
     if (!aligned(dw, 16)) return SBL_ERR_ALIGN;
-    return launch_status(sbl::launch_workspace_init(reinterpret_cast<uint64_t*>(dw), dwb / 8, s));
+    return launch_status(sbl::head::launch_zero(dw, c.n_vocab * c.k, s));
   }
   if (!lse || !dloss) return SBL_ERR_NULL;
   if (!aligned(lse, 4) || !aligned(dloss, 4) || (dlse && !aligned(dlse, 4)) || (dh && !aligned(dh, 16)) ||

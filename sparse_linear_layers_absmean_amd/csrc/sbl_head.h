@@ -151,5 +151,8 @@ hipError_t launch_finish(const RowArgs& a, bool compact, hipStream_t s);
 bool gather_alone(int32_t m_tok, int32_t top);
 hipError_t launch_gather(const RowArgs& a, bool own_rows, hipStream_t s);
 
+// out[0 .. values) = 0 (a multiple of 8 values, 16-byte aligned)
+hipError_t launch_zero(uint16_t* out, int64_t values, hipStream_t s);
+
 }  // namespace head
 }  // namespace sbl
