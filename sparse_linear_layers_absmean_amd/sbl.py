@@ -66,7 +66,19 @@ def load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
-    lib.sbl_abi_version.restype = ctypes.c_int
+    try:
+        lib.sbl_abi_version.restype = ctypes.c_int
+        if lib.sbl_abi_version() != ABI_VERSION:
+            raise RuntimeError("libsbl.so ABI version mismatch: rebuild it")
+        _declare(lib)
+    except AttributeError as e:                      # built before the newest functions
+        raise RuntimeError(f"libsbl.so is older than its binding ({e}): rebuild it") from e
+    _lib = lib
+    return lib
+
+
+def _declare(lib):
+    """Argument and result types of every function."""
     lib.sbl_status_string.restype = ctypes.c_char_p
     lib.sbl_status_string.argtypes = [ctypes.c_int]
     lib.sbl_last_hip_error.restype = ctypes.c_int
@@ -143,10 +155,6 @@ def load():
     lib.sbl_head_kd_backward.restype = ctypes.c_int
     lib.sbl_head_kd_backward.argtypes = [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_i32, ctypes.c_float, _c_p, _c_p,
                                          *sizes, *tail]
-    if lib.sbl_abi_version() != ABI_VERSION:
-        raise RuntimeError("libsbl.so ABI version mismatch: rebuild it")
-    _lib = lib
-    return lib
 
 
 # ---------------------------------------------------------------- helpers
