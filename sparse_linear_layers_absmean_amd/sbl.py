@@ -176,9 +176,16 @@ def _ptr(t, dtype, nbytes: int, name: str):
     return t.data_ptr()
 
 
+# The current stream's handle without the stream object (0.3 us a call, not 2.7).
+# torch has the function for its own use only: where it lacks it, the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:                               # torch.cuda.current_stream().cuda_stream, without the object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -24,3 +24,15 @@ def test_a_library_of_another_source_is_refused(tmp_path, monkeypatch, code):
     with pytest.raises(RuntimeError, match="rebuild it"):
         sbl.load()
     assert sbl._lib is None
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_stream_with_and_without_torchs_own_function(monkeypatch, private):
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    # stands in for a torch whose module has, or lacks, the function
+    monkeypatch.setattr(sbl, "_raw_stream", (lambda device: 4096 + device) if private else None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("Stream", (), {"cuda_stream": 8192}))
+    assert sbl._stream(None) == (4098 if private else 8192)
+    assert sbl._stream(64) == 64
