@@ -549,6 +549,8 @@ def _head_args(h, w):
 
 
 def _teacher_args(index, teacher, m_tok: int):
+    if not isinstance(index, torch.Tensor) or not isinstance(teacher, torch.Tensor):
+        raise TypeError("index and teacher must be torch.Tensors")
     if index.dim() != 2 or index.shape != teacher.shape or index.shape[0] != m_tok:
         raise ValueError("index and teacher must be [m_tok][top]")
     top = index.shape[1]
@@ -723,7 +725,8 @@ def head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, workspace=Non
         with torch.cuda.stream(_torch_stream(stream)):
             return head_kd_backward(h, w, index, teacher, tau, lse, dloss, workspace)
     if workspace is None:
-        workspace, _ = _new_scratch(load(), _head_args(h, w), index.shape[1], 1, h.device)
+        head = _head_args(h, w)
+        workspace, _ = _new_scratch(load(), head, _teacher_args(index, teacher, head[4])[2], 1, h.device)
     dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
     sbl_head_kd_backward(h, w, index, teacher, tau, lse, dloss, dh, dw, workspace)
     return dh, dw

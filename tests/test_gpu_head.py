@@ -631,3 +631,19 @@ def test_a_gradient_that_is_not_finite_stays_in_its_row(t, top, bad, dtype):
     want = sbl.head_kd_backward(h, w, index, teacher, 2.0, lse, dloss)[0]
     dh = sbl.head_kd_backward(h, w, index, teacher, 2.0, lse, spoilt)[0]
     assert torch.equal(dh[others], want[others]) and not dh[row].isfinite().any()
+
+
+def test_refusals_of_the_bindings_lists():
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    h, w = torch.randn(4, 64, device="cuda").bfloat16(), torch.randn(10, 64, device="cuda").bfloat16()
+    index, teacher = torch.zeros((4, 2), dtype=torch.int64, device="cuda"), torch.zeros((4, 2), device="cuda")
+    f = torch.zeros(4, device="cuda")
+    for i, x, error in [(None, teacher, TypeError), (index, None, TypeError), (index, [[0.0] * 2] * 4, TypeError),
+                        (index[:, 0].contiguous(), teacher, ValueError), (index[:3], teacher[:3], ValueError),
+                        (index.int(), teacher, TypeError), (index, teacher.double(), TypeError),
+                        (index.t().contiguous().t(), teacher, ValueError)]:
+        with pytest.raises(error):
+            sbl.head_kd(h, w, i, x, 1.0)
+        with pytest.raises(error):
+            sbl.head_kd_backward(h, w, i, x, 1.0, f, f)
