@@ -99,7 +99,6 @@ __global__ __launch_bounds__(1024) void rows_kernel(const RowArgs a, bool backwa
     a.hdr->count = before;
     const float amax = scale_base(top);
     a.hdr->amax = amax;
-    a.hdr->up = a.up / amax;
     a.hdr->down = amax / a.up;
   }
 }
@@ -301,7 +300,6 @@ __global__ __launch_bounds__(256) void gather_kernel(const RowArgs a) {
       if (t == 0) {
         a.hdr->count = all[0] + all[1] + all[2] + all[3];
         a.hdr->amax = amax;
-        a.hdr->up = a.up / amax;
         a.hdr->down = amax / a.up;
       }
     }

@@ -861,7 +861,7 @@ int head_backward(const HeadCall& c, bool ce, const float* lse, const float* dlo
   r.lse_in = lse;
   r.dloss = dloss;
   r.dlse = dlse;
-  r.up = fp16 ? 16384.0f : 1.0f;
+  r.up = fp16 ? sbl::head::kUpFp16 : sbl::head::kUpBf16;
   r.lse2 = at<float>(c, l.lse2);
   r.coef = at<float>(c, l.coef);
   r.index32 = at<int32_t>(c, l.index32);

@@ -14,10 +14,14 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // device words at the start of a workspace
 struct Header {
   int32_t count;                          // rows that take part
-  float amax;                             // backward: largest |coefficient|; the stored logit gradient is
-  float up;                               //   dz * up, up = kUp / amax (0 when amax is 0)
-  float down;                             //   amax / kUp
+  float amax;                             // backward: largest finite |coefficient| (scale_base); the stored logit
+  float down;                             //   gradient is dz / down, down = amax / up (RowArgs)
 };
+
+// Factor that keeps the logit gradient (at most 2 in magnitude once divided by
+// the largest coefficient) in the 16-bit type's range: with 2^14 FP16 keeps its
+// 11 bits down to 2^-28 and is off by 2^-39 at most below; BF16 has FP32's range.
+constexpr float kUpBf16 = 1.0f, kUpFp16 = 16384.0f;
 
 // Logits over one range of the vocabulary, never stored: forward (softmax
 // statistics and the listed logits) or backward (their gradient).
@@ -45,7 +49,7 @@ struct LogitsArgs {
   // backward
   int64_t v0;                             // first id of this range
   const float* lse2;                      // [token] lse * log2(e)
-  const float* coef;                      // [token] softmax coefficient * up
+  const float* coef;                      // [token] softmax coefficient / down
   const int32_t* index32;                 // [token][top] id, or -1 (absent, or merged into an earlier entry)
   const float* sub;                       // [token][top] what to subtract at the id
   uint16_t* dz;                           // [n_vocab / 256, rounded up][dz_rows][256]
@@ -108,7 +112,7 @@ struct RowArgs {
   const float* lse_in;
   const float* dloss;
   const float* dlse;                      // nullable
-  float up;                               // the type's kUp
+  float up;                               // kUpBf16 or kUpFp16
   float* lse2;
   float* coef;
   int32_t* index32;

@@ -37,11 +37,8 @@ typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
-// The two 16-bit types.  kUp: factor that keeps the logit gradient (at most 2
-// in magnitude once divided by the largest coefficient) in the type's normal
-// range: 2^14 leaves FP16 12 bits of precision down to 2^-28; BF16 has FP32's range.
+// The two 16-bit types.
 struct Bf16 {
-  static constexpr float kUp = 1.0f;
   static __device__ __forceinline__ v4f mma(v8s a, v8s b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
   }
@@ -55,7 +52,6 @@ struct Bf16 {
   }
 };
 struct Fp16 {
-  static constexpr float kUp = 16384.0f;
   static __device__ __forceinline__ v4f mma(v8s a, v8s b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
