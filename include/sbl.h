@@ -483,9 +483,9 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  *   taken out.
  * Both: dh = dz w, dw = dz^T h.
  * A row that is taken out has loss = lse = 0 and a zero dh, adds nothing to
- * dw, and its h (NaN and infinities included), lse, dloss and dlse are not
- * used.  An id past the vocabulary makes its row's loss NaN, and takes the
- * row out of the backward.
+ * dw, and its h (NaN and infinities included), lse, dloss and dlse reach no
+ * result.  An id past the vocabulary (of an entry that is not absent) makes its
+ * row's loss NaN, and takes the row out of the backward.
  *
  *   h          [m_tok] rows of k values, row t at h + t * h_stride (h_stride a
  *              multiple of 8, >= k).
@@ -506,9 +506,12 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  * fp32.  The backward rounds dz once to the 16-bit type before the two
  * products that read it, scaled so that the largest finite coefficient becomes 1
  * (BF16) or 2^14 (FP16): relative error 2^-8 (2^-11) of each at most, the size
- * of the outputs' own rounding.  Up to 64 tokens it is held in two 16-bit parts,
- * which leaves the outputs' rounding alone.  Sums have a fixed order: results
- * repeat bit for bit.
+ * of the outputs' own rounding.  In FP16 a dz below 2^-28 of the largest
+ * coefficient of any row is off by up to 2^-39 of that coefficient instead:
+ * rows of a far smaller weight than the largest lose the small softmax
+ * probabilities.  Up to 64 tokens dz is held in two 16-bit parts, which leaves
+ * the outputs' rounding alone (and in FP16 the same 2^-39).  Sums have a fixed
+ * order: results repeat bit for bit.
  * Limits: 8 <= k <= 131072, k % 8 == 0; n_vocab * k <= 2^34; m_tok <= 2^22 and
  * (m_tok + 256) * k and the span of h at most 2^30 values; m_tok * n_vocab below
  * about 2^42; 1e-4 <= tau <= 1e4.

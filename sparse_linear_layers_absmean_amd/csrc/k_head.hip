@@ -8,6 +8,13 @@
 //             rounded once to 16 bits, a range of the vocabulary at a time;
 //             dw = dz^T h, dh = dz w
 //
+// dz is rounded because the two products that read it run on the 16-bit matrix
+// instructions: held in two 16-bit parts, as up to 64 tokens where the products
+// cost nothing, both would run twice (at 2048 x 32000 x 3200 they are 690 to 720 of
+// 1040 us).  The rounding is as large as the outputs' own: against 64 bits the
+// BF16 gradients there are off by 1.9e-3 of their norm (cross entropy) and 2.3e-3
+// (distillation), with dz in 32 bits by 1.7e-3.
+//
 // The logits are computed again in the backward: keeping them would take
 // tokens x vocabulary values (1 GB at 4096 x 128256 in 16 bits).
 #include "sbl_head.h"
@@ -251,7 +258,10 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs& a, int tile, const
   }
 
   // Listed ids on this wave's rows and columns, 64 at a time by ballot, then one
-  // by one (a wave-uniform walk to the accumulator, a handful per tile).
+  // by one (a wave-uniform walk to the accumulator).  That costs with their
+  // number: 2048 x 32000 x 3200 forward 345 us with one id per token, 391 with 64
+  // spread evenly (140 in the fullest tile), 733 with 64 that follow 1 / (id + 10)
+  // (6300), 986 with all in one block of 256 ids (16384).
   // Forward: the logit.  Backward: the lane that stored the id's gradient
   // stores it again with the listed part taken off, still from 32 bits.
   auto take = [&](int rel, int et, int ek, float sub) {
@@ -346,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(const LogitsArg
 // Rows of the tile are features (contiguous in memory, read down the k axis),
 // so a lane's 4 consecutive results are 4 consecutive features of an output row.
 // Bound by the matrix pipe from some hundred tokens on (both gradients of 2048 x
-// 32000 x 3200 in 690 to 700 us, 1190 TFLOP/s, the pipe busy 65%): a tile of dw has few steps,
+// 32000 x 3200 in 690 to 720 us, 1190 TFLOP/s at best, the pipe busy 65%): a tile of dw has few steps,
 // 32 at 2048 tokens, beside the 7 us of its start and its 128 KB of stores.
 
 template <class E, int TM, int TN, int WM, int WN, class St>
@@ -490,7 +500,8 @@ __device__ __forceinline__ int xcd_share(int n, int& first) {
 // absent), so that one's last, part empty round is filled by the other.  Each
 // XCD takes a contiguous run of each kind's tiles, the hidden gradient's, the
 // longer ones, first.  (Taking the two in turn costs a quarter more time:
-// workgroups of one kind run in step and share operands in L2.)
+// workgroups of one kind run in step and share operands in L2.)  Of 256 registers
+// one is spilled (8 bytes of scratch per lane).
 template <class E>
 __global__ __launch_bounds__(512, 2) void grads_wide_kernel(const WeightGradArgs w, const HiddenGradArgs h, int n_w,
                                                             int n_h) {

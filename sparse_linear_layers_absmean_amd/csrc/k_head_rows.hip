@@ -5,8 +5,9 @@
 //   cross entropy  takes part: target >= 0
 //   distillation   an entry counts when its index >= 0 and its teacher logit is
 //                  not -infinity; takes part: any entry counts
-// Only rows that take part are read and multiplied afterwards, so whatever a
-// row that is taken out holds (NaN, infinities) reaches nothing.
+// Only rows that take part are multiplied afterwards (up to 256 tokens the
+// forward multiplies all: a row's products stay in its own column), so whatever
+// a row that is taken out holds (NaN, infinities) reaches nothing.
 #include "sbl_head.h"
 #include "sbl_head_tile.h"
 
