@@ -762,7 +762,8 @@ GradPlan grad_plan(int64_t m_tok, int64_t n_vocab, int64_t k) {
 // from 30 tokens 524 -> 469 us with its logits, of 98 MB 41 -> 50.
 bool past_cache(int64_t n_vocab, int64_t k) { return n_vocab * k * 2 > (int64_t(128) << 20); }
 
-// Threads of one launch stay below 2^32; a product of more takes several.
+// Threads of one launch stay below 2^32 (past that a grid is cut short, without an
+// error); a product of more takes several.
 constexpr int64_t kLaunchTiles = int64_t(1) << 22;
 
 template <class E, bool kBackward>

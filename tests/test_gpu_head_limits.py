@@ -108,3 +108,54 @@ def test_no_tokens_zero_a_large_gradient_quickly():
     mine, fill = took(call), took(lambda: w.fill_(0.0))
     say(f"zeroed in {mine * 1e3:.0f} us, a fill takes {fill * 1e3:.0f}")
     assert mine < 10 * fill
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_the_most_tokens(dtype):
+    """2^22 tokens: logit gradients of 2 GiB in each of two ranges of the vocabulary,
+    hidden states read in 65536 steps.  Every row of dh and dw within the oracle's
+    bounds; a sum over the tokens has one rounding per 32 of them, and 40 more."""
+    import torch
+    from oracle import head_oracle as H
+    from sparse_linear_layers_absmean_amd import sbl
+    t, v, d = 1 << 22, 300, 16
+    say(f"head_ce many tokens t={t} v={v} d={d} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(23)
+    h = torch.randn(t, d, generator=g, device="cuda").to(getattr(torch, dtype))
+    w = (torch.randn(v, d, generator=g, device="cuda") * 0.5).to(getattr(torch, dtype))
+    target = torch.randint(0, v, (t,), generator=g, device="cuda")
+    target[torch.rand(t, generator=g, device="cuda") < 0.01] = -1
+    target[0], target[t - 1] = v - 1, 0
+    # FP16: a scale at which the sum over the tokens stays in its range
+    dloss = (torch.rand(t, generator=g, device="cuda") + 0.5) * (2.0 ** -10 if dtype == "float16" else 2.0 ** -22)
+    lse = sbl.head_ce(h, w, target)[1]
+    dh, dw = sbl.head_ce_backward(h, w, target, lse, dloss)
+    torch.cuda.synchronize()
+    u, tiny = H.U16[dtype], H.TINY16[dtype]
+    wd, base = w.double(), 2 * float(dloss.max())
+    rw, sizes = torch.zeros(v, d, dtype=torch.float64, device="cuda"), torch.zeros(v, d, dtype=torch.float64, device="cuda")
+    errors = torch.zeros_like(rw)
+    for i in range(0, t, 1 << 18):
+        b = slice(i, i + (1 << 18))
+        hd, keep = h[b].double(), (target[b] >= 0).double()
+        z = hd @ wd.t()
+        ez = (d + 1) * H.U32 * (hd.abs() @ wd.abs().t())
+        ref = torch.logsumexp(z, 1)
+        bound = 2 * ez.max(1).values + 64 * H.U32 * (1 + ref.abs() + z.abs().max(1).values)
+        s = lse[b].double()
+        assert bool(((s - ref * keep).abs() <= bound).all())
+        first = (dloss[b].double() * keep)[:, None] * torch.exp(z - s[:, None] - 100.0 * (1 - keep)[:, None])
+        second = torch.zeros_like(first).scatter_(1, target[b].clamp(min=0)[:, None], (dloss[b].double() * keep)[:, None])
+        dz = first - second
+        e = u * dz.abs() + first * (2 * ez + 64 * H.U32 * (1 + s.abs()[:, None] + z.abs()))
+        e = (e + 64 * H.U32 * (first + second) + 2.0 ** -38 * base * keep[:, None]) * (1 + 2 * u)
+        want = dz @ wd
+        err = e @ wd.abs() + (v + 8) * H.U32 * ((dz.abs() + e) @ wd.abs())
+        off = (dh[b].double() - want).abs() - (err + u * (want.abs() + err) + tiny)
+        assert not bool((off > 0).any()), (i, float(off.max()))
+        rw += dz.t() @ hd
+        errors += e.t() @ hd.abs()
+        sizes += (dz.abs() + e).t() @ hd.abs()
+    err = errors + (t / 32 + 40) * H.U32 * sizes
+    off = (dw.double() - rw).abs() - (err + u * (rw.abs() + err) + tiny)
+    assert bool(dw.isfinite().all()) and not bool((off > 0).any()), float(off.max())
