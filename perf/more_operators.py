@@ -255,9 +255,8 @@ def _statistics(x, center):
     """mean, rstd (rounded to 32 bits) and x less its mean, from sums in 64 bits."""
     x = x.double()
     mean = x.mean(dim=1, keepdim=True) * (1.0 if center else 0.0)
-    d = (x - mean).float()
-    var = d.double().square().mean(dim=1, keepdim=True)
-    return mean.float()[:, 0], (1.0 / (var + EPS_NORM).sqrt()).float()[:, 0], d
+    var = (x - mean).square().mean(dim=1, keepdim=True)
+    return mean.float()[:, 0], (1.0 / (var + EPS_NORM).sqrt()).float()[:, 0], (x - mean).float()
 
 
 def _norm(s):
