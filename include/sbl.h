@@ -518,7 +518,7 @@ int sbl_linear_backward_ws(const uint16_t* dy_bf16, int64_t m_tok, int64_t n_out
  * m_tok == 0: the forward does nothing, the backward sets dw to zero.
  * Non-finite h or w in rows that take part: results are unspecified.  A dloss
  * or dlse that is not finite spoils its row of dh, and dw, but no other row of dh. */
-typedef enum { SBL_BF16 = 0, SBL_FP16 = 1 } sbl_dtype;
+typedef enum { SBL_BF16 = 0, SBL_FP16 = 1, SBL_FP32 = 2 } sbl_dtype;
 
 /* Bytes of workspace of a head call; -1 for invalid sizes. */
 int64_t sbl_head_workspace_bytes(int64_t m_tok, int64_t n_vocab, int64_t k, int32_t top, int32_t backward);
@@ -540,6 +540,141 @@ int sbl_head_kd_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w,
                          const float* teacher, int32_t top, float tau, const float* lse, const float* dloss,
                          int64_t m_tok, int64_t n_vocab, int64_t k, uint16_t* dh, uint16_t* dw, void* workspace,
                          int64_t workspace_bytes, sbl_stream stream);
+
+/* ------------------------------------------------------------------------
+ * The norm before an activation quantizer ("subln" of the BitNet project
+ * page, "Especificaciones Tecnicas"), forward and backward; layer norm
+ * (center != 0) or RMS norm (center == 0) over rows of k values:
+ *   mean = sum x / k (0 if not centered),  d = RN32(x - mean)
+ *   rstd = RN32(1 / sqrt(sum (x - mean)^2 / k + eps)),  both sums in 64 bits
+ *   y    = RN(RN(RN(d * rstd) * weight) + bias)                  (fp32)
+ * and, where xq is given, the activation quantizer in the same pass, as
+ * sbl_quant_acts would take it from an fp32 y:
+ *   gamma = max_k |y|,  xq = clamp(rint(RN(y / (max(gamma, 1e-5) / 128))), -127, 127)
+ *   x          [m_tok][k], x_dtype (SBL_BF16, SBL_FP16 or SBL_FP32).
+ *   weight, bias  [k] fp32, or NULL (1 and 0).
+ *   eps        > 0.
+ *   y          [m_tok][k] output, or NULL: y_dtype is x_dtype or SBL_FP32, y
+ *              rounded once more to a 16-bit type (xq and gamma come from the
+ *              fp32 value).
+ *   xq, gamma  [m_tok][k] int8 and [m_tok] fp32 outputs, or both NULL; with
+ *              them k % 64 == 0.
+ *   mean, rstd [m_tok] fp32 outputs, each nullable: what the backward takes
+ *              (mean is 0 if not centered).
+ * The backward takes the gradient dy of y (dy_dtype: x_dtype or SBL_FP32):
+ *   xh = (x - mean) rstd,  g = dy weight
+ *   dx = rstd (g - [center] mean_k(g) - xh mean_k(g xh))         [m_tok][k], x_dtype
+ *   dweight = sum_t dy xh,  dbias = sum_t dy                     [k] fp32
+ * each of the three outputs nullable; mean is read only if centered.  Its sums
+ * are fp32, in a fixed order: results repeat bit for bit.
+ *   workspace  sbl_norm_workspace_bytes(m_tok, k) bytes, 256-byte aligned, any
+ *              contents (the backward's partial sums); calls in flight at the
+ *              same time need their own.
+ * Any 1 <= k <= 131072, m_tok <= 2^22, m_tok * k <= 2^34.  Alignment: 16 bytes
+ * for x, y, dx, dy and xq, 4 for the rest.  Outputs must not overlap each other
+ * or an input (SBL_ERR_SHAPE).  m_tok == 0: the forward does nothing, the
+ * backward sets dweight and dbias to zero. */
+int sbl_norm_forward(const void* x, int32_t x_dtype, const float* weight, const float* bias, int64_t m_tok, int64_t k,
+                     double eps, int32_t center, void* y, int32_t y_dtype, int8_t* xq, float* gamma, float* mean,
+                     float* rstd, sbl_stream stream);
+
+int64_t sbl_norm_workspace_bytes(int64_t m_tok, int64_t k);
+
+int sbl_norm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const float* mean,
+                      const float* rstd, const float* weight, int64_t m_tok, int64_t k, int32_t center, void* dx,
+                      float* dweight, float* dbias, void* workspace, int64_t workspace_bytes, sbl_stream stream);
+
+/* ------------------------------------------------------------------------
+ * The embedding: dense, as the output head (whose weights it may share).
+ *   out[t] = RN(scale * table[ids[t]]): one fp32 product, rounded once to
+ *   out_dtype.  A negative id gives a row of zeros, an id past the table a row
+ *   of NaNs.
+ *   ids        [m_tok] int64.
+ *   table      [n_vocab][k], table_dtype (SBL_BF16, SBL_FP16 or SBL_FP32).
+ *   out        [m_tok][k], out_dtype: table_dtype or SBL_FP32.
+ * Its gradient, from dout [m_tok][k] (dout_dtype: table_dtype or SBL_FP32):
+ *   dtable[v] = scale * sum over the t with ids[t] == v of dout[t]
+ * in fp32, the tokens in ascending order (an id of many tokens: in stretches
+ * whose sums are added in ascending order), rounded once to table_dtype.  Ids
+ * below 0 or past the table add nothing.  The result repeats bit for bit.
+ *   add        0: dtable [n_vocab][k] is written, zeros where an id has no
+ *              token.  Otherwise the sum is added to what dtable holds (for a
+ *              table that is the head's too: the dw of sbl_head_*_backward),
+ *              one rounding; rows without a token are left as they are.
+ *   workspace  sbl_embed_workspace_bytes(m_tok, n_vocab, k, dout_dtype) bytes,
+ *              256-byte aligned, any contents; calls in flight at the same time
+ *              need their own.
+ * Any 1 <= k <= 131072, m_tok <= 2^22, n_vocab <= 2^24, m_tok * k and n_vocab *
+ * k <= 2^34.  Alignment: 8 bytes for ids, 16 for the rest.  Outputs must not
+ * overlap an input (SBL_ERR_SHAPE).  m_tok == 0: the forward does nothing, the
+ * backward sets dtable to zero, or with `add` does nothing. */
+int sbl_embed_forward(const int64_t* ids, const void* table, int32_t table_dtype, int64_t m_tok, int64_t n_vocab,
+                      int64_t k, float scale, void* out, int32_t out_dtype, sbl_stream stream);
+
+int64_t sbl_embed_workspace_bytes(int64_t m_tok, int64_t n_vocab, int64_t k, int32_t dout_dtype);
+
+int sbl_embed_backward(const int64_t* ids, const void* dout, int32_t dout_dtype, int64_t m_tok, int64_t n_vocab,
+                       int64_t k, float scale, void* dtable, int32_t table_dtype, int32_t add, void* workspace,
+                       int64_t workspace_bytes, sbl_stream stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors in one call: the update of the masters that the next
+ * sbl_quant_weights reads, and of the head, embedding and norm weights.  Per
+ * value, every step one fp32 operation rounded to nearest, in this order
+ * (a = RN32(1 - beta)):
+ *   g' = g * factor
+ *   m' = RN(RN(beta1 m) + RN(a1 g')),  v' = RN(RN(beta2 v) + RN(a2 RN(g' g')))
+ *   w' = RN(RN(w decay) - RN(RN(m' / RN(RN(sqrt(v') bias2) + eps)) c))
+ *   bias1 = 1 / (1 - beta1^step), bias2 = 1 / sqrt(1 - beta2^step)
+ *   l = RN(lr lr_scale), c = RN(l bias1), decay = RN(1 - RN(l weight_decay))
+ * so that a step repeats bit for bit.  w' is rounded once to w's type.
+ *   w          [n] weights, w_dtype (SBL_BF16, SBL_FP16 or SBL_FP32), in place.
+ *   w_low      [n] int16 or NULL, for SBL_BF16 alone: the low bits of an fp32
+ *              weight whose bits are (w << 16) + w_low (w the nearest BF16 value,
+ *              ties away from zero, so -2^15 <= w_low < 2^15), in place.  Without
+ *              it an update below half a BF16 step is lost.
+ *   g          [n] gradient, g_dtype (any of the three).
+ *   m, v       the states, in place.  state_bits 32: [n] fp32.  state_bits 8:
+ *              [n] e4m3 bytes (4 exponent bits, 3 mantissa bits, no infinities)
+ *              with an fp32 scale for each 256 consecutive values in m_scale and
+ *              v_scale [ceil(n / 256)]: m = byte * scale, sqrt(v) = byte * scale.
+ *              New scales are max(RN(amax / 448), 2^-126), amax over the block's
+ *              m' or sqrt(v').  m' / scale is rounded to nearest (even);
+ *              sqrt(v') / scale to one of its two neighbours, at random in
+ *              proportion (rounding to nearest would hold v where it is: a step
+ *              moves it by 0.05% at beta2 = 0.999; the root held is within about
+ *              15%, one deviation, of the average), a root above zero never to
+ *              zero.  The random bits are a hash of the value's index in its
+ *              tensor and the step's seed.  All bytes and scales zero is the
+ *              state before the first step.
+ *   lr_scale   factor of lr for this tensor;  weight_decay: its decay.
+ * `items` is a HOST array of `count` (1..65536) descriptors; every buffer that is
+ * written must overlap no other buffer of the call (SBL_ERR_SHAPE).  Tensors of
+ * any n (0: skipped) up to 2^34.  Alignment: the element's size for w, w_low, g
+ * and 32-bit states, 8 bytes for 8-bit states, 4 for scales.
+ *   schedule   device fp32 [5]: lr, bias1, bias2, factor, seed (a whole number
+ *              below 2^24), read when the step runs, so that a captured step
+ *              follows what the caller writes there (a learning rate, a clipping
+ *              factor that never leaves the device); `lr` and `step` are ignored.
+ *              NULL: from lr and step (>= 1), with factor 1 and seed = step
+ *              modulo 2^24.
+ * 0 <= beta < 1, eps > 0, lr finite (SBL_ERR_SHAPE).  A gradient that is not
+ * finite spoils its value (8-bit states: its block of 256). */
+typedef struct {
+  void* w;
+  int16_t* w_low;          /* nullable                                       */
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;          /* state_bits 8                                   */
+  float* v_scale;          /* state_bits 8                                   */
+  int64_t n;
+  int32_t w_dtype, g_dtype, state_bits;
+  float lr_scale, weight_decay;
+} sbl_adamw_item;
+
+int sbl_adamw_batch(const sbl_adamw_item* items, int32_t count, double lr, double beta1, double beta2, double eps,
+                    int64_t step, const float* schedule, sbl_stream stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,11 @@ from .sbl import (SBL_FMT_DENSE2, SBL_FMT_NM, SblError, linear, load, new_backwa
                   sbl_workspace_init,
                   SBL_BF16, SBL_FP16, head_ce, head_ce_backward, head_kd, head_kd_backward, new_head_workspace,
                   sbl_head_ce_backward, sbl_head_ce_forward, sbl_head_kd_backward, sbl_head_kd_forward,
-                  sbl_head_workspace_bytes)
+                  sbl_head_workspace_bytes,
+                  SBL_FP32, AdamWItems, adamw_schedule, adamw_state, embed, embed_backward, join_master,
+                  new_embed_workspace, new_norm_workspace, norm, norm_backward, norm_quant, sbl_adamw_batch,
+                  sbl_embed_backward, sbl_embed_forward, sbl_embed_workspace_bytes, sbl_norm_backward,
+                  sbl_norm_forward, sbl_norm_workspace_bytes, split_master)
 
 __all__ = [
     "SBL_FMT_DENSE2", "SBL_FMT_NM", "SblError", "linear", "load", "new_backward_workspace", "new_workspace",
@@ -35,4 +39,8 @@ __all__ = [
     "SBL_BF16", "SBL_FP16", "head_ce", "head_ce_backward", "head_kd", "head_kd_backward", "new_head_workspace",
     "sbl_head_ce_backward", "sbl_head_ce_forward", "sbl_head_kd_backward", "sbl_head_kd_forward",
     "sbl_head_workspace_bytes",
+    "SBL_FP32", "AdamWItems", "adamw_schedule", "adamw_state", "embed", "embed_backward", "join_master",
+    "new_embed_workspace", "new_norm_workspace", "norm", "norm_backward", "norm_quant", "sbl_adamw_batch",
+    "sbl_embed_backward", "sbl_embed_forward", "sbl_embed_workspace_bytes", "sbl_norm_backward",
+    "sbl_norm_forward", "sbl_norm_workspace_bytes", "split_master",
 ]

@@ -1,0 +1,545 @@
+// Layer norm and RMS norm of rows, forward (with the activation quantizer in
+// the same pass) and backward (with the reduction of the weight's gradient).
+//
+// Forward, per row of k values:
+//   mean = center * sum x / k,  var = sum (x - mean)^2 / k,
+//   rstd = RN32(1 / sqrt(var + eps)),  y = RN(RN(RN32(x - mean) rstd) w) + b
+//   gamma = max |y|,  xq = clamp(rint(RN(y / s)), -127, 127), s = max(gamma, 1e-5) / 128
+// The sums are taken in fp64 in one pass, of the differences to the row's
+// first value (with it the two sums cancel only as far as that value is from
+// the mean).  Their order moves them by some 2^-50, so that mean, rstd and the
+// differences, rounded to fp32, are the same numbers for any partition of a row
+// but for about one row in 10^7; what follows is one rounding per step.
+// Backward: xh = (x - mean) rstd, g = dy w,
+//   dx = rstd (g - center * mean(g) - xh mean(g xh)),  dw = sum_t dy xh,  db = sum_t dy.
+// Both are bound by memory: x (and dy) read once, the outputs written once.
+// A row lies in the registers of one workgroup from its load to its store;
+// workgroups go over rows, so that weights stay in registers, the next row's
+// loads are in flight while a row is reduced, and the backward's column sums
+// need no memory until the end (one partial row per workgroup, joined in a
+// fixed order by a second launch).
+#include "sbl_actq.h"
+#include "sbl_step.h"
+
+namespace sbl {
+namespace step {
+
+namespace {
+
+constexpr int V = 4;                             // values per thread and slot
+constexpr int kMaxWaves = 16;
+
+// 1 / sqrt(v) to fp64's precision: v_rsq_f64 (24 bits) and two Newton steps
+__device__ __forceinline__ double rsqrt64(double v) {
+  double r = __builtin_amdgcn_rsq(v);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
+  return r;
+}
+
+struct Stat {
+  double mean;
+  float rstd;
+};
+// s1, s2: sums of (x - x0) and (x - x0)^2 (not centered: x0 = 0)
+__device__ __forceinline__ Stat statistics(double s1, double s2, double x0, double inv_k, double eps, int center) {
+  const double e = center ? s1 * inv_k : 0.0;
+  const double var = fmax(__builtin_fma(-e, e, s2 * inv_k), 0.0);
+  return Stat{x0 + e, (float)rsqrt64(var + eps)};
+}
+
+template <int T> __device__ __forceinline__ void add_stats(const Vec<T, V>& x, int have, double x0, double& s1, double& s2) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (j < have) {
+      const double e = (double)x[j] - x0;
+      s1 += e;
+      s2 = __builtin_fma(e, e, s2);
+    }
+  }
+}
+
+// the row's value of one position
+__device__ __forceinline__ float normal(float x, const Stat& st, float w, float b) {
+  return (float)((double)x - st.mean) * st.rstd * w + b;
+}
+
+__device__ __forceinline__ void load_param(const float* p, int col, int have, float none, float (&f)[V]) {
+  const Vec<kFp32, V> v = p ? load<kFp32, V>(p + col, have) : Vec<kFp32, V>{};
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = p ? v[j] : none;
+}
+
+// Rows of at most blockDim.x * SLOTS * V values, one workgroup per row and
+// then the row gridDim.x later.
+template <int TX, int TY, int SLOTS>
+__global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
+  typedef typename Mem<TX>::E EX;
+  typedef typename Mem<TY>::E EY;
+  __shared__ double part[2][2][kMaxWaves];       // of even and odd rows: one barrier per reduction
+  __shared__ float peak[2][kMaxWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int k = a.k;
+  const double inv_k = 1.0 / k;
+  const EX* x = static_cast<const EX*>(a.x);
+  int col[SLOTS], have[SLOTS];
+  float w[SLOTS][V], b[SLOTS][V];
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    col[i] = (tid + i * (int)blockDim.x) * V;
+    have[i] = k - col[i];
+    load_param(a.w, col[i], have[i], 1.0f, w[i]);
+    load_param(a.b, col[i], have[i], 0.0f, b[i]);
+  }
+  int64_t row = blockIdx.x;
+  Vec<TX, V> next[SLOTS];
+  EX next0 = x[row * k];
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, V>(x + row * k + col[i], have[i]);
+  for (int p = 0;; p ^= 1) {
+    const int64_t base = row * k;
+    Vec<TX, V> v[SLOTS];
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) v[i] = next[i];
+    const double x0 = a.center ? (double)to_f32<TX>(next0) : 0.0;
+    row += gridDim.x;
+    if (row < a.m_tok) {
+      next0 = x[row * k];
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, V>(x + row * k + col[i], have[i]);
+    }
+    double s1 = 0.0, s2 = 0.0;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) add_stats<TX>(v[i], have[i], x0, s1, s2);
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if ((tid & 63) == 0) {
+      part[p][0][wave] = s1;
+      part[p][1][wave] = s2;
+    }
+    __syncthreads();
+    s1 = part[p][0][0];
+    s2 = part[p][1][0];
+    for (int i = 1; i < waves; ++i) {
+      s1 += part[p][0][i];
+      s2 += part[p][1][i];
+    }
+    const Stat st = statistics(s1, s2, x0, inv_k, a.eps, a.center);
+    float mx = 0.0f;
+    float y[SLOTS][V];
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        y[i][j] = normal(v[i][j], st, w[i][j], b[i][j]);
+        if (j < have[i]) mx = fmaxf(mx, fabsf(y[i][j]));
+      }
+      if (a.y && have[i] > 0) store<TY, V>(static_cast<EY*>(a.y) + base + col[i], y[i], have[i]);
+    }
+    const int64_t at = base / k;
+    if (tid == 0) {
+      if (a.mean) a.mean[at] = (float)st.mean;
+      if (a.rstd) a.rstd[at] = st.rstd;
+    }
+    if (a.xq) {
+      mx = wave_max(mx);
+      if ((tid & 63) == 0) peak[p][wave] = mx;
+      __syncthreads();
+      float g = peak[p][0];
+      for (int i = 1; i < waves; ++i) g = fmaxf(g, peak[p][i]);
+      const actq::Step sp = actq::make_step(g);
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i)
+        if (have[i] > 0)
+          *reinterpret_cast<uint32_t*>(a.xq + base + col[i]) =
+              actq::q_word(float4{y[i][0], y[i][1], y[i][2], y[i][3]}, sp);
+      if (tid == 0) a.gamma[at] = g;
+    }
+    if (row >= a.m_tok) break;
+  }
+}
+
+// Longer rows: one workgroup per row, which reads it once for the statistics,
+// once for y and once more for xq (from L2 by then).
+template <int TX, int TY>
+__global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
+  typedef typename Mem<TX>::E EX;
+  typedef typename Mem<TY>::E EY;
+  __shared__ double part[2][kMaxWaves];
+  __shared__ float peak[kMaxWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, k = a.k;
+  const int64_t base = (int64_t)blockIdx.x * k;
+  const EX* x = static_cast<const EX*>(a.x) + base;
+  const double x0 = a.center ? (double)to_f32<TX>(x[0]) : 0.0;
+  double s1 = 0.0, s2 = 0.0;
+  for (int c = tid * V; c < k; c += 1024 * V) add_stats<TX>(load<TX, V>(x + c, k - c), k - c, x0, s1, s2);
+  s1 = wave_sum(s1);
+  s2 = wave_sum(s2);
+  if ((tid & 63) == 0) {
+    part[0][wave] = s1;
+    part[1][wave] = s2;
+  }
+  __syncthreads();
+  s1 = part[0][0];
+  s2 = part[1][0];
+  for (int i = 1; i < kMaxWaves; ++i) {
+    s1 += part[0][i];
+    s2 += part[1][i];
+  }
+  const Stat st = statistics(s1, s2, x0, 1.0 / k, a.eps, a.center);
+  auto value = [&](int c, float (&y)[V]) {
+    const Vec<TX, V> v = load<TX, V>(x + c, k - c);
+    float w[V], b[V];
+    load_param(a.w, c, k - c, 1.0f, w);
+    load_param(a.b, c, k - c, 0.0f, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = normal(v[j], st, w[j], b[j]);
+  };
+  float mx = 0.0f;
+  for (int c = tid * V; c < k; c += 1024 * V) {
+    float y[V];
+    value(c, y);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (c + j < k) mx = fmaxf(mx, fabsf(y[j]));
+    if (a.y) store<TY, V>(static_cast<EY*>(a.y) + base + c, y, k - c);
+  }
+  if (tid == 0) {
+    if (a.mean) a.mean[blockIdx.x] = (float)st.mean;
+    if (a.rstd) a.rstd[blockIdx.x] = st.rstd;
+  }
+  if (!a.xq) return;
+  mx = wave_max(mx);
+  if ((tid & 63) == 0) peak[wave] = mx;
+  __syncthreads();
+  float g = peak[0];
+  for (int i = 1; i < kMaxWaves; ++i) g = fmaxf(g, peak[i]);
+  const actq::Step sp = actq::make_step(g);
+  for (int c = tid * V; c < k; c += 1024 * V) {
+    float y[V];
+    value(c, y);
+    *reinterpret_cast<uint32_t*>(a.xq + base + c) = actq::q_word(float4{y[0], y[1], y[2], y[3]}, sp);
+  }
+  if (tid == 0) a.gamma[blockIdx.x] = g;
+}
+
+// ---------------------------------------------------------------- backward
+
+struct Pair {
+  float g, gx;                                   // sums of g and g xh
+};
+
+__device__ __forceinline__ float xhat(float x, float mean, float rstd) { return (x - mean) * rstd; }
+
+__device__ __forceinline__ float grad(float dy, float xh, float w, float rstd, float c1, float c2) {
+  return rstd * (dy * w - c1 - xh * c2);
+}
+
+// Rows of at most blockDim.x * SLOTS * V values, blockDim.x at most MOST.  Every
+// thread keeps the column sums of its own columns over the workgroup's rows.
+template <int TX, int TD, int SLOTS, int MOST>
+__global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, float* part_w, float* part_b) {
+  // weights and the next row in registers too, where 512 / waves per SIMD leaves them
+  constexpr bool kHold = SLOTS * MOST <= 2048;
+  typedef typename Mem<TX>::E EX;
+  typedef typename Mem<TD>::E ED;
+  __shared__ Pair part[2][kMaxWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int k = a.k;
+  const float inv_k = 1.0f / k;
+  const EX* x = static_cast<const EX*>(a.x);
+  const ED* dy = static_cast<const ED*>(a.dy);
+  int col[SLOTS], have[SLOTS];
+  float w[kHold ? SLOTS : 1][V], sw[SLOTS][V], sb[SLOTS][V];
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    col[i] = (tid + i * (int)blockDim.x) * V;
+    have[i] = k - col[i];
+    if constexpr (kHold) load_param(a.w, col[i], have[i], 1.0f, w[i]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) sw[i][j] = sb[i][j] = 0.0f;
+  }
+  int64_t row = blockIdx.x;
+  Vec<TX, V> nx[SLOTS];
+  Vec<TD, V> nd[SLOTS];
+  float nm = 0.0f, nr;
+  auto fetch = [&] {
+    nm = a.mean ? a.mean[row] : 0.0f;
+    nr = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      nx[i] = load<TX, V>(x + row * k + col[i], have[i]);
+      nd[i] = load<TD, V>(dy + row * k + col[i], have[i]);
+    }
+  };
+  fetch();
+  for (int p = 0;; p ^= 1) {
+    const int64_t base = row * k;
+    const float mean = nm, rstd = nr;
+    Vec<TX, V> vx[SLOTS];
+    Vec<TD, V> vd[SLOTS];
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      vx[i] = nx[i];
+      vd[i] = nd[i];
+    }
+    row += gridDim.x;
+    if (kHold && row < a.m_tok) fetch();
+    // values past the row: dy is zero there
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      float(&wi)[V] = w[kHold ? i : 0];
+      if constexpr (!kHold) load_param(a.w, col[i], have[i], 1.0f, wi);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xh = xhat(vx[i][j], mean, rstd), d = vd[i][j], g = d * wi[j];
+        s1 += g;
+        s2 = __builtin_fmaf(g, xh, s2);
+        sw[i][j] = __builtin_fmaf(d, xh, sw[i][j]);
+        sb[i][j] += d;
+      }
+    }
+    if (a.dx) {
+      s1 = wave_sum(s1);
+      s2 = wave_sum(s2);
+      if ((tid & 63) == 0) part[p][wave] = Pair{s1, s2};
+      __syncthreads();
+      s1 = part[p][0].g;
+      s2 = part[p][0].gx;
+      for (int i = 1; i < waves; ++i) {
+        s1 += part[p][i].g;
+        s2 += part[p][i].gx;
+      }
+      const float c1 = a.center ? s1 * inv_k : 0.0f, c2 = s2 * inv_k;
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        float d[V];
+        float(&wi)[V] = w[kHold ? i : 0];
+        if constexpr (!kHold) load_param(a.w, col[i], have[i], 1.0f, wi);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          d[j] = grad(vd[i][j], xhat(vx[i][j], mean, rstd), wi[j], rstd, c1, c2);
+        if (have[i] > 0) store<TX, V>(static_cast<EX*>(a.dx) + base + col[i], d, have[i]);
+      }
+    }
+    if (row >= a.m_tok) break;
+    if constexpr (!kHold) fetch();
+  }
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    if (have[i] <= 0) continue;
+    if (part_w) store<kFp32, V>(part_w + (int64_t)blockIdx.x * k + col[i], sw[i], have[i]);
+    if (part_b) store<kFp32, V>(part_b + (int64_t)blockIdx.x * k + col[i], sb[i], have[i]);
+  }
+}
+
+// Longer rows: the two means of every row first (one workgroup per row), then
+// every column by a thread of its own, which needs no other.
+template <int TX, int TD>
+__global__ __launch_bounds__(1024) void norm_grad_rows_kernel(const NormGradArgs a, float2* means) {
+  __shared__ Pair part[kMaxWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, k = a.k;
+  const int64_t row = blockIdx.x, base = row * k;
+  const typename Mem<TX>::E* x = static_cast<const typename Mem<TX>::E*>(a.x) + base;
+  const typename Mem<TD>::E* dy = static_cast<const typename Mem<TD>::E*>(a.dy) + base;
+  const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+  float s1 = 0.0f, s2 = 0.0f;
+  for (int c = tid * V; c < k; c += 1024 * V) {
+    const Vec<TX, V> vx = load<TX, V>(x + c, k - c);
+    const Vec<TD, V> vd = load<TD, V>(dy + c, k - c);
+    float w[V];
+    load_param(a.w, c, k - c, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float g = vd[j] * w[j];
+      s1 += g;
+      s2 = __builtin_fmaf(g, xhat(vx[j], mean, rstd), s2);
+    }
+  }
+  s1 = wave_sum(s1);
+  s2 = wave_sum(s2);
+  if ((tid & 63) == 0) part[wave] = Pair{s1, s2};
+  __syncthreads();
+  if (tid != 0) return;
+  s1 = s2 = 0.0f;
+  for (int i = 0; i < kMaxWaves; ++i) {
+    s1 += part[i].g;
+    s2 += part[i].gx;
+  }
+  means[row] = float2{a.center ? s1 / k : 0.0f, s2 / k};
+}
+
+template <int TX, int TD>
+__global__ __launch_bounds__(256) void norm_grad_columns_kernel(const NormGradArgs a, const float2* means, float* part_w,
+                                                                float* part_b) {
+  const int k = a.k, col = (blockIdx.x * 256 + threadIdx.x) * V, have = k - col;
+  if (have <= 0) return;
+  const typename Mem<TX>::E* x = static_cast<const typename Mem<TX>::E*>(a.x) + col;
+  const typename Mem<TD>::E* dy = static_cast<const typename Mem<TD>::E*>(a.dy) + col;
+  float w[V], sw[V] = {}, sb[V] = {};
+  load_param(a.w, col, have, 1.0f, w);
+  for (int64_t row = blockIdx.y; row < a.m_tok; row += gridDim.y) {
+    const Vec<TX, V> vx = load<TX, V>(x + row * k, have);
+    const Vec<TD, V> vd = load<TD, V>(dy + row * k, have);
+    const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+    const float2 c = a.dx ? means[row] : float2{0.0f, 0.0f};
+    float d[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float xh = xhat(vx[j], mean, rstd);
+      sw[j] = __builtin_fmaf(vd[j], xh, sw[j]);
+      sb[j] += vd[j];
+      d[j] = grad(vd[j], xh, w[j], rstd, c.x, c.y);
+    }
+    if (a.dx) store<TX, V>(static_cast<typename Mem<TX>::E*>(a.dx) + row * k + col, d, have);
+  }
+  if (part_w) store<kFp32, V>(part_w + (int64_t)blockIdx.y * k + col, sw, have);
+  if (part_b) store<kFp32, V>(part_b + (int64_t)blockIdx.y * k + col, sb, have);
+}
+
+// out[c] = sum over the partial rows, in ascending order within each of 16
+// shares, then share by share.  blockIdx.y: 0 the weight, 1 the bias.
+__global__ __launch_bounds__(256) void norm_grad_final_kernel(const float* part_w, const float* part_b, int rows, int k,
+                                                              float* dw, float* db) {
+  __shared__ float sum[16][16][V];
+  const float* part = blockIdx.y == 0 ? part_w : part_b;
+  float* out = blockIdx.y == 0 ? dw : db;
+  if (!out) return;
+  const int lane = threadIdx.x & 15, share = threadIdx.x >> 4;
+  const int col = (blockIdx.x * 16 + lane) * V, have = k - col;
+  float s[V] = {};
+  const int per = (rows + 15) / 16, r1 = min(rows, (share + 1) * per);
+  if (have > 0) {
+#pragma unroll 8
+    for (int r = share * per; r < r1; ++r) {
+      const Vec<kFp32, V> v = load<kFp32, V>(part + (int64_t)r * k + col, have);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] += v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[share][lane][j] = s[j];
+  __syncthreads();
+  if (share != 0 || have <= 0) return;
+#pragma unroll
+  for (int r = 1; r < 16; ++r)
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] += sum[r][lane][j];
+  store<kFp32, V>(out + col, s, have);
+}
+
+__global__ __launch_bounds__(256) void zero_floats_kernel(float* p, int n) {
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) p[i] = 0.0f;
+}
+
+constexpr int kMaxSlots = 4;                     // rows of up to 1024 * 4 * V values in registers (8 slots spill)
+
+int vectors(int64_t k) { return (int)((k + V - 1) / V); }
+
+// Slots per thread: one per thread as long as 1024 threads hold the row and
+// there are few rows (all of a row's loads in flight from as many waves as
+// possible); with more rows, 4 (more bytes in flight per wave, fewer waves to
+// join in a reduction), as long as that leaves two waves.
+int slots_for(int nv, int64_t m_tok) {
+  int s = 1;
+  if (m_tok >= 1024)
+    while (s < 4 && nv >= 2 * s * 128) s *= 2;
+  while (s < kMaxSlots && nv > 1024 * s) s *= 2;
+  return s;
+}
+int threads_for(int nv, int slots) { return ((nv + slots - 1) / slots + 63) / 64 * 64; }
+
+// workgroups that the chip holds at once
+int resident(int threads, int waves_per_simd) {
+  const int per_cu = 4 * waves_per_simd / (threads / 64);
+  return 256 * (per_cu < 1 ? 1 : per_cu);
+}
+
+template <int TX, int TY> hipError_t forward(const NormArgs& a, hipStream_t s) {
+  const int nv = vectors(a.k), slots = slots_for(nv, a.m_tok);
+  if (nv > 1024 * kMaxSlots) {
+    hipLaunchKernelGGL((norm_long_kernel<TX, TY>), dim3((unsigned)a.m_tok), dim3(1024), 0, s, a);
+    return hipGetLastError();
+  }
+  const int threads = threads_for(nv, slots);
+  const int64_t most = resident(threads, 4);
+  const dim3 grid((unsigned)(a.m_tok < most ? a.m_tok : most)), block((unsigned)threads);
+  if (slots == 1) hipLaunchKernelGGL((norm_kernel<TX, TY, 1>), grid, block, 0, s, a);
+  else if (slots == 2) hipLaunchKernelGGL((norm_kernel<TX, TY, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_kernel<TX, TY, 4>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+struct GradPlan {
+  int slots, threads;                            // slots 0: long rows
+  int64_t parts;                                 // partial rows of the column sums
+};
+GradPlan grad_plan(int64_t m_tok, int64_t k) {
+  const int nv = vectors(k);
+  GradPlan p{0, 256, 0};
+  if (nv <= 1024 * kMaxSlots) {
+    p.slots = slots_for(nv, m_tok);
+    p.threads = threads_for(nv, p.slots);
+    p.parts = resident(p.threads, p.slots == 4 && p.threads <= 512 ? 3 : 4);
+  } else {
+    p.parts = 2048 / ((nv + 255) / 256);         // 8 workgroups a CU over the columns and the rows' shares
+  }
+  if (p.parts > m_tok) p.parts = m_tok;
+  return p;
+}
+
+template <int TX, int TD> hipError_t backward(const NormGradArgs& a, hipStream_t s) {
+  const GradPlan p = grad_plan(a.m_tok, a.k);
+  // one share of the rows: its sums are the outputs
+  const bool join = p.parts > 1;
+  float* pw = !a.dw ? nullptr : join ? a.ws : a.dw;
+  float* pb = !a.db ? nullptr : join ? a.ws + p.parts * a.k : a.db;
+  const dim3 grid((unsigned)p.parts), block((unsigned)p.threads);
+  if (p.slots == 0) {
+    float2* means = reinterpret_cast<float2*>(a.ws + 2 * p.parts * a.k);
+    if (a.dx) hipLaunchKernelGGL((norm_grad_rows_kernel<TX, TD>), dim3((unsigned)a.m_tok), dim3(1024), 0, s, a, means);
+    hipLaunchKernelGGL((norm_grad_columns_kernel<TX, TD>), dim3((unsigned)((vectors(a.k) + 255) / 256), (unsigned)p.parts),
+                       dim3(256), 0, s, a, means, pw, pb);
+  } else if (p.slots == 1) {
+    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 1, 1024>), grid, block, 0, s, a, pw, pb);
+  } else if (p.slots == 2) {
+    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 2, 1024>), grid, block, 0, s, a, pw, pb);
+  } else if (p.threads <= 512) {
+    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 4, 512>), grid, block, 0, s, a, pw, pb);
+  } else {
+    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 4, 1024>), grid, block, 0, s, a, pw, pb);
+  }
+  if (join && (a.dw || a.db))
+    hipLaunchKernelGGL(norm_grad_final_kernel, dim3((unsigned)((vectors(a.k) + 15) / 16), 2), dim3(256), 0, s, pw, pb,
+                       (int)p.parts, a.k, a.dw, a.db);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(const NormArgs& a, int tx, int ty, hipStream_t s) {
+  if (tx == kBf16) return ty == kFp32 ? forward<kBf16, kFp32>(a, s) : forward<kBf16, kBf16>(a, s);
+  if (tx == kFp16) return ty == kFp32 ? forward<kFp16, kFp32>(a, s) : forward<kFp16, kFp16>(a, s);
+  return forward<kFp32, kFp32>(a, s);
+}
+
+// partial rows of both column sums; long rows: two means per row, 8-byte aligned
+int64_t norm_grad_ws_bytes(int64_t m_tok, int64_t k) {
+  const GradPlan p = grad_plan(m_tok, k);
+  return (2 * p.parts * k * 4 + (p.slots == 0 ? m_tok * 8 : 0) + 255) / 256 * 256;
+}
+
+hipError_t launch_norm_backward(const NormGradArgs& a, int tx, int td, hipStream_t s) {
+  if (a.m_tok == 0) {
+    for (float* p : {a.dw, a.db})
+      if (p) hipLaunchKernelGGL(zero_floats_kernel, dim3((unsigned)((a.k + 255) / 256)), dim3(256), 0, s, p, a.k);
+    return hipGetLastError();
+  }
+  if (tx == kBf16) return td == kFp32 ? backward<kBf16, kFp32>(a, s) : backward<kBf16, kBf16>(a, s);
+  if (tx == kFp16) return td == kFp32 ? backward<kFp16, kFp32>(a, s) : backward<kFp16, kFp16>(a, s);
+  return backward<kFp32, kFp32>(a, s);
+}
+
+}  // namespace step
+}  // namespace sbl

@@ -3,6 +3,7 @@
 
 #include "sbl.h"
 #include "sbl_head.h"
+#include "sbl_host.h"
 #include "sbl_internal.h"
 
 namespace {
@@ -13,19 +14,21 @@ constexpr int64_t kMaxK = 131072;            // 127*k < 2^24: fp32(acc) exact
 constexpr int64_t kMaxElems = int64_t(1) << 34;
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using sbl::aligned;
+using sbl::launch_status;
+using sbl::ranges_overlap;
 
 bool nm_ok(int32_t n, int32_t m) { return (m == 4 || m == 8) && n >= 1 && n <= m; }
 
 bool k_ok(int64_t k) { return k >= 64 && k <= kMaxK && k % 64 == 0; }
 
-int launch_status(hipError_t e) {
+}  // namespace
+
+int sbl::launch_status(hipError_t e) {
   if (e == hipSuccess) return SBL_OK;
   g_last_hip_error = (int)e;
   return SBL_ERR_LAUNCH;
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -77,11 +80,6 @@ int sbl_workspace_init(void* workspace, int64_t workspace_bytes, sbl_stream stre
 }  // extern "C"
 
 namespace {
-
-bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a && b && a0 < b0 + (uintptr_t)nb && b0 < a0 + (uintptr_t)na;
-}
 
 // own_ws: the item brings its workspace (checked here); false when the call
 // supplies the scratch itself (sbl_quant_weights_batch_noalloc).

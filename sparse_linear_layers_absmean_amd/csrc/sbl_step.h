@@ -1,0 +1,200 @@
+// Internal declarations of what a training step needs around the layer and
+// the head: the norm (k_norm.hip), the embedding (k_embed.hip) and the AdamW
+// update (k_adamw.hip); their calls are in sbl_api_step.hip.
+#pragma once
+
+#include "sbl_internal.h"
+
+namespace sbl {
+namespace step {
+
+// numeric types, numbered as sbl_dtype
+enum Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+inline int64_t type_bytes(int t) { return t == kFp32 ? 4 : 2; }
+
+// ---------------------------------------------------------------- norm
+
+struct NormArgs {
+  const void* x;                  // [m_tok][k]
+  const float* w;                 // [k] or NULL (ones)
+  const float* b;                 // [k] or NULL (zeros)
+  int64_t m_tok;
+  int32_t k;
+  int32_t center;                 // subtract the mean (layer norm) or not (RMS norm)
+  double eps;
+  void* y;                        // [m_tok][k] or NULL
+  int8_t* xq;                     // [m_tok][k] and
+  float* gamma;                   // [m_tok], or both NULL
+  float* mean;                    // [m_tok] or NULL
+  float* rstd;                    // [m_tok] or NULL
+};
+hipError_t launch_norm_forward(const NormArgs& a, int x_type, int y_type, hipStream_t s);
+
+struct NormGradArgs {
+  const void* dy;                 // [m_tok][k]
+  const void* x;                  // [m_tok][k]
+  const float* mean;              // [m_tok] or NULL (zeros)
+  const float* rstd;              // [m_tok]
+  const float* w;                 // [k] or NULL
+  int64_t m_tok;
+  int32_t k;
+  int32_t center;
+  void* dx;                       // [m_tok][k] or NULL
+  float* dw;                      // [k] or NULL
+  float* db;                      // [k] or NULL
+  float* ws;
+};
+int64_t norm_grad_ws_bytes(int64_t m_tok, int64_t k);
+hipError_t launch_norm_backward(const NormGradArgs& a, int x_type, int dy_type, hipStream_t s);
+
+// ---------------------------------------------------------------- embedding
+
+struct EmbedArgs {
+  const int64_t* ids;             // [m_tok]
+  const void* table;              // [n_vocab][k]
+  int64_t m_tok, n_vocab;
+  int32_t k;
+  float scale;
+  void* out;                      // [m_tok][k]
+};
+hipError_t launch_embed_forward(const EmbedArgs& a, int table_type, int out_type, hipStream_t s);
+
+struct EmbedGradArgs {
+  const int64_t* ids;             // [m_tok]
+  const void* dout;               // [m_tok][k]
+  int64_t m_tok, n_vocab;
+  int32_t k;
+  float scale;
+  void* dtable;                   // [n_vocab][k]
+  bool add;                       // add to what dtable holds, or write all of it
+  void* ws;
+};
+int64_t embed_grad_ws_bytes(int64_t m_tok, int64_t n_vocab, int64_t k, int out_type);
+hipError_t launch_embed_backward(const EmbedGradArgs& a, int out_type, int table_type, hipStream_t s);
+
+// ---------------------------------------------------------------- AdamW
+
+struct AdamItem {
+  void* w;
+  int16_t* low;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float lr_scale, weight_decay;
+  int32_t kind;                   // w_type + 3 * g_type
+  int32_t bits;                   // of the states: 32 or 8
+};
+
+// the factors of one step, on the device or by value
+struct AdamSchedule {
+  float lr, bias1, bias2, factor, seed;
+};
+
+struct AdamStep {
+  float b1, a1, b2, a2, eps;      // a = 1 - b
+  AdamSchedule now;
+  const AdamSchedule* schedule;   // or NULL: now
+};
+hipError_t launch_adamw(const AdamItem* items, int count, const AdamStep& step, hipStream_t s);
+
+// ---------------------------------------------------------------- values in memory
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+template <int T> struct Mem { typedef uint16_t E; };
+template <> struct Mem<kFp32> { typedef float E; };
+
+template <int T> __device__ __forceinline__ float to_f32(typename Mem<T>::E e) {
+  if constexpr (T == kBf16) return __builtin_bit_cast(float, (uint32_t)e << 16);
+  else if constexpr (T == kFp16) return (float)__builtin_bit_cast(_Float16, e);
+  else return e;
+}
+// one rounding to nearest, ties to even (fp32: none)
+template <int T> __device__ __forceinline__ typename Mem<T>::E from_f32(float f) {
+  if constexpr (T == kBf16) return __builtin_bit_cast(uint16_t, (__bf16)f);
+  else if constexpr (T == kFp16) return __builtin_bit_cast(uint16_t, (_Float16)f);
+  else return f;
+}
+
+// V consecutive values held as they lie in memory.  Rows of an odd number of
+// 16-bit values start anywhere, so the type asks for no more alignment than an
+// element has: gfx950 takes wide global accesses at any address.
+template <int T, int V> struct Vec {
+  typedef typename Mem<T>::E E;
+  E e[V];
+  __device__ __forceinline__ float operator[](int i) const { return to_f32<T>(e[i]); }
+};
+template <int T, int V> struct __attribute__((packed, aligned(sizeof(typename Mem<T>::E)))) Loose {
+  Vec<T, V> v;
+};
+
+// the V values at p, or its first `have` and zeros
+template <int T, int V>
+__device__ __forceinline__ Vec<T, V> load(const typename Mem<T>::E* p, int have) {
+  if (have >= V) return reinterpret_cast<const Loose<T, V>*>(p)->v;
+  Vec<T, V> v;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v.e[i] = i < have ? p[i] : (typename Mem<T>::E)0;
+  return v;
+}
+template <int T, int V>
+__device__ __forceinline__ void store(typename Mem<T>::E* p, const float (&f)[V], int have) {
+  if (have >= V) {
+    Loose<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.v.e[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<Loose<T, V>*>(p) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < have) p[i] = from_f32<T>(f[i]);
+  }
+}
+
+// ---------------------------------------------------------------- reductions over a wave
+
+// x of another lane of the wave: DPP control words, and lane 63's value after the last
+template <int CTRL, int ROWS> __device__ __forceinline__ float dpp(float x, float none) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x), CTRL,
+                                                               ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp(double x, double none) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x), n = __builtin_bit_cast(uint64_t, none);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)n, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(n >> 32), (int)(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the wave's 64 lanes in a fixed order, in every lane: pairs, fours,
+// eights and sixteens within each row of 16 lanes, then row after row.
+template <class F> __device__ __forceinline__ F wave_sum(F x) {
+  x += dpp<0xB1, 0xf>(x, (F)0);                 // quad_perm [1,0,3,2]
+  x += dpp<0x4E, 0xf>(x, (F)0);                 // quad_perm [2,3,0,1]
+  x += dpp<0x141, 0xf>(x, (F)0);                // row_half_mirror
+  x += dpp<0x140, 0xf>(x, (F)0);                // row_mirror
+  return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, dpp<0xB1, 0xf>(x, x));
+  x = fmaxf(x, dpp<0x4E, 0xf>(x, x));
+  x = fmaxf(x, dpp<0x141, 0xf>(x, x));
+  x = fmaxf(x, dpp<0x140, 0xf>(x, x));
+  return fmaxf(fmaxf(lane_value(x, 0), lane_value(x, 16)), fmaxf(lane_value(x, 32), lane_value(x, 48)));
+}
+
+}  // namespace step
+}  // namespace sbl

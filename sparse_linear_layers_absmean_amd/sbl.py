@@ -24,8 +24,8 @@ SBL_FMT_NM = 1
 # weight-preparation variants and execution choices (sbl_quant_weights_batch_ex flags)
 SBL_QW_DEFAULT, SBL_QW_BETA_KEPT, SBL_QW_MASK_FROM_CODES = 0, 1, 2
 SBL_QW_TWO_PASS, SBL_QW_NO_WAIT = 4, 8
-# 16-bit types of the output head's losses (sbl_dtype)
-SBL_BF16, SBL_FP16 = 0, 1
+# numeric types of dense operands (sbl_dtype); the output head's losses take the 16-bit ones
+SBL_BF16, SBL_FP16, SBL_FP32 = 0, 1, 2
 ABI_VERSION = 11
 
 _c_i64 = ctypes.c_int64
@@ -46,6 +46,13 @@ class QuantItem(ctypes.Structure):
     _fields_ = [("w_bf16", _c_p), ("n_out", _c_i64), ("k", _c_i64), ("beta", _c_p),
                 ("mask_bits", _c_p), ("codes", _c_p), ("packed", _c_p), ("meta", _c_p),
                 ("workspace", _c_p), ("workspace_bytes", _c_i64)]
+
+
+class AdamWItem(ctypes.Structure):
+    """sbl_adamw_item of include/sbl.h."""
+    _fields_ = [("w", _c_p), ("w_low", _c_p), ("g", _c_p), ("m", _c_p), ("v", _c_p), ("m_scale", _c_p), ("v_scale", _c_p),
+                ("n", _c_i64), ("w_dtype", _c_i32), ("g_dtype", _c_i32), ("state_bits", _c_i32),
+                ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
 
 
 class SblError(RuntimeError):
@@ -155,6 +162,24 @@ def _declare(lib):
     lib.sbl_head_kd_backward.restype = ctypes.c_int
     lib.sbl_head_kd_backward.argtypes = [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_i32, ctypes.c_float, _c_p, _c_p,
                                          *sizes, *tail]
+    c_f32, c_f64 = ctypes.c_float, ctypes.c_double
+    lib.sbl_norm_forward.restype = ctypes.c_int
+    lib.sbl_norm_forward.argtypes = [_c_p, _c_i32, _c_p, _c_p, _c_i64, _c_i64, c_f64, _c_i32, _c_p, _c_i32, _c_p, _c_p,
+                                     _c_p, _c_p, _c_p]
+    lib.sbl_norm_workspace_bytes.restype = _c_i64
+    lib.sbl_norm_workspace_bytes.argtypes = [_c_i64, _c_i64]
+    lib.sbl_norm_backward.restype = ctypes.c_int
+    lib.sbl_norm_backward.argtypes = [_c_p, _c_i32, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_p,
+                                      _c_p, _c_p, _c_i64, _c_p]
+    lib.sbl_embed_forward.restype = ctypes.c_int
+    lib.sbl_embed_forward.argtypes = [_c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_i64, c_f32, _c_p, _c_i32, _c_p]
+    lib.sbl_embed_workspace_bytes.restype = _c_i64
+    lib.sbl_embed_workspace_bytes.argtypes = [_c_i64, _c_i64, _c_i64, _c_i32]
+    lib.sbl_embed_backward.restype = ctypes.c_int
+    lib.sbl_embed_backward.argtypes = [_c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_i64, c_f32, _c_p, _c_i32, _c_i32, _c_p,
+                                       _c_i64, _c_p]
+    lib.sbl_adamw_batch.restype = ctypes.c_int
+    lib.sbl_adamw_batch.argtypes = [ctypes.POINTER(AdamWItem), _c_i32, c_f64, c_f64, c_f64, c_f64, _c_i64, _c_p, _c_p]
 
 
 # ---------------------------------------------------------------- helpers
@@ -605,6 +630,172 @@ def sbl_head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, dh, dw, w
         _stream(stream)))
 
 
+# ---------------------------------------------------------------- norm, embedding, AdamW
+
+_TYPES = {torch.bfloat16: SBL_BF16, torch.float16: SBL_FP16, torch.float32: SBL_FP32}
+
+
+def _type(t, name: str) -> int:
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_TYPES)}")
+    return _TYPES[t.dtype]
+
+
+def _here(t, dtype, shape, name: str):
+    """Device pointer of a contiguous tensor of this shape on the current GPU, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() if t.numel() else None
+
+
+def _rows(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.shape
+
+
+def _scratch(t, name: str = "workspace"):
+    """(pointer, bytes) of a workspace."""
+    return (_ptr(t, None, 0, name), _nbytes(t)) if t is not None else (None, 0)
+
+
+def sbl_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, y=None, xq=None, gamma=None,
+                     mean=None, rstd=None, stream=None):
+    """Layer norm (center) or RMS norm of the rows of x [m_tok][k] -> y (x's type or fp32) and/or its
+    int8 codes xq with gamma; mean, rstd fp32 [m_tok] for the backward.  Every output may be None."""
+    m_tok, k = _rows(x, "x")
+    f32 = torch.float32
+    _check("sbl_norm_forward", load().sbl_norm_forward(
+        _here(x, None, (m_tok, k), "x"), _type(x, "x"), _here(weight, f32, (k,), "weight"), _here(bias, f32, (k,), "bias"),
+        m_tok, k, eps, int(center), _here(y, None, (m_tok, k), "y"), _type(y if y is not None else x, "y"),
+        _here(xq, torch.int8, (m_tok, k), "xq"), _here(gamma, f32, (m_tok,), "gamma"), _here(mean, f32, (m_tok,), "mean"),
+        _here(rstd, f32, (m_tok,), "rstd"), _stream(stream)))
+
+
+def sbl_norm_workspace_bytes(m_tok: int, k: int) -> int:
+    return load().sbl_norm_workspace_bytes(m_tok, k)
+
+
+def sbl_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, center: bool = True, stream=None):
+    """Gradients of the norm from dy [m_tok][k] (x's type or fp32): dx in x's type, dweight and dbias fp32 [k]
+    (each may be None).  mean may be None where not centered."""
+    m_tok, k = _rows(x, "x")
+    f32 = torch.float32
+    _check("sbl_norm_backward", load().sbl_norm_backward(
+        _here(dy, None, (m_tok, k), "dy"), _type(dy, "dy"), _here(x, None, (m_tok, k), "x"), _type(x, "x"),
+        _here(mean, f32, (m_tok,), "mean"), _here(rstd, f32, (m_tok,), "rstd"), _here(weight, f32, (k,), "weight"), m_tok, k,
+        int(center), _here(dx, x.dtype, (m_tok, k), "dx"), _here(dweight, f32, (k,), "dweight"),
+        _here(dbias, f32, (k,), "dbias"), *_scratch(workspace), _stream(stream)))
+
+
+def _ids(ids):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    return _here(ids, torch.int64, tuple(ids.shape), "ids"), ids.numel()
+
+
+def sbl_embed_forward(ids, table, out, scale: float = 1.0, stream=None):
+    """out[t] = scale * table[ids[t]]: ids int64 of any shape, table [n_vocab][k], out [ids' shape][k] in the
+    table's type or fp32.  A negative id gives zeros, an id past the table NaNs."""
+    n_vocab, k = _rows(table, "table")
+    at, m_tok = _ids(ids)
+    _check("sbl_embed_forward", load().sbl_embed_forward(
+        at, _here(table, None, (n_vocab, k), "table"), _type(table, "table"), m_tok, n_vocab, k, scale,
+        _here(out, None, (*ids.shape, k), "out"), _type(out, "out"), _stream(stream)))
+
+
+def sbl_embed_workspace_bytes(m_tok: int, n_vocab: int, k: int, dtype=torch.bfloat16) -> int:
+    """dtype: of the gradient that comes in."""
+    return load().sbl_embed_workspace_bytes(m_tok, n_vocab, k, _TYPES[dtype])
+
+
+def sbl_embed_backward(ids, dout, dtable, workspace, scale: float = 1.0, add: bool = False, stream=None):
+    """Gradient of the table from dout [ids' shape][k] (the table's type or fp32): written to dtable
+    [n_vocab][k], or added to what it holds."""
+    n_vocab, k = _rows(dtable, "dtable")
+    at, m_tok = _ids(ids)
+    _check("sbl_embed_backward", load().sbl_embed_backward(
+        at, _here(dout, None, (*ids.shape, k), "dout"), _type(dout, "dout"), m_tok, n_vocab, k, scale,
+        _here(dtable, None, (n_vocab, k), "dtable"), _type(dtable, "dtable"), int(add), *_scratch(workspace),
+        _stream(stream)))
+
+
+class AdamWItems:
+    """The tensors of an AdamW step, checked once and kept alive: a sequence of dicts with keys
+      w             weights, any shape, contiguous: bfloat16, float16 or float32 (updated in place)
+      w_low         int16, of BF16 masters: the low bits of an fp32 weight (split_master), or absent
+      g             gradient, bfloat16, float16 or float32
+      m, v          states: both float32, or both float8_e4m3fn (or their bytes as uint8) with
+      m_scale, v_scale  float32, one for each 256 values
+      lr_scale, weight_decay  numbers (1 and 0 if absent)
+    of as many values as w each."""
+
+    def __init__(self, tensors):
+        self.tensors = [dict(t) for t in tensors]
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.device = None
+        self.array = (AdamWItem * len(self.tensors))()
+        for i, t in enumerate(self.tensors):
+            w, n = t["w"], t["w"].numel()
+            self._on_device(w, "w")
+            small = t["m"].dtype != torch.float32
+            state = (torch.float8_e4m3fn, torch.uint8) if small else torch.float32
+            scales = 4 * (-(-n // 256)) if small else 0
+            for name in ("m", "v", "w_low", "m_scale", "v_scale"):
+                if t.get(name) is not None:
+                    self._on_device(t[name], name)
+            if t["m"].numel() != n or t["v"].numel() != n:
+                raise ValueError(f"m and v have {t['m'].numel()} and {t['v'].numel()} values, w {n}")
+            self.array[i] = AdamWItem(
+                _ptr(w, None, 0, "w"), _ptr(t.get("w_low"), torch.int16, 2 * n, "w_low"), None,
+                _ptr(t["m"], state, n, "m"), _ptr(t["v"], state, n, "v"),
+                _ptr(t.get("m_scale"), torch.float32, scales, "m_scale") if small else None,
+                _ptr(t.get("v_scale"), torch.float32, scales, "v_scale") if small else None, n, _type(w, "w"), 0,
+                8 if small else 32, float(t.get("lr_scale", 1.0)), float(t.get("weight_decay", 0.0)))
+            self.set_gradient(i, t["g"])
+
+    def _on_device(self, t, name: str):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda or self.device not in (None, t.device):
+            raise ValueError(f"{name} must be on the GPU that the first tensor is on")
+        self.device = t.device
+
+    def set_gradient(self, i: int, g):
+        """Tensor i's gradient of the next steps."""
+        t, item = self.tensors[i], self.array[i]
+        self._on_device(g, "g")
+        if g.numel() != item.n:
+            raise ValueError(f"g has {g.numel()} values, w {item.n}")
+        item.g, item.g_dtype = _ptr(g, None, 0, "g"), _type(g, "g")
+        t["g"] = g
+
+
+def sbl_adamw_batch(items, lr: float, beta1: float, beta2: float, eps: float, step: int, schedule=None, stream=None):
+    """One AdamW step of every tensor of `items` (an AdamWItems, or a sequence of its dicts).  schedule: float32
+    [5] on the GPU (adamw_schedule), read in place of lr and step when the step runs."""
+    if not isinstance(items, AdamWItems):
+        items = AdamWItems(items)
+    if items.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current GPU")
+    _check("sbl_adamw_batch", load().sbl_adamw_batch(
+        items.array, len(items.tensors), lr, beta1, beta2, eps, step, _here(schedule, torch.float32, (5,), "schedule"),
+        _stream(stream)))
+
+
 # ---------------------------------------------------------------- allocating conveniences
 
 def new_workspace(n_out: int, k: int, device="cuda"):
@@ -730,3 +921,129 @@ def head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, workspace=Non
     dh, dw = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(w)
     sbl_head_kd_backward(h, w, index, teacher, tau, lse, dloss, dh, dw, workspace)
     return dh, dw
+
+
+def _like(x, dtype, name: str):
+    """The output type: x's unless another is asked for."""
+    if dtype not in (None, x.dtype, torch.float32):
+        raise TypeError(f"{name} must be {x.dtype} or torch.float32")
+    return dtype if dtype is not None else x.dtype
+
+
+def norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, dtype=None, stream=None):
+    """Allocate outputs and run sbl_norm_forward; returns (y, mean, rstd), y in x's type or float32."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return norm(x, weight, bias, eps, center, dtype)
+    m_tok, k = _rows(x, "x")
+    y = torch.empty((m_tok, k), dtype=_like(x, dtype, "dtype"), device=x.device)
+    mean = torch.empty(m_tok, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(m_tok, dtype=torch.float32, device=x.device)
+    sbl_norm_forward(x, weight, bias, eps, center, y=y, mean=mean, rstd=rstd)
+    return y, mean, rstd
+
+
+def norm_quant(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, dtype=None, want_y: bool = True,
+               stream=None):
+    """Allocate outputs and run sbl_norm_forward with the activation quantizer; returns (xq, gamma, y, mean, rstd):
+    what linear takes, and what the backward of both takes (y None unless wanted)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return norm_quant(x, weight, bias, eps, center, dtype, want_y)
+    m_tok, k = _rows(x, "x")
+    y = torch.empty((m_tok, k), dtype=_like(x, dtype, "dtype"), device=x.device) if want_y else None
+    xq = torch.empty((m_tok, k), dtype=torch.int8, device=x.device)
+    gamma, mean, rstd = torch.empty((3, m_tok), dtype=torch.float32, device=x.device).unbind(0)
+    sbl_norm_forward(x, weight, bias, eps, center, y=y, xq=xq, gamma=gamma, mean=mean, rstd=rstd)
+    return xq, gamma, y, mean, rstd
+
+
+def new_norm_workspace(m_tok: int, k: int, device="cuda"):
+    """Scratch for sbl_norm_backward at these sizes (any contents)."""
+    nbytes = sbl_norm_workspace_bytes(m_tok, k)
+    if nbytes < 0:
+        raise ValueError("unsupported shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def norm_backward(dy, x, mean, rstd, weight=None, want_bias: bool = False, center: bool = True, workspace=None,
+                  stream=None):
+    """Allocate outputs (and a workspace) and run sbl_norm_backward; returns (dx, dweight, dbias), dbias None
+    unless wanted.  dweight is that of a weight of ones where weight is None."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return norm_backward(dy, x, mean, rstd, weight, want_bias, center, workspace)
+    m_tok, k = _rows(x, "x")
+    if workspace is None:
+        workspace = new_norm_workspace(m_tok, k, x.device)
+    dx = torch.empty((m_tok, k), dtype=x.dtype, device=x.device)
+    dweight = torch.empty(k, dtype=torch.float32, device=x.device)
+    dbias = torch.empty(k, dtype=torch.float32, device=x.device) if want_bias else None
+    sbl_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, center=center)
+    return dx, dweight, dbias
+
+
+def embed(ids, table, scale: float = 1.0, dtype=None, stream=None):
+    """Allocate the output and run sbl_embed_forward; returns rows of the table's type or float32."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return embed(ids, table, scale, dtype)
+    _, k = _rows(table, "table")
+    out = torch.empty((*ids.shape, k), dtype=_like(table, dtype, "dtype"), device=table.device)
+    sbl_embed_forward(ids, table, out, scale)
+    return out
+
+
+def new_embed_workspace(m_tok: int, n_vocab: int, k: int, dtype=torch.bfloat16, device="cuda"):
+    """Scratch for sbl_embed_backward at these sizes (any contents); dtype: of the gradient that comes in."""
+    nbytes = sbl_embed_workspace_bytes(m_tok, n_vocab, k, dtype)
+    if nbytes < 0:
+        raise ValueError("unsupported shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def embed_backward(ids, dout, n_vocab: int, scale: float = 1.0, dtype=None, add_to=None, workspace=None, stream=None):
+    """Allocate outputs (and a workspace) and run sbl_embed_backward; returns the table's gradient [n_vocab][k] in
+    dtype (dout's unless given), or add_to with the gradient added."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return embed_backward(ids, dout, n_vocab, scale, dtype, add_to, workspace)
+    k = dout.shape[-1]
+    if add_to is not None and tuple(add_to.shape) != (n_vocab, k):
+        raise ValueError(f"add_to has shape {tuple(add_to.shape)}, expected {(n_vocab, k)}")
+    out = add_to if add_to is not None else \
+        torch.empty((n_vocab, k), dtype=dtype if dtype is not None else dout.dtype, device=dout.device)
+    if workspace is None:
+        workspace = new_embed_workspace(ids.numel(), n_vocab, k, dout.dtype, dout.device)
+    sbl_embed_backward(ids, dout, out, workspace, scale, add=add_to is not None)
+    return out
+
+
+def split_master(w32):
+    """An fp32 weight as BF16 master and int16 low bits: (w, w_low), nearest BF16, ties away from zero."""
+    bits = w32.contiguous().view(torch.int32)
+    high = (bits + 0x8000) >> 16
+    return high.to(torch.int16).view(torch.bfloat16), (bits - (high << 16)).to(torch.int16)
+
+
+def join_master(w, w_low):
+    """The fp32 weight that a BF16 master and its low bits are."""
+    return ((w.view(torch.int16).to(torch.int32) << 16) + w_low.to(torch.int32)).view(torch.float32)
+
+
+def adamw_state(w, bits: int = 32):
+    """The states of w before the first step, as keys of an AdamWItems dict: m and v, in 8 bits with their scales."""
+    n, device = w.numel(), w.device
+    if bits == 32:
+        return {name: torch.zeros(n, dtype=torch.float32, device=device) for name in ("m", "v")}
+    if bits != 8:
+        raise ValueError("bits must be 8 or 32")
+    state = {name: torch.zeros(n, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for name in ("m", "v")}
+    state.update({name: torch.zeros(-(-n // 256), dtype=torch.float32, device=device) for name in ("m_scale", "v_scale")})
+    return state
+
+
+def adamw_schedule(lr: float, beta1: float, beta2: float, step: int, factor: float = 1.0):
+    """The five numbers of a step's schedule, as a float32 tensor on the host."""
+    return torch.tensor([lr, 1.0 / (1.0 - beta1 ** step), (1.0 - beta2 ** step) ** -0.5, factor,
+                         float(step % (1 << 24))], dtype=torch.float32)
