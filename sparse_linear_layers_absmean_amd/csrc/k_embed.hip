@@ -30,56 +30,78 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// tx threads (a power of two) side by side in a row, V values each
-template <int TT, int TO, int V>
-__global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedArgs a, int tx) {
+// n / d for n < 2^31 (d + 1) / (d - 1), or any n below 2^32 if d is a power of two: the
+// factor is off by e < d / 2^(31 + s), and n e < 2^(31 + s) leaves the quotient whole
+struct Divider {
+  uint32_t factor;
+  int shift;
+};
+Divider divider(uint32_t d) {
+  int s = 0;
+  while ((uint64_t(1) << s) < d) ++s;            // 2^(s-1) < d <= 2^s: the factor lies in [2^31, 2^32)
+  return Divider{(uint32_t)(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, Divider d) { return (uint32_t)(((uint64_t)n * d.factor) >> d.shift); }
+
+// The output as one sequence of vectors, nv to a row, U of each thread:
+// consecutive lanes hold consecutive vectors whatever a row's length is, and the
+// ids, then the rows, of all U are in flight together.
+template <int TT, int TO, int V, int U>
+__global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedArgs a, uint32_t nv, Divider by_nv, uint32_t total) {
   typedef typename Mem<TT>::E ET;
   typedef typename Mem<TO>::E EO;
-  const int x = threadIdx.x & (tx - 1), y = threadIdx.x / tx, ty = kThreads / tx;
-  const int64_t row = (int64_t)blockIdx.x * ty + y;
-  if (row >= a.m_tok) return;
-  const int64_t id = a.ids[row];
-  EO* out = static_cast<EO*>(a.out) + row * a.k;
-  const bool here = id >= 0 && id < a.n_vocab;
-  const ET* in = static_cast<const ET*>(a.table) + (here ? id * a.k : 0);
-  const float fill = id < 0 ? 0.0f : __builtin_nanf("");
-  const int step = tx * V * gridDim.y;
-  for (int c = (blockIdx.y * tx + x) * V; c < a.k; c += 4 * step) {
-    Vec<TT, V> v[4] = {};
-    if (here) {
+  const uint32_t first = blockIdx.x * (kThreads * U) + threadIdx.x;
+  uint32_t row[U];
+  int64_t id[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + u * step < a.k) v[u] = load<TT, V>(in + c + u * step, a.k - c - u * step);
+  for (int u = 0; u < U; ++u) {
+    const uint32_t n = first + u * kThreads;
+    row[u] = divide(n < total ? n : total - 1, by_nv);
+    id[u] = a.ids[row[u]];
+  }
+  Vec<TT, V> v[U];
+  Place at[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t n = first + u * kThreads;
+    at[u] = place<V>((int)((n < total ? n : total - 1) - row[u] * nv) * V, a.k);
+    const bool here = id[u] >= 0 && id[u] < a.n_vocab;
+    v[u] = load<TT, V>(static_cast<const ET*>(a.table) + (here ? id[u] * a.k : 0) + at[u].col);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (first + u * kThreads >= total) break;
+    float f[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      f[j] = v[u][j] * a.scale;
+      if (id[u] < 0) f[j] = 0.0f;
+      if (id[u] >= a.n_vocab) f[j] = __builtin_nanf("");
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (c + u * step >= a.k) break;
-      float f[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = here ? v[u][j] * a.scale : fill;
-      store<TO, V>(out + c + u * step, f, a.k - c - u * step);
-    }
+    store_own<TO, V, true>(static_cast<EO*>(a.out) + (int64_t)row[u] * a.k + at[u].col, f, at[u].skip);
   }
 }
 
-template <int TT, int TO> hipError_t forward(const EmbedArgs& a, hipStream_t s) {
-  constexpr int V = 8;
-  const int nv = (a.k + V - 1) / V;
-  int tx = 1;
-  while (tx < kThreads && tx < nv) tx *= 2;
-  const int64_t gx = (a.m_tok + kThreads / tx - 1) / (kThreads / tx);
-  // few rows: a row's columns over several workgroups
-  int64_t gy = 1;
-  while (gx * gy < 1024 && gy * tx < nv) gy *= 2;
-  hipLaunchKernelGGL((embed_kernel<TT, TO, V>), dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), 0, s, a, tx);
+template <int TT, int TO, int V, int U> hipError_t forward_vectors(const EmbedArgs& a, hipStream_t s) {
+  const uint32_t nv = (uint32_t)((a.k + V - 1) / V), total = (uint32_t)(a.m_tok * nv);
+  hipLaunchKernelGGL((embed_kernel<TT, TO, V, U>), dim3((total + kThreads * U - 1) / (kThreads * U)), dim3(kThreads), 0, s, a,
+                     nv, divider(nv), total);
   return hipGetLastError();
+}
+
+template <int TT, int TO> hipError_t forward(const EmbedArgs& a, hipStream_t s) {
+  constexpr int V = 8;                           // m_tok * nv <= 2^31 + 7/8 m_tok vectors: within the divider's range
+  if (a.k < V) return forward_vectors<TT, TO, 1, 1>(a, s);
+  // few vectors: one of each thread, so that there are more waves
+  if (a.m_tok * ((a.k + V - 1) / V) < 4 * 1024 * kThreads) return forward_vectors<TT, TO, V, 1>(a, s);
+  return forward_vectors<TT, TO, V, 4>(a, s);
 }
 
 // ---------------------------------------------------------------- backward: order
 
 constexpr int kSortWaves = 16;
 constexpr int kSortThreads = 64 * kSortWaves;
-constexpr int kMaxRange = 1008;                  // ids per workgroup (63 KB of counters)
+constexpr int kMaxRange = 800;                   // ids per workgroup (counters and lists in 64 KB)
 
 // Workspace
 struct Order {
@@ -94,11 +116,33 @@ struct SortArgs {
   Order o;
 };
 
+constexpr int kListed = 96;                      // tokens of the range that a wave remembers from its count
+
 __device__ __forceinline__ uint64_t lanes_below() { return (uint64_t(1) << (threadIdx.x & 63)) - 1; }
+
+// f(t, d, inside) for 64 tokens at a time of [t0, t1), d = id - v0; the ids of
+// 1024 tokens are in flight together
+template <class F> __device__ __forceinline__ void scan(const int64_t* ids, int t0, int t1, F f) {
+  constexpr int U = 16;
+  const int lane = threadIdx.x & 63;
+  for (int t = t0; t < t1; t += 64 * U) {
+    int64_t id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = t + 64 * u + lane;
+      id[u] = ids[at < t1 ? at : t1 - 1];
+      if (at >= t1) id[u] = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + 64 * u < t1) f(t + 64 * u + lane, id[u]);
+  }
+}
 
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
   extern __shared__ uint32_t count[];            // [wave][range]: counts, then the next place
   __shared__ uint32_t below[kSortWaves], sums[kSortWaves];
+  __shared__ uint2 list[kSortWaves][kListed];    // (token, id - v0) in order
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t v0 = (int64_t)blockIdx.x * a.range;
   const uint32_t range = (uint32_t)(a.n_vocab - v0 < a.range ? a.n_vocab - v0 : a.range);
@@ -108,18 +152,19 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
   const int per = ((a.m_tok + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   const int t0 = wave * per, t1 = t0 + per < a.m_tok ? t0 + per : a.m_tok;
   uint32_t* mine = count + wave * a.range;
-  uint32_t low = 0;
-  for (int t = t0; t < t1; t += 256) {
-    int64_t id[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) id[u] = t + 64 * u + lane < t1 ? a.ids[t + 64 * u + lane] : -1;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      low += id[u] >= 0 && id[u] < v0;
-      const uint64_t d = (uint64_t)(id[u] - v0);
-      if (d < range) atomicAdd(&mine[d], 1u);
+  uint32_t low = 0, listed = 0;
+  scan(a.ids, t0, t1, [&](int t, int64_t id) {
+    low += id >= 0 && id < v0;
+    const uint64_t d = (uint64_t)(id - v0);
+    const uint64_t inside = __ballot(d < range);
+    if (!inside) return;
+    if (d < range) {
+      atomicAdd(&mine[d], 1u);
+      const uint32_t at = listed + (uint32_t)__builtin_popcountll(inside & lanes_below());
+      if (at < kListed) list[wave][at] = uint2{(uint32_t)t, (uint32_t)d};
     }
-  }
+    listed += (uint32_t)__builtin_popcountll(inside);
+  });
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) low += __shfl_xor(low, m, 64);
   if (lane == 0) below[wave] = low;
@@ -148,30 +193,35 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
     }
   }
   __syncthreads();
-  for (int t = t0; t < t1; t += 256) {
-    int64_t id[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) id[u] = t + 64 * u + lane < t1 ? a.ids[t + 64 * u + lane] : -1;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint64_t d = (uint64_t)(id[u] - v0);
-      uint64_t left = __ballot(d < range);
-      while (left) {                             // the distinct ids among these 64 tokens
-        const int first = __builtin_ctzll(left);
-        const uint32_t which = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)d, first);
-        const bool same = d < range && (uint32_t)d == which;
-        const uint64_t group = __ballot(same);
-        const uint32_t place = mine[which];      // this wave's counters: no other wave writes them
-        if (same) {
-          const uint32_t at = place + (uint32_t)__builtin_popcountll(group & lanes_below());
-          a.o.key[at] = (int32_t)id[u];
-          a.o.pos[at] = t + 64 * u + lane;
-        }
-        if (lane == first) mine[which] = place + (uint32_t)__builtin_popcountll(group);
-        __builtin_amdgcn_wave_barrier();
-        left &= ~group;
+  // 64 tokens of this wave in order, those inside the range (d < range) to their places
+  auto put = [&](int t, uint32_t d) {
+    uint64_t left = __ballot(d < range);
+    while (left) {                               // the distinct ids among them
+      const int first = __builtin_ctzll(left);
+      const uint32_t which = (uint32_t)__builtin_amdgcn_readlane((int)d, first);
+      const uint64_t group = __ballot(d == which);
+      const uint32_t place = mine[which];        // this wave's counters: no other wave touches them
+      if (d == which) {
+        const uint32_t at = place + (uint32_t)__builtin_popcountll(group & lanes_below());
+        a.o.key[at] = (int32_t)(v0 + d);
+        a.o.pos[at] = t;
       }
+      if (lane == first) mine[which] = place + (uint32_t)__builtin_popcountll(group);
+      __builtin_amdgcn_wave_barrier();
+      left &= ~group;
     }
+  };
+  if (listed <= kListed) {
+    for (uint32_t i = 0; i < listed; i += 64) {
+      const bool has = i + lane < listed;
+      const uint2 e = has ? list[wave][i + lane] : uint2{0, range};
+      put((int)e.x, e.y);
+    }
+  } else {                                       // too many to remember: read the ids again
+    scan(a.ids, t0, t1, [&](int t, int64_t id) {
+      const uint64_t d = (uint64_t)(id - v0);
+      put(t, d < range ? (uint32_t)d : range);
+    });
   }
 }
 
@@ -185,20 +235,21 @@ struct SumArgs {
   int32_t segment;                               // S
   int32_t segments, chunks;                      // of columns: chunk_vecs vectors each
   int32_t chunk_vecs;
-  int32_t zero_groups;                           // workgroups that zero rows, after the others
+  int32_t zero_groups, zero_rows;                // workgroups that zero rows, after the others; rows of each wave
   Order o;
   float* part;                                   // [segments][2][k]: what a long run has in a segment that it comes
                                                  //   into [0], or begins in [1]
 };
 
-// one row's columns to memory
-template <int TT, int V, bool ADD>
-__device__ __forceinline__ void put(typename Mem<TT>::E* row, int have, const float (&sum)[V], float scale,
+// One row's columns to memory.  LINES: rows are whole 128-byte lines, stored past
+// the caches.
+template <int TT, int V, bool ADD, bool LINES>
+__device__ __forceinline__ void put(typename Mem<TT>::E* row, int skip, const float (&sum)[V], float scale,
                                     const Vec<TT, V>& old) {
   float f[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) f[j] = ADD ? old[j] + sum[j] * scale : sum[j] * scale;
-  store<TT, V>(row, f, have);
+  store_own<TT, V, LINES>(row, f, skip);
 }
 
 // where the run of id `v` lies
@@ -207,23 +258,44 @@ struct Run {
 };
 __device__ __forceinline__ Run run_of(const Order& o, int v) { return Run{o.start[v], o.start[v + 1]}; }
 
-template <int TD, int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads) void sum_kernel(const SumArgs a) {
+// Zeros in those of `many` (at most 64) rows from row v0 on that have no token.
+// Neighbouring ones are one stretch of memory, whose 128-byte lines are stored
+// whole and past the caches (rows of an odd length begin anywhere; lines in
+// parts past the caches are slower than within them).  One wave.
+template <class E>
+__device__ __forceinline__ void zero_rows(E* table, const int32_t* start, int n_vocab, int k, int v0, int many) {
+  const int lane = threadIdx.x & 63;
+  if (v0 >= n_vocab) return;
+  const int n = n_vocab - v0 < many ? n_vocab - v0 : many;
+  uint64_t empty = __ballot(lane < n && start[v0 + (lane < n ? lane : 0)] == start[v0 + (lane < n ? lane : 0) + 1]);
+  while (empty) {
+    const int from = __builtin_ctzll(empty);
+    const uint64_t rest = ~(empty >> from);
+    const int rows = rest ? __builtin_ctzll(rest) : 64 - from;
+    empty = from + rows < 64 ? empty >> (from + rows) << (from + rows) : 0;
+    E* p = table + (int64_t)(v0 + from) * k;
+    const int64_t values = (int64_t)rows * k;
+    const int per = 128 / (int)sizeof(E);        // at most 64: an edge is a value a lane
+    int64_t head = (128 - (reinterpret_cast<uintptr_t>(p) & 127)) % 128 / sizeof(E);
+    if (head > values) head = values;
+    const int64_t lines = (values - head) / per, tail = head + lines * per;
+    if (lane < head) p[lane] = (E)0;
+    u32x4* piece = reinterpret_cast<u32x4*>(p + head);
+    for (int64_t i = lane; i < lines * 8; i += 64) __builtin_nontemporal_store(u32x4{}, piece + i);
+    if (tail + lane < values) p[tail + lane] = (E)0;
+  }
+}
+
+template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bounds__(kThreads) void sum_kernel(const SumArgs a) {
   typedef typename Mem<TD>::E ED;
   typedef typename Mem<TT>::E ET;
   ET* table = static_cast<ET*>(a.dtable);
   const int work = a.segments * a.chunks;
   const int lane = threadIdx.x & 63;
   if constexpr (!ADD) {
-    if ((int)blockIdx.x >= work) {               // rows without a token: a wave each
+    if ((int)blockIdx.x >= work) {               // rows without a token
       const int wave = ((int)blockIdx.x - work) * (kThreads / 64) + (threadIdx.x >> 6);
-      const int waves = a.zero_groups * (kThreads / 64);
-      for (int v = wave; v < a.n_vocab; v += waves) {
-        const Run r = run_of(a.o, v);
-        if (r.begin != r.end) continue;
-        ET* row = table + (int64_t)v * a.k;
-        const float none[V] = {};
-        for (int c = lane * V; c < a.k; c += 64 * V) store<TT, V>(row + c, none, a.k - c);
-      }
+      zero_rows(table, a.o.start, a.n_vocab, a.k, wave * a.zero_rows, a.zero_rows);
       return;
     }
   }
@@ -232,8 +304,8 @@ template <int TD, int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads
   const int i0 = seg * S;
   if (i0 >= total) return;
   const int i1 = i0 + S < total ? i0 + S : total;
-  const int col = threadIdx.x < a.chunk_vecs ? (chunk * a.chunk_vecs + (int)threadIdx.x) * V : a.k;
-  const int have = a.k - col > 0 ? a.k - col : 0;
+  // (a thread past the chunk: no column of its own)
+  const Place c = place<V>((int)threadIdx.x < a.chunk_vecs ? (chunk * a.chunk_vecs + (int)threadIdx.x) * V : a.k + V, a.k);
   // the tokens of this segment: from the first run that begins in it (or from
   // its start, inside a long run) to the end of the last one that begins in it
   // (or to its own end, inside a long run)
@@ -242,7 +314,7 @@ template <int TD, int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads
   const bool long_tail = tail.end > i1 && tail.end - tail.begin > S;
   const int from = head.begin == i0 || long_head ? i0 : head.end;
   const int to = long_tail ? i1 : tail.end;
-  const ED* dout = static_cast<const ED*>(a.dout) + col;
+  const ED* dout = static_cast<const ED*>(a.dout) + c.col;
   float sum[V] = {};
   constexpr int U = 8;                           // tokens whose loads are in flight
   for (int i = from; i < to; i += 64) {
@@ -259,10 +331,10 @@ template <int TD, int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads
       for (int u = 0; u < U; ++u) {
         if (j + u >= n) break;
         const int t = __builtin_amdgcn_readlane(pos, j + u);
-        d[u] = load<TD, V>(dout + (int64_t)t * a.k, have);
+        d[u] = load<TD, V>(dout + (int64_t)t * a.k);
         if constexpr (ADD) {
           if (ends >> (j + u) & 1)
-            old[u] = load<TT, V>(table + (int64_t)__builtin_amdgcn_readlane(key, j + u) * a.k + col, have);
+            old[u] = load<TT, V>(table + (int64_t)__builtin_amdgcn_readlane(key, j + u) * a.k + c.col);
         }
       }
 #pragma unroll
@@ -275,9 +347,9 @@ template <int TD, int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads
           const bool in_head = long_head && at < head.end, in_tail = long_tail && at == to - 1;
           if (in_head || in_tail) {
             const bool begins = in_tail && tail.begin >= i0;
-            if (have > 0) store<kFp32, V>(a.part + ((int64_t)seg * 2 + begins) * a.k + col, sum, have);
-          } else if (have > 0) {
-            put<TT, V, ADD>(table + (int64_t)v * a.k + col, have, sum, a.scale, old[ADD ? u : 0]);
+            store_own<kFp32, V>(a.part + ((int64_t)seg * 2 + begins) * a.k + c.col, sum, c.skip);
+          } else {
+            put<TT, V, ADD, LINES>(table + (int64_t)v * a.k + c.col, c.skip, sum, a.scale, old[ADD ? u : 0]);
           }
 #pragma unroll
           for (int e = 0; e < V; ++e) sum[e] = 0.0f;
@@ -289,7 +361,7 @@ template <int TD, int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads
 
 // The long run that begins in segment blockIdx.x / chunks, if one does (a run
 // longer than a segment leaves no room for a second one).
-template <int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
+template <int TT, int V, bool ADD, bool LINES> __global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
   typedef typename Mem<TT>::E ET;
   const int seg = (int)blockIdx.x / a.chunks, chunk = (int)blockIdx.x - seg * a.chunks;
   const int total = a.o.start[a.n_vocab], S = a.segment;
@@ -299,23 +371,23 @@ template <int TT, int V, bool ADD> __global__ __launch_bounds__(kThreads) void j
   const int v = a.o.key[i1 - 1];
   const Run r = run_of(a.o, v);
   if (r.begin < i0 || r.end <= i1 || r.end - r.begin <= S) return;
-  const int col = (chunk * a.chunk_vecs + (int)threadIdx.x) * V, have = a.k - col;
-  if ((int)threadIdx.x >= a.chunk_vecs || have <= 0) return;
-  ET* row = static_cast<ET*>(a.dtable) + (int64_t)v * a.k + col;
+  if ((int)threadIdx.x >= a.chunk_vecs) return;
+  const Place c = place<V>((chunk * a.chunk_vecs + (int)threadIdx.x) * V, a.k);
+  ET* row = static_cast<ET*>(a.dtable) + (int64_t)v * a.k + c.col;
   Vec<TT, V> old{};
-  if constexpr (ADD) old = load<TT, V>(row, have);
+  if constexpr (ADD) old = load<TT, V>(row);
   float sum[V];
-  const Vec<kFp32, V> first = load<kFp32, V>(a.part + ((int64_t)seg * 2 + 1) * a.k + col, have);
+  const Vec<kFp32, V> first = load<kFp32, V>(a.part + ((int64_t)seg * 2 + 1) * a.k + c.col);
 #pragma unroll
   for (int e = 0; e < V; ++e) sum[e] = first[e];
   const int last = (r.end - 1) / S;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = seg + 1; s <= last; ++s) {
-    const Vec<kFp32, V> p = load<kFp32, V>(a.part + (int64_t)s * 2 * a.k + col, have);
+    const Vec<kFp32, V> p = load<kFp32, V>(a.part + (int64_t)s * 2 * a.k + c.col);
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] += p[e];
   }
-  put<TT, V, ADD>(row, have, sum, a.scale, old);
+  put<TT, V, ADD, LINES>(row, c.skip, sum, a.scale, old);
 }
 
 // `words` 16-bit zeros, 16-byte aligned
@@ -342,9 +414,11 @@ Plan plan_of(int64_t m_tok, int64_t n_vocab, int64_t k, int dout_type) {
   if (p.range > kMaxRange) p.range = kMaxRange;
   p.groups = (int)((n_vocab + p.range - 1) / p.range);
   p.vec = dout_type == kFp32 ? 4 : 8;
+  if (k < p.vec) p.vec = 1;
   const int64_t nv = (k + p.vec - 1) / p.vec;
   p.chunks = (int)((nv + kThreads - 1) / kThreads);
-  p.chunk_vecs = (int)((nv + p.chunks - 1) / p.chunks);
+  // whole 128-byte lines to a chunk, whatever the table's type
+  p.chunk_vecs = (int)(((nv + p.chunks - 1) / p.chunks + 15) / 16 * 16);
   // long enough that partial rows are few, short enough that a batch makes a workgroup or two per CU
   p.segment = 64;
   while (p.segment > 8 && (m_tok / p.segment) * p.chunks < 1024) p.segment /= 2;
@@ -364,16 +438,23 @@ Plan plan_of(int64_t m_tok, int64_t n_vocab, int64_t k, int dout_type) {
   return p;
 }
 
-template <int TD, int TT, int V, bool ADD> hipError_t sums(const SumArgs& a, bool join, hipStream_t s) {
-  hipLaunchKernelGGL((sum_kernel<TD, TT, V, ADD>), dim3((unsigned)(a.segments * a.chunks + (ADD ? 0 : a.zero_groups))),
-                     dim3(kThreads), 0, s, a);
+template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const SumArgs& a, bool join, hipStream_t s) {
+  hipLaunchKernelGGL((sum_kernel<TD, TT, V, ADD, LINES>),
+                     dim3((unsigned)(a.segments * a.chunks + (ADD ? 0 : a.zero_groups))), dim3(kThreads), 0, s, a);
   if (join)
-    hipLaunchKernelGGL((join_kernel<TT, V, ADD>), dim3((unsigned)(a.segments * a.chunks)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((join_kernel<TT, V, ADD, LINES>), dim3((unsigned)(a.segments * a.chunks)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
+template <int TD, int TT, int V, bool ADD> hipError_t by_row_length(const SumArgs& a, bool join, hipStream_t s) {
+  if (a.k < V) return sums<TD, TT, 1, ADD, false>(a, join, s);
+  if (a.k * type_bytes(TT) % 128 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 128 == 0)
+    return sums<TD, TT, V, ADD, true>(a, join, s);
+  return sums<TD, TT, V, ADD, false>(a, join, s);
+}
+
 template <int TD, int TT, int V> hipError_t backward(const SumArgs& a, bool add, bool join, hipStream_t s) {
-  return add ? sums<TD, TT, V, true>(a, join, s) : sums<TD, TT, V, false>(a, join, s);
+  return add ? by_row_length<TD, TT, V, true>(a, join, s) : by_row_length<TD, TT, V, false>(a, join, s);
 }
 
 }  // namespace
@@ -401,11 +482,12 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
                 reinterpret_cast<int32_t*>(ws + p.pos)};
   const SortArgs sa{g.ids, (int32_t)g.m_tok, (int32_t)g.n_vocab, p.range, o};
   hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
-  // rows to zero: at least four a wave, and no more than 8 workgroups a CU
-  int64_t zero = (g.n_vocab + 15) / 16;
-  if (zero > 2048) zero = 2048;
+  // rows to zero: a few of each wave, so that there are many waves; at most 64 (the bits of a mask)
+  int64_t zero_rows = 4;
+  while (zero_rows < 64 && g.n_vocab / zero_rows > 8192) zero_rows *= 2;
+  const int64_t zero = (g.n_vocab + zero_rows * 4 - 1) / (zero_rows * 4);
   const SumArgs a{g.dout, g.dtable, (int32_t)g.m_tok, (int32_t)g.n_vocab, g.k, g.scale, p.segment, p.segments, p.chunks,
-                  p.chunk_vecs, (int32_t)zero, o, reinterpret_cast<float*>(ws + p.part)};
+                  p.chunk_vecs, (int32_t)zero, (int32_t)zero_rows, o, reinterpret_cast<float*>(ws + p.part)};
   const bool join = g.m_tok > p.segment;         // else no run is longer than a segment
   if (td == kFp32) {
     if (tt == kBf16) return backward<kFp32, kBf16, 4>(a, g.add, join, s);

@@ -29,6 +29,12 @@ namespace {
 constexpr int V = 4;                             // values per thread and slot
 constexpr int kMaxWaves = 16;
 
+// What is known of the rows of an output when a kernel is compiled.  kLines:
+// they are whole 128-byte lines, and many: stored past the caches (4096 x 5120
+// BF16 to fp32 and int8: 42 -> 32 us; rows that end inside a line would be slower
+// so).  kWhole: also exactly as many values as the threads hold.
+enum Rows { kAny = 0, kLines = 1, kWhole = 2 };
+
 // 1 / sqrt(v) to fp64's precision: v_rsq_f64 (24 bits) and two Newton steps
 __device__ __forceinline__ double rsqrt64(double v) {
   double r = __builtin_amdgcn_rsq(v);
@@ -69,11 +75,20 @@ __device__ __forceinline__ void load_param(const float* p, int col, int have, fl
 #pragma unroll
   for (int j = 0; j < V; ++j) f[j] = p ? v[j] : none;
 }
+template <int W> __device__ __forceinline__ void load_param(const float* p, int col, float none, float (&f)[W]) {
+#pragma unroll
+  for (int j = 0; j < W; ++j) f[j] = none;
+  if (!p) return;
+  const Vec<kFp32, W> v = load<kFp32, W>(p + col);
+#pragma unroll
+  for (int j = 0; j < W; ++j) f[j] = v[j];
+}
 
-// Rows of at most blockDim.x * SLOTS * V values, one workgroup per row and
+// Rows of at most blockDim.x * SLOTS * W values, one workgroup per row and
 // then the row gridDim.x later.
-template <int TX, int TY, int SLOTS>
+template <int TX, int TY, int SLOTS, int W, int ROWS>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
+  constexpr bool WHOLE = ROWS == kWhole;
   typedef typename Mem<TX>::E EX;
   typedef typename Mem<TY>::E EY;
   __shared__ double part[2][2][kMaxWaves];       // of even and odd rows: one barrier per reduction
@@ -82,35 +97,43 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
   const int k = a.k;
   const double inv_k = 1.0 / k;
   const EX* x = static_cast<const EX*>(a.x);
-  int col[SLOTS], have[SLOTS];
-  float w[SLOTS][V], b[SLOTS][V];
+  Place at[SLOTS];
+  float w[SLOTS][W], b[SLOTS][W];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    col[i] = (tid + i * (int)blockDim.x) * V;
-    have[i] = k - col[i];
-    load_param(a.w, col[i], have[i], 1.0f, w[i]);
-    load_param(a.b, col[i], have[i], 0.0f, b[i]);
+    at[i] = place<W>((tid + i * (int)blockDim.x) * W, k);
+    load_param<W>(a.w, at[i].col, 1.0f, w[i]);
+    load_param<W>(a.b, at[i].col, 0.0f, b[i]);
   }
   int64_t row = blockIdx.x;
-  Vec<TX, V> next[SLOTS];
-  EX next0 = x[row * k];
+  Vec<TX, W> next[SLOTS];
+  EX next0;
+  auto fetch = [&] {
+    const EX* p = x + row * k;
+    next0 = p[0];
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, V>(x + row * k + col[i], have[i]);
+    for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, W>(p + at[i].col);
+  };
+  fetch();
   for (int p = 0;; p ^= 1) {
-    const int64_t base = row * k;
-    Vec<TX, V> v[SLOTS];
+    const int64_t now = row, base = row * k;
+    Vec<TX, W> v[SLOTS];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) v[i] = next[i];
     const double x0 = a.center ? (double)to_f32<TX>(next0) : 0.0;
     row += gridDim.x;
-    if (row < a.m_tok) {
-      next0 = x[row * k];
-#pragma unroll
-      for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, V>(x + row * k + col[i], have[i]);
-    }
+    if (row < a.m_tok) fetch();
     double s1 = 0.0, s2 = 0.0;
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) add_stats<TX>(v[i], have[i], x0, s1, s2);
+    for (int i = 0; i < SLOTS; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        double e = (double)v[i][j] - x0;
+        if (!WHOLE) e = j >= at[i].skip ? e : 0.0;
+        s1 += e;
+        s2 = __builtin_fma(e, e, s2);
+      }
+    }
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if ((tid & 63) == 0) {
@@ -126,22 +149,21 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
     }
     const Stat st = statistics(s1, s2, x0, inv_k, a.eps, a.center);
     float mx = 0.0f;
-    float y[SLOTS][V];
+    float y[SLOTS][W];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < W; ++j) {
         y[i][j] = normal(v[i][j], st, w[i][j], b[i][j]);
-        if (j < have[i]) mx = fmaxf(mx, fabsf(y[i][j]));
+        mx = fmaxf(mx, fabsf(y[i][j]));          // a column seen twice does not change the largest
       }
-      if (a.y && have[i] > 0) store<TY, V>(static_cast<EY*>(a.y) + base + col[i], y[i], have[i]);
+      if (a.y) store_own<TY, W, ROWS != kAny>(static_cast<EY*>(a.y) + base + at[i].col, y[i], WHOLE ? 0 : at[i].skip);
     }
-    const int64_t at = base / k;
     if (tid == 0) {
-      if (a.mean) a.mean[at] = (float)st.mean;
-      if (a.rstd) a.rstd[at] = st.rstd;
+      if (a.mean) a.mean[now] = (float)st.mean;
+      if (a.rstd) a.rstd[now] = st.rstd;
     }
-    if (a.xq) {
+    if (W == V && a.xq) {                        // k % 64 == 0: no vector passes the row's end
       mx = wave_max(mx);
       if ((tid & 63) == 0) peak[p][wave] = mx;
       __syncthreads();
@@ -150,10 +172,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
       const actq::Step sp = actq::make_step(g);
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i)
-        if (have[i] > 0)
-          *reinterpret_cast<uint32_t*>(a.xq + base + col[i]) =
-              actq::q_word(float4{y[i][0], y[i][1], y[i][2], y[i][3]}, sp);
-      if (tid == 0) a.gamma[at] = g;
+        if (WHOLE || at[i].skip == 0)
+          *reinterpret_cast<uint32_t*>(a.xq + base + at[i].col) =
+              actq::q_word(float4{y[i][0], y[i][W > 1 ? 1 : 0], y[i][W > 2 ? 2 : 0], y[i][W > 3 ? 3 : 0]}, sp);
+      if (tid == 0) a.gamma[now] = g;
     }
     if (row >= a.m_tok) break;
   }
@@ -235,10 +257,11 @@ __device__ __forceinline__ float grad(float dy, float xh, float w, float rstd, f
   return rstd * (dy * w - c1 - xh * c2);
 }
 
-// Rows of at most blockDim.x * SLOTS * V values, blockDim.x at most MOST.  Every
-// thread keeps the column sums of its own columns over the workgroup's rows.
-template <int TX, int TD, int SLOTS, int MOST>
+// Rows of at most blockDim.x * SLOTS * W values, blockDim.x at most MOST.  Every thread keeps the column sums of its own
+// columns over the workgroup's rows.
+template <int TX, int TD, int SLOTS, int W, int MOST, int ROWS>
 __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, float* part_w, float* part_b) {
+  constexpr bool WHOLE = ROWS == kWhole;
   // weights and the next row in registers too, where 512 / waves per SIMD leaves them
   constexpr bool kHold = SLOTS * MOST <= 2048;
   typedef typename Mem<TX>::E EX;
@@ -249,35 +272,34 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
   const float inv_k = 1.0f / k;
   const EX* x = static_cast<const EX*>(a.x);
   const ED* dy = static_cast<const ED*>(a.dy);
-  int col[SLOTS], have[SLOTS];
-  float w[kHold ? SLOTS : 1][V], sw[SLOTS][V], sb[SLOTS][V];
+  Place at[SLOTS];
+  float w[kHold ? SLOTS : 1][W], sw[SLOTS][W], sb[SLOTS][W];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    col[i] = (tid + i * (int)blockDim.x) * V;
-    have[i] = k - col[i];
-    if constexpr (kHold) load_param(a.w, col[i], have[i], 1.0f, w[i]);
+    at[i] = place<W>((tid + i * (int)blockDim.x) * W, k);
+    if constexpr (kHold) load_param<W>(a.w, at[i].col, 1.0f, w[i]);
 #pragma unroll
-    for (int j = 0; j < V; ++j) sw[i][j] = sb[i][j] = 0.0f;
+    for (int j = 0; j < W; ++j) sw[i][j] = sb[i][j] = 0.0f;
   }
   int64_t row = blockIdx.x;
-  Vec<TX, V> nx[SLOTS];
-  Vec<TD, V> nd[SLOTS];
+  Vec<TX, W> nx[SLOTS];
+  Vec<TD, W> nd[SLOTS];
   float nm = 0.0f, nr;
   auto fetch = [&] {
     nm = a.mean ? a.mean[row] : 0.0f;
     nr = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      nx[i] = load<TX, V>(x + row * k + col[i], have[i]);
-      nd[i] = load<TD, V>(dy + row * k + col[i], have[i]);
+      nx[i] = load<TX, W>(x + row * k + at[i].col);
+      nd[i] = load<TD, W>(dy + row * k + at[i].col);
     }
   };
   fetch();
   for (int p = 0;; p ^= 1) {
     const int64_t base = row * k;
     const float mean = nm, rstd = nr;
-    Vec<TX, V> vx[SLOTS];
-    Vec<TD, V> vd[SLOTS];
+    Vec<TX, W> vx[SLOTS];
+    Vec<TD, W> vd[SLOTS];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       vx[i] = nx[i];
@@ -285,15 +307,16 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
     }
     row += gridDim.x;
     if (kHold && row < a.m_tok) fetch();
-    // values past the row: dy is zero there
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      float(&wi)[V] = w[kHold ? i : 0];
-      if constexpr (!kHold) load_param(a.w, col[i], have[i], 1.0f, wi);
+      float(&wi)[W] = w[kHold ? i : 0];
+      if constexpr (!kHold) load_param<W>(a.w, at[i].col, 1.0f, wi);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float xh = xhat(vx[i][j], mean, rstd), d = vd[i][j], g = d * wi[j];
+      for (int j = 0; j < W; ++j) {
+        const float xh = xhat(vx[i][j], mean, rstd), d = vd[i][j];
+        float g = d * wi[j];
+        if (!WHOLE) g = j >= at[i].skip ? g : 0.0f;
         s1 += g;
         s2 = __builtin_fmaf(g, xh, s2);
         sw[i][j] = __builtin_fmaf(d, xh, sw[i][j]);
@@ -314,13 +337,13 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
       const float c1 = a.center ? s1 * inv_k : 0.0f, c2 = s2 * inv_k;
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i) {
-        float d[V];
-        float(&wi)[V] = w[kHold ? i : 0];
-        if constexpr (!kHold) load_param(a.w, col[i], have[i], 1.0f, wi);
+        float d[W];
+        float(&wi)[W] = w[kHold ? i : 0];
+        if constexpr (!kHold) load_param<W>(a.w, at[i].col, 1.0f, wi);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+        for (int j = 0; j < W; ++j)
           d[j] = grad(vd[i][j], xhat(vx[i][j], mean, rstd), wi[j], rstd, c1, c2);
-        if (have[i] > 0) store<TX, V>(static_cast<EX*>(a.dx) + base + col[i], d, have[i]);
+        store_own<TX, W, ROWS != kAny>(static_cast<EX*>(a.dx) + base + at[i].col, d, WHOLE ? 0 : at[i].skip);
       }
     }
     if (row >= a.m_tok) break;
@@ -328,9 +351,9 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
   }
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    if (have[i] <= 0) continue;
-    if (part_w) store<kFp32, V>(part_w + (int64_t)blockIdx.x * k + col[i], sw[i], have[i]);
-    if (part_b) store<kFp32, V>(part_b + (int64_t)blockIdx.x * k + col[i], sb[i], have[i]);
+    const int skip = WHOLE ? 0 : at[i].skip;
+    if (part_w) store_own<kFp32, W>(part_w + (int64_t)blockIdx.x * k + at[i].col, sw[i], skip);
+    if (part_b) store_own<kFp32, W>(part_b + (int64_t)blockIdx.x * k + at[i].col, sb[i], skip);
   }
 }
 
@@ -433,6 +456,7 @@ __global__ __launch_bounds__(256) void zero_floats_kernel(float* p, int n) {
   for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) p[i] = 0.0f;
 }
 
+constexpr int64_t kStreamBytes = 16 << 20;       // outputs of less stay in the caches
 constexpr int kMaxSlots = 4;                     // rows of up to 1024 * 4 * V values in registers (8 slots spill)
 
 int vectors(int64_t k) { return (int)((k + V - 1) / V); }
@@ -456,6 +480,19 @@ int resident(int threads, int waves_per_simd) {
   return 256 * (per_cu < 1 ? 1 : per_cu);
 }
 
+// the rows of an output of `bytes` in all
+Rows rows_of(const void* out, int64_t k, int64_t bytes, int64_t held, int type) {
+  if (bytes < kStreamBytes || k * type_bytes(type) % 128 != 0 || reinterpret_cast<uintptr_t>(out) % 128 != 0) return kAny;
+  return k == held ? kWhole : kLines;
+}
+
+template <int TX, int TY, int SLOTS> void forward_rows(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
+  const Rows rows = rows_of(a.y, a.k, a.m_tok * a.k * type_bytes(TY), (int64_t)block.x * SLOTS * V, TY);
+  if (rows == kWhole) hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, V, kWhole>), grid, block, 0, s, a);
+  else if (rows == kLines) hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, V, kLines>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, V, kAny>), grid, block, 0, s, a);
+}
+
 template <int TX, int TY> hipError_t forward(const NormArgs& a, hipStream_t s) {
   const int nv = vectors(a.k), slots = slots_for(nv, a.m_tok);
   if (nv > 1024 * kMaxSlots) {
@@ -465,9 +502,10 @@ template <int TX, int TY> hipError_t forward(const NormArgs& a, hipStream_t s) {
   const int threads = threads_for(nv, slots);
   const int64_t most = resident(threads, 4);
   const dim3 grid((unsigned)(a.m_tok < most ? a.m_tok : most)), block((unsigned)threads);
-  if (slots == 1) hipLaunchKernelGGL((norm_kernel<TX, TY, 1>), grid, block, 0, s, a);
-  else if (slots == 2) hipLaunchKernelGGL((norm_kernel<TX, TY, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_kernel<TX, TY, 4>), grid, block, 0, s, a);
+  if (a.k < V) hipLaunchKernelGGL((norm_kernel<TX, TY, 1, 1, kAny>), grid, block, 0, s, a);
+  else if (slots == 1) forward_rows<TX, TY, 1>(a, grid, block, s);
+  else if (slots == 2) forward_rows<TX, TY, 2>(a, grid, block, s);
+  else forward_rows<TX, TY, 4>(a, grid, block, s);
   return hipGetLastError();
 }
 
@@ -489,6 +527,14 @@ GradPlan grad_plan(int64_t m_tok, int64_t k) {
   return p;
 }
 
+template <int TX, int TD, int SLOTS, int MOST>
+void backward_rows(const NormGradArgs& a, float* pw, float* pb, dim3 grid, dim3 block, hipStream_t s) {
+  const Rows rows = rows_of(a.dx, a.k, a.m_tok * a.k * type_bytes(TX), (int64_t)block.x * SLOTS * V, TX);
+  if (rows == kWhole) hipLaunchKernelGGL((norm_grad_kernel<TX, TD, SLOTS, V, MOST, kWhole>), grid, block, 0, s, a, pw, pb);
+  else if (rows == kLines) hipLaunchKernelGGL((norm_grad_kernel<TX, TD, SLOTS, V, MOST, kLines>), grid, block, 0, s, a, pw, pb);
+  else hipLaunchKernelGGL((norm_grad_kernel<TX, TD, SLOTS, V, MOST, kAny>), grid, block, 0, s, a, pw, pb);
+}
+
 template <int TX, int TD> hipError_t backward(const NormGradArgs& a, hipStream_t s) {
   const GradPlan p = grad_plan(a.m_tok, a.k);
   // one share of the rows: its sums are the outputs
@@ -501,14 +547,16 @@ template <int TX, int TD> hipError_t backward(const NormGradArgs& a, hipStream_t
     if (a.dx) hipLaunchKernelGGL((norm_grad_rows_kernel<TX, TD>), dim3((unsigned)a.m_tok), dim3(1024), 0, s, a, means);
     hipLaunchKernelGGL((norm_grad_columns_kernel<TX, TD>), dim3((unsigned)((vectors(a.k) + 255) / 256), (unsigned)p.parts),
                        dim3(256), 0, s, a, means, pw, pb);
+  } else if (a.k < V) {
+    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 1, 1, 1024, kAny>), grid, block, 0, s, a, pw, pb);
   } else if (p.slots == 1) {
-    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 1, 1024>), grid, block, 0, s, a, pw, pb);
+    backward_rows<TX, TD, 1, 1024>(a, pw, pb, grid, block, s);
   } else if (p.slots == 2) {
-    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 2, 1024>), grid, block, 0, s, a, pw, pb);
+    backward_rows<TX, TD, 2, 1024>(a, pw, pb, grid, block, s);
   } else if (p.threads <= 512) {
-    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 4, 512>), grid, block, 0, s, a, pw, pb);
+    backward_rows<TX, TD, 4, 512>(a, pw, pb, grid, block, s);
   } else {
-    hipLaunchKernelGGL((norm_grad_kernel<TX, TD, 4, 1024>), grid, block, 0, s, a, pw, pb);
+    backward_rows<TX, TD, 4, 1024>(a, pw, pb, grid, block, s);
   }
   if (join && (a.dw || a.db))
     hipLaunchKernelGGL(norm_grad_final_kernel, dim3((unsigned)((vectors(a.k) + 15) / 16), 2), dim3(256), 0, s, pw, pb,

@@ -133,6 +133,27 @@ template <int T, int V> struct __attribute__((packed, aligned(sizeof(typename Me
   Vec<T, V> v;
 };
 
+// n bytes at once, past the caches where STREAM (data that nothing reads soon)
+template <int N> struct Words;
+template <> struct Words<4> { typedef uint32_t T __attribute__((aligned(2), may_alias)); };
+template <> struct Words<8> { typedef uint32_t T __attribute__((ext_vector_type(2), aligned(2), may_alias)); };
+template <> struct Words<16> { typedef uint32_t T __attribute__((ext_vector_type(4), aligned(2), may_alias)); };
+template <bool STREAM, class S> __device__ __forceinline__ void put_bytes(void* p, const S& v) {
+  constexpr int N = sizeof(S);
+  if constexpr (!STREAM || N < 4) {
+    __builtin_memcpy(p, &v, N);
+  } else if constexpr (N > 16) {
+    struct Half {
+      uint8_t b[16];
+    } h[N / 16];
+    __builtin_memcpy(h, &v, N);
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) put_bytes<true>(static_cast<uint8_t*>(p) + 16 * i, h[i]);
+  } else {
+    __builtin_nontemporal_store(__builtin_bit_cast(typename Words<N>::T, v), static_cast<typename Words<N>::T*>(p));
+  }
+}
+
 // the V values at p, or its first `have` and zeros
 template <int T, int V>
 __device__ __forceinline__ Vec<T, V> load(const typename Mem<T>::E* p, int have) {
@@ -142,17 +163,53 @@ __device__ __forceinline__ Vec<T, V> load(const typename Mem<T>::E* p, int have)
   for (int i = 0; i < V; ++i) v.e[i] = i < have ? p[i] : (typename Mem<T>::E)0;
   return v;
 }
-template <int T, int V>
+template <int T, int V, bool STREAM = false>
 __device__ __forceinline__ void store(typename Mem<T>::E* p, const float (&f)[V], int have) {
   if (have >= V) {
-    Loose<T, V> o;
+    Vec<T, V> o;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o.v.e[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<Loose<T, V>*>(p) = o;
+    for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(f[i]);
+    if constexpr (STREAM) put_bytes<true>(p, o);
+    else reinterpret_cast<Loose<T, V>*>(p)->v = o;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i < have) p[i] = from_f32<T>(f[i]);
+  }
+}
+
+// Where a thread's V columns of a row of k >= V lie.  The vector that would
+// pass the row's end (and those that begin past it) is moved back to end with
+// the row, so that every load is a whole one, without a branch: its first
+// `skip` columns are another thread's too (all of them where skip >= V).
+struct Place {
+  int col, skip;
+};
+template <int V> __device__ __forceinline__ Place place(int col, int k) {
+  const int at = col < k - V ? col : k - V;
+  return Place{at, col - at};
+}
+template <int T, int V> __device__ __forceinline__ Vec<T, V> load_once(const typename Mem<T>::E* p) {
+  constexpr int N = sizeof(Vec<T, V>) > 16 ? 16 : sizeof(Vec<T, V>);
+  Vec<T, V> v;
+  typename Words<N>::T w[sizeof(v) / N];
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(v) / N); ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const typename Words<N>::T*>(p) + i);
+  __builtin_memcpy(&v, w, sizeof(v));
+  return v;
+}
+template <int T, int V> __device__ __forceinline__ Vec<T, V> load(const typename Mem<T>::E* p) {
+  return reinterpret_cast<const Loose<T, V>*>(p)->v;
+}
+// the columns that are this thread's own
+template <int T, int V, bool STREAM = false>
+__device__ __forceinline__ void store_own(typename Mem<T>::E* p, const float (&f)[V], int skip) {
+  if (skip == 0) {
+    store<T, V, STREAM>(p, f, V);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i >= skip) p[i] = from_f32<T>(f[i]);
   }
 }
 
