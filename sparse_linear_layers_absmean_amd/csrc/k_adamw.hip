@@ -33,14 +33,15 @@ namespace step {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;                     // values per workgroup
+constexpr int kMostChunk = 8192;                 // values per workgroup, where that leaves every CU a few
+constexpr int kLeastChunk = 2048;                // one round of 256 threads (8-bit states: 8 values each)
 constexpr int kMaxItems = 40;                    // of one launch: their descriptors are its arguments (< 4 KB)
 
 struct AdamBatch {
   AdamItem item[kMaxItems];
   uint32_t start[kMaxItems];                     // first workgroup of each item
   AdamStep step;
-  int32_t count;
+  int32_t count, chunk;
 };
 static_assert(sizeof(AdamBatch) <= 4096, "kernel arguments");
 
@@ -119,9 +120,10 @@ __device__ __forceinline__ float max32(float x) {
 template <int TW, bool LOW, int V>
 __device__ __forceinline__ void load_w(const AdamItem& it, int64_t i, int have, float (&w)[V]) {
   typedef typename Mem<TW>::E E;
-  const Vec<TW, V> v = load<TW, V>(static_cast<const E*>(it.w) + i, have);
+  const Vec<TW, V> v = have >= V ? load_once<TW, V>(static_cast<const E*>(it.w) + i) : load<TW, V>(static_cast<const E*>(it.w) + i, have);
   if constexpr (LOW) {
-    const Vec<kBf16, V> l = load<kBf16, V>(reinterpret_cast<const uint16_t*>(it.low) + i, have);
+    const uint16_t* pl = reinterpret_cast<const uint16_t*>(it.low) + i;
+    const Vec<kBf16, V> l = have >= V ? load_once<kBf16, V>(pl) : load<kBf16, V>(pl, have);
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] = join(v.e[j], (int16_t)l.e[j]);
   } else {
@@ -142,8 +144,8 @@ __device__ __forceinline__ void store_w(const AdamItem& it, int64_t i, int have,
     }
     uint16_t *ph = static_cast<uint16_t*>(it.w) + i, *pl = reinterpret_cast<uint16_t*>(it.low) + i;
     if (have >= V) {
-      *reinterpret_cast<Loose<kBf16, V>*>(ph) = h;
-      *reinterpret_cast<Loose<kBf16, V>*>(pl) = l;
+      put_bytes<true>(ph, h.v);
+      put_bytes<true>(pl, l.v);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -153,22 +155,30 @@ __device__ __forceinline__ void store_w(const AdamItem& it, int64_t i, int have,
         }
     }
   } else {
-    store<TW, V>(static_cast<E*>(it.w) + i, w, have);
+    store<TW, V, true>(static_cast<E*>(it.w) + i, w, have);
   }
 }
 
-// values [first, first + kChunk) of a tensor whose states have 32 bits
-template <int TW, bool LOW, int TG> __device__ void chunk32(const AdamItem& it, int64_t first, const Factors& f) {
+// values [first, first + chunk) of a tensor whose states have 32 bits
+template <int TW, bool LOW, int TG> __device__ void chunk32(const AdamItem& it, int64_t first, int chunk, const Factors& f) {
   constexpr int V = 4;
   const int64_t left = it.n - first;
-  for (int at = threadIdx.x * V; at < kChunk && at < left; at += kThreads * V) {
+  for (int at = threadIdx.x * V; at < chunk && at < left; at += kThreads * V) {
     const int64_t i = first + at;
     const int have = left - at < V ? (int)(left - at) : V;
     float w[V], mf[V], vf[V];
     load_w<TW, LOW, V>(it, i, have, w);
-    const Vec<TG, V> g = load<TG, V>(static_cast<const typename Mem<TG>::E*>(it.g) + i, have);
-    const Vec<kFp32, V> m = load<kFp32, V>(static_cast<const float*>(it.m) + i, have);
-    const Vec<kFp32, V> v = load<kFp32, V>(static_cast<const float*>(it.v) + i, have);
+    Vec<TG, V> g;
+    Vec<kFp32, V> m, v;
+    if (have >= V) {
+      g = load_once<TG, V>(static_cast<const typename Mem<TG>::E*>(it.g) + i);
+      m = load_once<kFp32, V>(static_cast<const float*>(it.m) + i);
+      v = load_once<kFp32, V>(static_cast<const float*>(it.v) + i);
+    } else {
+      g = load<TG, V>(static_cast<const typename Mem<TG>::E*>(it.g) + i, have);
+      m = load<kFp32, V>(static_cast<const float*>(it.m) + i, have);
+      v = load<kFp32, V>(static_cast<const float*>(it.v) + i, have);
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       mf[j] = m[j];
@@ -176,17 +186,17 @@ template <int TW, bool LOW, int TG> __device__ void chunk32(const AdamItem& it, 
       update(w[j], g[j], mf[j], vf[j], f);
     }
     store_w<TW, LOW, V>(it, i, have, w);
-    store<kFp32, V>(static_cast<float*>(it.m) + i, mf, have);
-    store<kFp32, V>(static_cast<float*>(it.v) + i, vf, have);
+    store<kFp32, V, true>(static_cast<float*>(it.m) + i, mf, have);
+    store<kFp32, V, true>(static_cast<float*>(it.v) + i, vf, have);
   }
 }
 
 // the same with states in 8 bits: 8 values a lane, 32 lanes a block
-template <int TW, bool LOW, int TG> __device__ void chunk8(const AdamItem& it, int64_t first, const Factors& f) {
+template <int TW, bool LOW, int TG> __device__ void chunk8(const AdamItem& it, int64_t first, int chunk, const Factors& f) {
   constexpr int V = 8;
   const int64_t left = it.n - first;
   uint8_t *cm = static_cast<uint8_t*>(it.m), *cv = static_cast<uint8_t*>(it.v);
-  for (int at = threadIdx.x * V; at < kChunk; at += kThreads * V) {
+  for (int at = threadIdx.x * V; at < chunk; at += kThreads * V) {
     const int64_t i = first + at, block = i >> 8;
     const int have = left - at <= 0 ? 0 : left - at < V ? (int)(left - at) : V;
     if ((at & ~255) >= left) continue;             // whole blocks past the end
@@ -260,15 +270,16 @@ template <int TW, bool LOW, int TG> __device__ void chunk8(const AdamItem& it, i
 }
 
 template <int TW, bool LOW, int TG>
-__device__ __forceinline__ void chunk(const AdamItem& it, int64_t first, const Factors& f) {
-  if (it.bits == 8) chunk8<TW, LOW, TG>(it, first, f);
-  else chunk32<TW, LOW, TG>(it, first, f);
+__device__ __forceinline__ void by_states(const AdamItem& it, int64_t first, int chunk, const Factors& f) {
+  if (it.bits == 8) chunk8<TW, LOW, TG>(it, first, chunk, f);
+  else chunk32<TW, LOW, TG>(it, first, chunk, f);
 }
-template <int TW, bool LOW> __device__ __forceinline__ void by_gradient(const AdamItem& it, int64_t first, const Factors& f) {
+template <int TW, bool LOW>
+__device__ __forceinline__ void by_gradient(const AdamItem& it, int64_t first, int chunk, const Factors& f) {
   const int tg = it.kind / 3;
-  if (tg == kFp32) chunk<TW, LOW, kFp32>(it, first, f);
-  else if (tg == kBf16) chunk<TW, LOW, kBf16>(it, first, f);
-  else chunk<TW, LOW, kFp16>(it, first, f);
+  if (tg == kFp32) by_states<TW, LOW, kFp32>(it, first, chunk, f);
+  else if (tg == kBf16) by_states<TW, LOW, kBf16>(it, first, chunk, f);
+  else by_states<TW, LOW, kFp16>(it, first, chunk, f);
 }
 
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamBatch a) {
@@ -281,12 +292,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamBatch a) {
   const float lr = t.lr * it.lr_scale;
   const Factors f{a.step.b1, a.step.a1, a.step.b2, a.step.a2, a.step.eps, lr * t.bias1, 1.0f - lr * it.weight_decay,
                   t.bias2, t.factor, (uint32_t)t.seed};
-  const int64_t first = (int64_t)(blockIdx.x - a.start[i]) * kChunk;
+  const int64_t first = (int64_t)(blockIdx.x - a.start[i]) * a.chunk;
   const int tw = it.kind % 3;
-  if (tw == kFp32) by_gradient<kFp32, false>(it, first, f);
-  else if (tw == kFp16) by_gradient<kFp16, false>(it, first, f);
-  else if (it.low) by_gradient<kBf16, true>(it, first, f);
-  else by_gradient<kBf16, false>(it, first, f);
+  if (tw == kFp32) by_gradient<kFp32, false>(it, first, a.chunk, f);
+  else if (tw == kFp16) by_gradient<kFp16, false>(it, first, a.chunk, f);
+  else if (it.low) by_gradient<kBf16, true>(it, first, a.chunk, f);
+  else by_gradient<kBf16, false>(it, first, a.chunk, f);
 }
 
 }  // namespace
@@ -294,6 +305,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamBatch a) {
 hipError_t launch_adamw(const AdamItem* items, int count, const AdamStep& step, hipStream_t s) {
   AdamBatch b{};
   b.step = step;
+  int64_t all = 0;
+  for (int i = 0; i < count; ++i) all += items[i].n;
+  // small models: a workgroup's rounds follow each other, more workgroups do not
+  b.chunk = all >= (int64_t)1024 * kMostChunk ? kMostChunk : kLeastChunk;
   uint32_t groups = 0;
   auto run = [&] {
     if (groups == 0) return hipSuccess;
@@ -303,7 +318,7 @@ hipError_t launch_adamw(const AdamItem* items, int count, const AdamStep& step, 
     return hipGetLastError();
   };
   for (int i = 0; i < count; ++i) {
-    const int64_t need = (items[i].n + kChunk - 1) / kChunk;
+    const int64_t need = (items[i].n + b.chunk - 1) / b.chunk;
     if (need == 0) continue;
     // a grid holds fewer than 2^32 threads
     if (b.count == kMaxItems || (int64_t)groups + need > (int64_t(1) << 32) / kThreads - 1) {

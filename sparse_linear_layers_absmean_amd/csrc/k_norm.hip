@@ -18,6 +18,8 @@
 // loads are in flight while a row is reduced, and the backward's column sums
 // need no memory until the end (one partial row per workgroup, joined in a
 // fixed order by a second launch).
+#include <algorithm>
+
 #include "sbl_actq.h"
 #include "sbl_step.h"
 
@@ -32,7 +34,7 @@ constexpr int kMaxWaves = 16;
 // What is known of the rows of an output when a kernel is compiled.  kLines:
 // they are whole 128-byte lines, and many: stored past the caches (4096 x 5120
 // BF16 to fp32 and int8: 42 -> 32 us; rows that end inside a line would be slower
-// so).  kWhole: also exactly as many values as the threads hold.
+// so; loads past the caches as well: 42 us, an input is often there still).  kWhole: also exactly as many values as the threads hold.
 enum Rows { kAny = 0, kLines = 1, kWhole = 2 };
 
 // 1 / sqrt(v) to fp64's precision: v_rsq_f64 (24 bits) and two Newton steps
@@ -421,18 +423,21 @@ __global__ __launch_bounds__(256) void norm_grad_columns_kernel(const NormGradAr
   if (part_b) store<kFp32, V>(part_b + (int64_t)blockIdx.y * k + col, sb, have);
 }
 
-// out[c] = sum over the partial rows, in ascending order within each of 16
-// shares, then share by share.  blockIdx.y: 0 the weight, 1 the bias.
+// out[c] = sum over the partial rows, in ascending order within each of 256 / L
+// shares, then share by share; L lanes side by side.  blockIdx.y: 0 the weight, 1
+// the bias.
+template <int L>
 __global__ __launch_bounds__(256) void norm_grad_final_kernel(const float* part_w, const float* part_b, int rows, int k,
                                                               float* dw, float* db) {
-  __shared__ float sum[16][16][V];
+  constexpr int kShares = 256 / L;
+  __shared__ float sum[kShares][L][V];
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;
-  const int lane = threadIdx.x & 15, share = threadIdx.x >> 4;
-  const int col = (blockIdx.x * 16 + lane) * V, have = k - col;
+  const int lane = threadIdx.x % L, share = threadIdx.x / L;
+  const int col = (blockIdx.x * L + lane) * V, have = k - col;
   float s[V] = {};
-  const int per = (rows + 15) / 16, r1 = min(rows, (share + 1) * per);
+  const int per = (rows + kShares - 1) / kShares, r1 = min(rows, (share + 1) * per);
   if (have > 0) {
 #pragma unroll 8
     for (int r = share * per; r < r1; ++r) {
@@ -445,8 +450,8 @@ __global__ __launch_bounds__(256) void norm_grad_final_kernel(const float* part_
   for (int j = 0; j < V; ++j) sum[share][lane][j] = s[j];
   __syncthreads();
   if (share != 0 || have <= 0) return;
-#pragma unroll
-  for (int r = 1; r < 16; ++r)
+#pragma unroll 16
+  for (int r = 1; r < kShares; ++r)
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] += sum[r][lane][j];
   store<kFp32, V>(out + col, s, have);
@@ -457,6 +462,7 @@ __global__ __launch_bounds__(256) void zero_floats_kernel(float* p, int n) {
 }
 
 constexpr int64_t kStreamBytes = 16 << 20;       // outputs of less stay in the caches
+constexpr int kWideFinal = 1024;
 constexpr int kMaxSlots = 4;                     // rows of up to 1024 * 4 * V values in registers (8 slots spill)
 
 int vectors(int64_t k) { return (int)((k + V - 1) / V); }
@@ -523,7 +529,10 @@ GradPlan grad_plan(int64_t m_tok, int64_t k) {
   } else {
     p.parts = 2048 / ((nv + 255) / 256);         // 8 workgroups a CU over the columns and the rows' shares
   }
-  if (p.parts > m_tok) p.parts = m_tok;
+  // narrow rows: a part takes 8 of them at least, so that joining the parts does not cost more than the rows;
+  // the first few rows: one part, and no second launch
+  const int64_t most = m_tok <= 4 ? 1 : m_tok < 4096 ? m_tok : std::max<int64_t>(512, m_tok / 8);
+  if (p.parts > most) p.parts = most;
   return p;
 }
 
@@ -558,9 +567,15 @@ template <int TX, int TD> hipError_t backward(const NormGradArgs& a, hipStream_t
   } else {
     backward_rows<TX, TD, 4, 1024>(a, pw, pb, grid, block, s);
   }
-  if (join && (a.dw || a.db))
-    hipLaunchKernelGGL(norm_grad_final_kernel, dim3((unsigned)((vectors(a.k) + 15) / 16), 2), dim3(256), 0, s, pw, pb,
-                       (int)p.parts, a.k, a.dw, a.db);
+  if (join && (a.dw || a.db)) {
+    const int nv = vectors(a.k);
+    if (nv < kWideFinal)                         // few columns: more shares of the parts
+      hipLaunchKernelGGL(norm_grad_final_kernel<4>, dim3((unsigned)((nv + 3) / 4), 2), dim3(256), 0, s, pw, pb, (int)p.parts,
+                         a.k, a.dw, a.db);
+    else
+      hipLaunchKernelGGL(norm_grad_final_kernel<16>, dim3((unsigned)((nv + 15) / 16), 2), dim3(256), 0, s, pw, pb,
+                         (int)p.parts, a.k, a.dw, a.db);
+  }
   return hipGetLastError();
 }
 

@@ -189,17 +189,22 @@ template <int V> __device__ __forceinline__ Place place(int col, int k) {
   const int at = col < k - V ? col : k - V;
   return Place{at, col - at};
 }
-template <int T, int V> __device__ __forceinline__ Vec<T, V> load_once(const typename Mem<T>::E* p) {
-  constexpr int N = sizeof(Vec<T, V>) > 16 ? 16 : sizeof(Vec<T, V>);
-  Vec<T, V> v;
-  typename Words<N>::T w[sizeof(v) / N];
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(v) / N); ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const typename Words<N>::T*>(p) + i);
-  __builtin_memcpy(&v, w, sizeof(v));
-  return v;
-}
 template <int T, int V> __device__ __forceinline__ Vec<T, V> load(const typename Mem<T>::E* p) {
   return reinterpret_cast<const Loose<T, V>*>(p)->v;
+}
+// the same, past the caches: values that are read once
+template <int T, int V> __device__ __forceinline__ Vec<T, V> load_once(const typename Mem<T>::E* p) {
+  constexpr int all = sizeof(Vec<T, V>), N = all > 16 ? 16 : all;
+  if constexpr (N < 4) {
+    return load<T, V>(p);
+  } else {
+    typename Words<N>::T w[all / N];
+#pragma unroll
+    for (int i = 0; i < all / N; ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const typename Words<N>::T*>(p) + i);
+    Vec<T, V> v;
+    __builtin_memcpy(&v, w, all);
+    return v;
+  }
 }
 // the columns that are this thread's own
 template <int T, int V, bool STREAM = false>

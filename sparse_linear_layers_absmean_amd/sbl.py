@@ -636,26 +636,27 @@ _TYPES = {torch.bfloat16: SBL_BF16, torch.float16: SBL_FP16, torch.float32: SBL_
 
 
 def _type(t, name: str) -> int:
-    if t.dtype not in _TYPES:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_TYPES)}")
-    return _TYPES[t.dtype]
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_TYPES)}") from None
 
 
-def _here(t, dtype, shape, name: str):
-    """Device pointer of a contiguous tensor of this shape on the current GPU, or None."""
+def _here(t, dtype, shape, name: str, device: int):
+    """Device pointer of a contiguous tensor of this shape on the current GPU (`device`), or None."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on the current GPU")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() if t.numel() else None
+    return t.data_ptr()
 
 
 def _rows(t, name: str):
@@ -675,13 +676,16 @@ def sbl_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, center: bool 
                      mean=None, rstd=None, stream=None):
     """Layer norm (center) or RMS norm of the rows of x [m_tok][k] -> y (x's type or fp32) and/or its
     int8 codes xq with gamma; mean, rstd fp32 [m_tok] for the backward.  Every output may be None."""
-    m_tok, k = _rows(x, "x")
-    f32 = torch.float32
-    _check("sbl_norm_forward", load().sbl_norm_forward(
-        _here(x, None, (m_tok, k), "x"), _type(x, "x"), _here(weight, f32, (k,), "weight"), _here(bias, f32, (k,), "bias"),
-        m_tok, k, eps, int(center), _here(y, None, (m_tok, k), "y"), _type(y if y is not None else x, "y"),
-        _here(xq, torch.int8, (m_tok, k), "xq"), _here(gamma, f32, (m_tok,), "gamma"), _here(mean, f32, (m_tok,), "mean"),
-        _here(rstd, f32, (m_tok,), "rstd"), _stream(stream)))
+    m_tok, k = rows = _rows(x, "x")
+    f32, device, row, col = torch.float32, torch.cuda.current_device(), (m_tok,), (k,)
+    st = load().sbl_norm_forward(
+        _here(x, None, rows, "x", device), _type(x, "x"), _here(weight, f32, col, "weight", device),
+        _here(bias, f32, col, "bias", device), m_tok, k, eps, center, _here(y, None, rows, "y", device),
+        _type(y if y is not None else x, "y"), _here(xq, torch.int8, rows, "xq", device),
+        _here(gamma, f32, row, "gamma", device), _here(mean, f32, row, "mean", device),
+        _here(rstd, f32, row, "rstd", device), _stream(stream))
+    if st != SBL_OK:
+        raise SblError("sbl_norm_forward", st)
 
 
 def sbl_norm_workspace_bytes(m_tok: int, k: int) -> int:
@@ -691,29 +695,31 @@ def sbl_norm_workspace_bytes(m_tok: int, k: int) -> int:
 def sbl_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, center: bool = True, stream=None):
     """Gradients of the norm from dy [m_tok][k] (x's type or fp32): dx in x's type, dweight and dbias fp32 [k]
     (each may be None).  mean may be None where not centered."""
-    m_tok, k = _rows(x, "x")
-    f32 = torch.float32
+    m_tok, k = rows = _rows(x, "x")
+    f32, device, row, col = torch.float32, torch.cuda.current_device(), (m_tok,), (k,)
     _check("sbl_norm_backward", load().sbl_norm_backward(
-        _here(dy, None, (m_tok, k), "dy"), _type(dy, "dy"), _here(x, None, (m_tok, k), "x"), _type(x, "x"),
-        _here(mean, f32, (m_tok,), "mean"), _here(rstd, f32, (m_tok,), "rstd"), _here(weight, f32, (k,), "weight"), m_tok, k,
-        int(center), _here(dx, x.dtype, (m_tok, k), "dx"), _here(dweight, f32, (k,), "dweight"),
-        _here(dbias, f32, (k,), "dbias"), *_scratch(workspace), _stream(stream)))
+        _here(dy, None, rows, "dy", device), _type(dy, "dy"), _here(x, None, rows, "x", device), _type(x, "x"),
+        _here(mean, f32, row, "mean", device), _here(rstd, f32, row, "rstd", device),
+        _here(weight, f32, col, "weight", device), m_tok, k, center, _here(dx, x.dtype, rows, "dx", device),
+        _here(dweight, f32, col, "dweight", device), _here(dbias, f32, col, "dbias", device), *_scratch(workspace),
+        _stream(stream)))
 
 
 def _ids(ids):
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")
-    return _here(ids, torch.int64, tuple(ids.shape), "ids"), ids.numel()
+    device = torch.cuda.current_device()
+    return _here(ids, torch.int64, ids.shape, "ids", device), ids.numel(), device
 
 
 def sbl_embed_forward(ids, table, out, scale: float = 1.0, stream=None):
     """out[t] = scale * table[ids[t]]: ids int64 of any shape, table [n_vocab][k], out [ids' shape][k] in the
     table's type or fp32.  A negative id gives zeros, an id past the table NaNs."""
-    n_vocab, k = _rows(table, "table")
-    at, m_tok = _ids(ids)
+    n_vocab, k = rows = _rows(table, "table")
+    at, m_tok, device = _ids(ids)
     _check("sbl_embed_forward", load().sbl_embed_forward(
-        at, _here(table, None, (n_vocab, k), "table"), _type(table, "table"), m_tok, n_vocab, k, scale,
-        _here(out, None, (*ids.shape, k), "out"), _type(out, "out"), _stream(stream)))
+        at, _here(table, None, rows, "table", device), _type(table, "table"), m_tok, n_vocab, k, scale,
+        _here(out, None, (*ids.shape, k), "out", device), _type(out, "out"), _stream(stream)))
 
 
 def sbl_embed_workspace_bytes(m_tok: int, n_vocab: int, k: int, dtype=torch.bfloat16) -> int:
@@ -724,11 +730,11 @@ def sbl_embed_workspace_bytes(m_tok: int, n_vocab: int, k: int, dtype=torch.bflo
 def sbl_embed_backward(ids, dout, dtable, workspace, scale: float = 1.0, add: bool = False, stream=None):
     """Gradient of the table from dout [ids' shape][k] (the table's type or fp32): written to dtable
     [n_vocab][k], or added to what it holds."""
-    n_vocab, k = _rows(dtable, "dtable")
-    at, m_tok = _ids(ids)
+    n_vocab, k = rows = _rows(dtable, "dtable")
+    at, m_tok, device = _ids(ids)
     _check("sbl_embed_backward", load().sbl_embed_backward(
-        at, _here(dout, None, (*ids.shape, k), "dout"), _type(dout, "dout"), m_tok, n_vocab, k, scale,
-        _here(dtable, None, (n_vocab, k), "dtable"), _type(dtable, "dtable"), int(add), *_scratch(workspace),
+        at, _here(dout, None, (*ids.shape, k), "dout", device), _type(dout, "dout"), m_tok, n_vocab, k, scale,
+        _here(dtable, None, rows, "dtable", device), _type(dtable, "dtable"), add, *_scratch(workspace),
         _stream(stream)))
 
 
@@ -789,11 +795,12 @@ def sbl_adamw_batch(items, lr: float, beta1: float, beta2: float, eps: float, st
     [5] on the GPU (adamw_schedule), read in place of lr and step when the step runs."""
     if not isinstance(items, AdamWItems):
         items = AdamWItems(items)
-    if items.device.index != torch.cuda.current_device():
+    device = torch.cuda.current_device()
+    if items.device.index != device:
         raise ValueError("the tensors must be on the current GPU")
     _check("sbl_adamw_batch", load().sbl_adamw_batch(
-        items.array, len(items.tensors), lr, beta1, beta2, eps, step, _here(schedule, torch.float32, (5,), "schedule"),
-        _stream(stream)))
+        items.array, len(items.tensors), lr, beta1, beta2, eps, step,
+        _here(schedule, torch.float32, (5,), "schedule", device), _stream(stream)))
 
 
 # ---------------------------------------------------------------- allocating conveniences
@@ -930,16 +937,31 @@ def _like(x, dtype, name: str):
     return dtype if dtype is not None else x.dtype
 
 
+def _norm_out(x, weight, bias, eps, center, y, quant: bool):
+    """Run sbl_norm_forward on outputs made here, which need no checks: (xq or None, [mean, rstd, and with xq gamma])."""
+    m_tok, k = rows = _rows(x, "x")
+    device, where = torch.cuda.current_device(), x.device
+    at, x_type = _here(x, None, rows, "x", device), _type(x, "x")
+    w, b = _here(weight, torch.float32, (k,), "weight", device), _here(bias, torch.float32, (k,), "bias", device)
+    stat = torch.empty((3 if quant else 2, m_tok), dtype=torch.float32, device=where)
+    xq = torch.empty(rows, dtype=torch.int8, device=where) if quant else None
+    p = stat.data_ptr()
+    st = load().sbl_norm_forward(
+        at, x_type, w, b, m_tok, k, eps, center, y.data_ptr() if y is not None else None,
+        _TYPES[y.dtype] if y is not None else x_type, xq.data_ptr() if quant else None, p + 8 * m_tok if quant else None,
+        p, p + 4 * m_tok, _stream(None))
+    if st != SBL_OK:
+        raise SblError("sbl_norm_forward", st)
+    return xq, stat
+
+
 def norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, dtype=None, stream=None):
     """Allocate outputs and run sbl_norm_forward; returns (y, mean, rstd), y in x's type or float32."""
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return norm(x, weight, bias, eps, center, dtype)
-    m_tok, k = _rows(x, "x")
-    y = torch.empty((m_tok, k), dtype=_like(x, dtype, "dtype"), device=x.device)
-    mean = torch.empty(m_tok, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(m_tok, dtype=torch.float32, device=x.device)
-    sbl_norm_forward(x, weight, bias, eps, center, y=y, mean=mean, rstd=rstd)
+    y = torch.empty(_rows(x, "x"), dtype=_like(x, dtype, "dtype"), device=x.device)
+    mean, rstd = _norm_out(x, weight, bias, eps, center, y, False)[1]
     return y, mean, rstd
 
 
@@ -950,11 +972,9 @@ def norm_quant(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return norm_quant(x, weight, bias, eps, center, dtype, want_y)
-    m_tok, k = _rows(x, "x")
-    y = torch.empty((m_tok, k), dtype=_like(x, dtype, "dtype"), device=x.device) if want_y else None
-    xq = torch.empty((m_tok, k), dtype=torch.int8, device=x.device)
-    gamma, mean, rstd = torch.empty((3, m_tok), dtype=torch.float32, device=x.device).unbind(0)
-    sbl_norm_forward(x, weight, bias, eps, center, y=y, xq=xq, gamma=gamma, mean=mean, rstd=rstd)
+    y = torch.empty(_rows(x, "x"), dtype=_like(x, dtype, "dtype"), device=x.device) if want_y else None
+    xq, stat = _norm_out(x, weight, bias, eps, center, y, True)
+    mean, rstd, gamma = stat
     return xq, gamma, y, mean, rstd
 
 
