@@ -74,8 +74,8 @@ __device__ __forceinline__ void split(float w, uint16_t& high, int16_t& low) {
 
 // 16 bits each for values 2 pair and 2 pair + 1: the low and high half of a
 // hash of the pair's number (two rounds of xor-shift and multiply)
-__device__ __forceinline__ uint32_t dither(uint64_t pair, uint32_t seed) {
-  uint32_t h = (uint32_t)pair * 0x9E3779B9u + seed;
+constexpr uint32_t kNextPair = 0x9E3779B9u;      // what pair + 1 adds to pair * kNextPair + seed
+__device__ __forceinline__ uint32_t dither(uint32_t h) {
   h ^= h >> 16;
   h *= 0x7FEB352Du;
   h ^= h >> 15;
@@ -237,11 +237,12 @@ template <int TW, bool LOW, int TG> __device__ void chunk8(const AdamItem& it, i
     sm = scale_of(max32(am));
     sv = scale_of(max32(av));
     const float rm = 1.0f / sm, rv = 1.0f / sv;
+    const uint32_t pair = (uint32_t)(i >> 1) * kNextPair + f.seed;
 #pragma unroll
     for (int j = 0; j < V; j += 2) {
-      const uint32_t d = dither((uint64_t)(i + j) >> 1, f.seed);
-      mf[j] = fminf(fmaxf(mf[j] * rm, -448.0f), 448.0f);
-      mf[j + 1] = fminf(fmaxf(mf[j + 1] * rm, -448.0f), 448.0f);
+      const uint32_t d = dither(pair + (uint32_t)(j / 2) * kNextPair);
+      mf[j] = mf[j] * rm;
+      mf[j + 1] = mf[j + 1] * rm;
       const float lo = fminf(fmaxf(cut_e4m3(root[j] * rv, d & 0xFFFFu), 0x1p-9f), 448.0f);
       const float hi = fminf(fmaxf(cut_e4m3(root[j + 1] * rv, d >> 16), 0x1p-9f), 448.0f);
       root[j] = root[j] > 0.0f ? lo : 0.0f;

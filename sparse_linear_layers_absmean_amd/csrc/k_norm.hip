@@ -589,6 +589,7 @@ hipError_t launch_norm_forward(const NormArgs& a, int tx, int ty, hipStream_t s)
 
 // partial rows of both column sums; long rows: two means per row, 8-byte aligned
 int64_t norm_grad_ws_bytes(int64_t m_tok, int64_t k) {
+  if (m_tok == 0) return 0;
   const GradPlan p = grad_plan(m_tok, k);
   return (2 * p.parts * k * 4 + (p.slots == 0 ? m_tok * 8 : 0) + 255) / 256 * 256;
 }

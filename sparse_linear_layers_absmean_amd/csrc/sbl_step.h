@@ -116,9 +116,16 @@ template <int T> __device__ __forceinline__ float to_f32(typename Mem<T>::E e) {
 }
 // one rounding to nearest, ties to even (fp32: none)
 template <int T> __device__ __forceinline__ typename Mem<T>::E from_f32(float f) {
-  if constexpr (T == kBf16) return __builtin_bit_cast(uint16_t, (__bf16)f);
-  else if constexpr (T == kFp16) return __builtin_bit_cast(uint16_t, (_Float16)f);
-  else return f;
+  if constexpr (T == kBf16) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+  } else if constexpr (T == kFp16) {
+    // f as an fp32 number first: else a product and its rounding to FP16 become one
+    // instruction with one rounding (v_fma_mixlo_f16)
+    asm("" : "+v"(f));
+    return __builtin_bit_cast(uint16_t, (_Float16)f);
+  } else {
+    return f;
+  }
 }
 
 // V consecutive values held as they lie in memory.  Rows of an odd number of

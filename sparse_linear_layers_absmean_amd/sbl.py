@@ -667,9 +667,11 @@ def _rows(t, name: str):
     return t.shape
 
 
-def _scratch(t, name: str = "workspace"):
+def _scratch(t, device: int):
     """(pointer, bytes) of a workspace."""
-    return (_ptr(t, None, 0, name), _nbytes(t)) if t is not None else (None, 0)
+    if t is None:
+        return None, 0
+    return _here(t, None, t.shape, "workspace", device), _nbytes(t)
 
 
 def sbl_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, y=None, xq=None, gamma=None,
@@ -701,7 +703,7 @@ def sbl_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, 
         _here(dy, None, rows, "dy", device), _type(dy, "dy"), _here(x, None, rows, "x", device), _type(x, "x"),
         _here(mean, f32, row, "mean", device), _here(rstd, f32, row, "rstd", device),
         _here(weight, f32, col, "weight", device), m_tok, k, center, _here(dx, x.dtype, rows, "dx", device),
-        _here(dweight, f32, col, "dweight", device), _here(dbias, f32, col, "dbias", device), *_scratch(workspace),
+        _here(dweight, f32, col, "dweight", device), _here(dbias, f32, col, "dbias", device), *_scratch(workspace, device),
         _stream(stream)))
 
 
@@ -734,7 +736,7 @@ def sbl_embed_backward(ids, dout, dtable, workspace, scale: float = 1.0, add: bo
     at, m_tok, device = _ids(ids)
     _check("sbl_embed_backward", load().sbl_embed_backward(
         at, _here(dout, None, (*ids.shape, k), "dout", device), _type(dout, "dout"), m_tok, n_vocab, k, scale,
-        _here(dtable, None, rows, "dtable", device), _type(dtable, "dtable"), add, *_scratch(workspace),
+        _here(dtable, None, rows, "dtable", device), _type(dtable, "dtable"), add, *_scratch(workspace, device),
         _stream(stream)))
 
 
