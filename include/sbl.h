@@ -554,14 +554,14 @@ int sbl_head_kd_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w,
  *   x          [m_tok][k], x_dtype (SBL_BF16, SBL_FP16 or SBL_FP32).
  *   weight, bias  [k] fp32, or NULL (1 and 0).
  *   eps        > 0.
- *   y          [m_tok][k] output, or NULL: y_dtype is x_dtype or SBL_FP32, y
- *              rounded once more to a 16-bit type (xq and gamma come from the
- *              fp32 value).
+ *   y          [m_tok][k] output, or NULL: y_dtype is x_dtype, or one of the two
+ *              is SBL_FP32; y is rounded once more to a 16-bit type (xq and gamma
+ *              come from the fp32 value).
  *   xq, gamma  [m_tok][k] int8 and [m_tok] fp32 outputs, or both NULL; with
  *              them k % 64 == 0.
  *   mean, rstd [m_tok] fp32 outputs, each nullable: what the backward takes
  *              (mean is 0 if not centered).
- * The backward takes the gradient dy of y (dy_dtype: x_dtype or SBL_FP32):
+ * The backward takes the gradient dy of y (dy_dtype beside x_dtype as y_dtype):
  *   xh = (x - mean) rstd,  g = dy weight
  *   dx = rstd (g - [center] mean_k(g) - xh mean_k(g xh))         [m_tok][k], x_dtype
  *   dweight = sum_t dy xh,  dbias = sum_t dy                     [k] fp32
@@ -591,8 +591,8 @@ int sbl_norm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x
  *   of NaNs.
  *   ids        [m_tok] int64.
  *   table      [n_vocab][k], table_dtype (SBL_BF16, SBL_FP16 or SBL_FP32).
- *   out        [m_tok][k], out_dtype: table_dtype or SBL_FP32.
- * Its gradient, from dout [m_tok][k] (dout_dtype: table_dtype or SBL_FP32):
+ *   out        [m_tok][k], out_dtype: table_dtype, or one of the two is SBL_FP32.
+ * Its gradient, from dout [m_tok][k] (dout_dtype beside table_dtype as out_dtype):
  *   dtable[v] = scale * sum over the t with ids[t] == v of dout[t]
  * in fp32, the tokens in ascending order (an id of many tokens: in stretches
  * whose sums are added in ascending order), rounded once to table_dtype.  Ids

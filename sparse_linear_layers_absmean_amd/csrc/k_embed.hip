@@ -482,9 +482,7 @@ template <int TD, int TT, int V> hipError_t backward(const SumArgs& a, bool add,
 }  // namespace
 
 hipError_t launch_embed_forward(const EmbedArgs& a, int tt, int to, hipStream_t s) {
-  if (tt == kBf16) return to == kFp32 ? forward<kBf16, kFp32>(a, s) : forward<kBf16, kBf16>(a, s);
-  if (tt == kFp16) return to == kFp32 ? forward<kFp16, kFp32>(a, s) : forward<kFp16, kFp16>(a, s);
-  return forward<kFp32, kFp32>(a, s);
+  return with_types(tt, to, [&](auto t, auto o) { return forward<t.value, o.value>(a, s); });
 }
 
 int64_t embed_grad_ws_bytes(int64_t m_tok, int64_t n_vocab, int64_t k, int out_type) {
@@ -511,13 +509,7 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
   const SumArgs a{g.dout, g.dtable, (int32_t)g.m_tok, (int32_t)g.n_vocab, g.k, g.scale, p.segment, p.segments, p.chunks,
                   p.chunk_vecs, (int32_t)zero, (int32_t)zero_rows, o, reinterpret_cast<float*>(ws + p.part)};
   const bool join = g.m_tok > p.segment;         // else no run is longer than a segment
-  if (td == kFp32) {
-    if (tt == kBf16) return backward<kFp32, kBf16, 4>(a, g.add, join, s);
-    if (tt == kFp16) return backward<kFp32, kFp16, 4>(a, g.add, join, s);
-    return backward<kFp32, kFp32, 4>(a, g.add, join, s);
-  }
-  if (td == kBf16) return backward<kBf16, kBf16, 8>(a, g.add, join, s);
-  return backward<kFp16, kFp16, 8>(a, g.add, join, s);
+  return with_types(td, tt, [&](auto d, auto t) { return backward<d.value, t.value, d.value == kFp32 ? 4 : 8>(a, g.add, join, s); });
 }
 
 }  // namespace step

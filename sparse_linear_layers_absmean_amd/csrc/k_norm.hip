@@ -582,9 +582,7 @@ template <int TX, int TD> hipError_t backward(const NormGradArgs& a, hipStream_t
 }  // namespace
 
 hipError_t launch_norm_forward(const NormArgs& a, int tx, int ty, hipStream_t s) {
-  if (tx == kBf16) return ty == kFp32 ? forward<kBf16, kFp32>(a, s) : forward<kBf16, kBf16>(a, s);
-  if (tx == kFp16) return ty == kFp32 ? forward<kFp16, kFp32>(a, s) : forward<kFp16, kFp16>(a, s);
-  return forward<kFp32, kFp32>(a, s);
+  return with_types(tx, ty, [&](auto x, auto y) { return forward<x.value, y.value>(a, s); });
 }
 
 // partial rows of both column sums; long rows: two means per row, 8-byte aligned
@@ -600,9 +598,7 @@ hipError_t launch_norm_backward(const NormGradArgs& a, int tx, int td, hipStream
       if (p) hipLaunchKernelGGL(zero_floats_kernel, dim3((unsigned)((a.k + 255) / 256)), dim3(256), 0, s, p, a.k);
     return hipGetLastError();
   }
-  if (tx == kBf16) return td == kFp32 ? backward<kBf16, kFp32>(a, s) : backward<kBf16, kBf16>(a, s);
-  if (tx == kFp16) return td == kFp32 ? backward<kFp16, kFp32>(a, s) : backward<kFp16, kFp16>(a, s);
-  return backward<kFp32, kFp32>(a, s);
+  return with_types(tx, td, [&](auto x, auto d) { return backward<x.value, d.value>(a, s); });
 }
 
 }  // namespace step

@@ -25,8 +25,8 @@ static_assert((int)SBL_BF16 == sbl::step::kBf16 && (int)SBL_FP16 == sbl::step::k
               "types");
 
 bool type_ok(int32_t t) { return t == SBL_BF16 || t == SBL_FP16 || t == SBL_FP32; }
-// a second type beside the first: the same, or fp32
-bool pair_ok(int32_t t, int32_t wide) { return type_ok(t) && (wide == t || wide == SBL_FP32); }
+// two types of one call: the same, or fp32 and any other
+bool pair_ok(int32_t a, int32_t b) { return type_ok(a) && type_ok(b) && (a == b || a == SBL_FP32 || b == SBL_FP32); }
 
 bool rows_ok(int64_t m_tok, int64_t k) {
   return m_tok >= 0 && m_tok <= kMaxTokens && k >= 1 && k <= kMaxK && m_tok * k <= kMaxValues;

@@ -3,6 +3,8 @@
 // update (k_adamw.hip); their calls are in sbl_api_step.hip.
 #pragma once
 
+#include <type_traits>
+
 #include "sbl_internal.h"
 
 namespace sbl {
@@ -10,7 +12,17 @@ namespace step {
 
 // numeric types, numbered as sbl_dtype
 enum Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
-inline int64_t type_bytes(int t) { return t == kFp32 ? 4 : 2; }
+__host__ __device__ constexpr int64_t type_bytes(int t) { return t == kFp32 ? 4 : 2; }
+
+// f(a, b) with two types as constants: the same, or fp32 and another
+template <class F> hipError_t with_types(int a, int b, F f) {
+  std::integral_constant<int, kBf16> bf16;
+  std::integral_constant<int, kFp16> fp16;
+  std::integral_constant<int, kFp32> fp32;
+  if (a == kBf16) return b == kFp32 ? f(bf16, fp32) : f(bf16, bf16);
+  if (a == kFp16) return b == kFp32 ? f(fp16, fp32) : f(fp16, fp16);
+  return b == kBf16 ? f(fp32, bf16) : b == kFp16 ? f(fp32, fp16) : f(fp32, fp32);
+}
 
 // ---------------------------------------------------------------- norm
 

@@ -676,7 +676,7 @@ def _scratch(t, device: int):
 
 def sbl_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, y=None, xq=None, gamma=None,
                      mean=None, rstd=None, stream=None):
-    """Layer norm (center) or RMS norm of the rows of x [m_tok][k] -> y (x's type or fp32) and/or its
+    """Layer norm (center) or RMS norm of the rows of x [m_tok][k] -> y (x's type, or one of them fp32) and/or its
     int8 codes xq with gamma; mean, rstd fp32 [m_tok] for the backward.  Every output may be None."""
     m_tok, k = rows = _rows(x, "x")
     f32, device, row, col = torch.float32, torch.cuda.current_device(), (m_tok,), (k,)
@@ -695,7 +695,7 @@ def sbl_norm_workspace_bytes(m_tok: int, k: int) -> int:
 
 
 def sbl_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, center: bool = True, stream=None):
-    """Gradients of the norm from dy [m_tok][k] (x's type or fp32): dx in x's type, dweight and dbias fp32 [k]
+    """Gradients of the norm from dy [m_tok][k] (x's type, or one of them fp32): dx in x's type, dweight and dbias fp32 [k]
     (each may be None).  mean may be None where not centered."""
     m_tok, k = rows = _rows(x, "x")
     f32, device, row, col = torch.float32, torch.cuda.current_device(), (m_tok,), (k,)
@@ -716,7 +716,7 @@ def _ids(ids):
 
 def sbl_embed_forward(ids, table, out, scale: float = 1.0, stream=None):
     """out[t] = scale * table[ids[t]]: ids int64 of any shape, table [n_vocab][k], out [ids' shape][k] in the
-    table's type or fp32.  A negative id gives zeros, an id past the table NaNs."""
+    table's type (or one of them fp32).  A negative id gives zeros, an id past the table NaNs."""
     n_vocab, k = rows = _rows(table, "table")
     at, m_tok, device = _ids(ids)
     _check("sbl_embed_forward", load().sbl_embed_forward(
@@ -730,7 +730,7 @@ def sbl_embed_workspace_bytes(m_tok: int, n_vocab: int, k: int, dtype=torch.bflo
 
 
 def sbl_embed_backward(ids, dout, dtable, workspace, scale: float = 1.0, add: bool = False, stream=None):
-    """Gradient of the table from dout [ids' shape][k] (the table's type or fp32): written to dtable
+    """Gradient of the table from dout [ids' shape][k] (the table's type, or one of them fp32): written to dtable
     [n_vocab][k], or added to what it holds."""
     n_vocab, k = rows = _rows(dtable, "dtable")
     at, m_tok, device = _ids(ids)
@@ -933,10 +933,12 @@ def head_kd_backward(h, w, index, teacher, tau: float, lse, dloss, workspace=Non
 
 
 def _like(x, dtype, name: str):
-    """The output type: x's unless another is asked for."""
-    if dtype not in (None, x.dtype, torch.float32):
+    """The output type: x's unless another is asked for (one of the two float32)."""
+    if dtype is None or dtype is x.dtype:
+        return x.dtype
+    if dtype not in _TYPES or (dtype is not torch.float32 and x.dtype is not torch.float32):
         raise TypeError(f"{name} must be {x.dtype} or torch.float32")
-    return dtype if dtype is not None else x.dtype
+    return dtype
 
 
 def _norm_out(x, weight, bias, eps, center, y, quant: bool):
@@ -958,7 +960,8 @@ def _norm_out(x, weight, bias, eps, center, y, quant: bool):
 
 
 def norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, dtype=None, stream=None):
-    """Allocate outputs and run sbl_norm_forward; returns (y, mean, rstd), y in x's type or float32."""
+    """Allocate outputs and run sbl_norm_forward; returns (y, mean, rstd), y in x's type unless another
+    is asked for."""
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return norm(x, weight, bias, eps, center, dtype)
@@ -1006,7 +1009,8 @@ def norm_backward(dy, x, mean, rstd, weight=None, want_bias: bool = False, cente
 
 
 def embed(ids, table, scale: float = 1.0, dtype=None, stream=None):
-    """Allocate the output and run sbl_embed_forward; returns rows of the table's type or float32."""
+    """Allocate the output and run sbl_embed_forward; returns rows of the table's type unless another is
+    asked for."""
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return embed(ids, table, scale, dtype)

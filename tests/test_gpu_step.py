@@ -14,7 +14,7 @@ from oracle import step_oracle as S
 pytestmark = pytest.mark.gpu
 
 PAIRS = [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float16", "float16"), ("float16", "float32"),
-         ("float32", "float32")]
+         ("float32", "float32"), ("float32", "bfloat16"), ("float32", "float16")]
 GUARD = 0x5A
 
 
@@ -93,7 +93,7 @@ def _near(got, want, bound, dtype, name):
 # ---------------------------------------------------------------- norm
 
 # one slot per thread up to 4096 values, two, four up to 16384, rows in sweeps above; few and many rows
-NORM = [(1, 1), (3, 2), (2, 5), (5, 63), (4, 64), (3, 65), (2, 250), (7, 1000), (3, 1541), (1, 3200), (2, 4095), (2, 4096),
+NORM = [(1, 1), (3, 2), (4, 3), (2, 5), (5, 63), (4, 64), (3, 65), (2, 250), (7, 1000), (3, 1541), (1, 3200), (2, 4095), (2, 4096),
         (2, 4097), (3, 8192), (2, 8200), (1, 16384), (2, 16385), (2, 28672), (1, 40000), (1, 131072),
         (1030, 64), (1025, 333), (1500, 512), (2100, 1541), (1100, 2048), (1030, 5120), (1024, 12000)]
 
