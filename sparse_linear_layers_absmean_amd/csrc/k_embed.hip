@@ -266,12 +266,12 @@ struct SumArgs {
 // One row's columns to memory.  LINES: rows are whole 128-byte lines, stored past
 // the caches.
 template <int TT, int V, bool ADD, bool LINES>
-__device__ __forceinline__ void put(typename Mem<TT>::E* row, int skip, const float (&sum)[V], float scale,
+__device__ __forceinline__ void put(typename Mem<TT>::E* row, Place c, const float (&sum)[V], float scale,
                                     const Vec<TT, V>& old) {
   float f[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) f[j] = ADD ? old[j] + sum[j] * scale : sum[j] * scale;
-  store_own<TT, V, LINES>(row, f, skip);
+  store_own<TT, V, LINES>(row, c, f);
 }
 
 // where the run of id `v` lies
@@ -336,7 +336,7 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
   const bool long_tail = tail.end > i1 && tail.end - tail.begin > S;
   const int from = head.begin == i0 || long_head ? i0 : head.end;
   const int to = long_tail ? i1 : tail.end;
-  const ED* dout = static_cast<const ED*>(a.dout) + c.col;
+  const ED* dout = static_cast<const ED*>(a.dout);
   float sum[V] = {};
   constexpr int U = 8;                           // tokens whose loads are in flight
   for (int i = from; i < to; i += 64) {
@@ -353,10 +353,10 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
       for (int u = 0; u < U; ++u) {
         if (j + u >= n) break;
         const int t = __builtin_amdgcn_readlane(pos, j + u);
-        d[u] = load_once<TD, V>(dout + (int64_t)t * a.k);
+        d[u] = load_once<TD, V>(at_col(dout + (int64_t)t * a.k, c.col));
         if constexpr (ADD) {
           if (ends >> (j + u) & 1)
-            old[u] = load<TT, V>(table + (int64_t)__builtin_amdgcn_readlane(key, j + u) * a.k + c.col);
+            old[u] = load<TT, V>(at_col(table + (int64_t)__builtin_amdgcn_readlane(key, j + u) * a.k, c.col));
         }
       }
 #pragma unroll
@@ -369,9 +369,9 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
           const bool in_head = long_head && at < head.end, in_tail = long_tail && at == to - 1;
           if (in_head || in_tail) {
             const bool begins = in_tail && tail.begin >= i0;
-            store_own<kFp32, V>(a.part + ((int64_t)seg * 2 + begins) * a.k + c.col, sum, c.skip);
+            store_own<kFp32, V>(a.part + ((int64_t)seg * 2 + begins) * a.k, c, sum);
           } else {
-            put<TT, V, ADD, LINES>(table + (int64_t)v * a.k + c.col, c.skip, sum, a.scale, old[ADD ? u : 0]);
+            put<TT, V, ADD, LINES>(table + (int64_t)v * a.k, c, sum, a.scale, old[ADD ? u : 0]);
           }
 #pragma unroll
           for (int e = 0; e < V; ++e) sum[e] = 0.0f;
@@ -395,21 +395,21 @@ template <int TT, int V, bool ADD, bool LINES> __global__ __launch_bounds__(kThr
   if (r.begin < i0 || r.end <= i1 || r.end - r.begin <= S) return;
   if ((int)threadIdx.x >= a.chunk_vecs) return;
   const Place c = place<V>((chunk * a.chunk_vecs + (int)threadIdx.x) * V, a.k);
-  ET* row = static_cast<ET*>(a.dtable) + (int64_t)v * a.k + c.col;
+  ET* row = static_cast<ET*>(a.dtable) + (int64_t)v * a.k;
   Vec<TT, V> old{};
-  if constexpr (ADD) old = load<TT, V>(row);
+  if constexpr (ADD) old = load<TT, V>(at_col(row, c.col));
   float sum[V];
-  const Vec<kFp32, V> first = load<kFp32, V>(a.part + ((int64_t)seg * 2 + 1) * a.k + c.col);
+  const Vec<kFp32, V> first = load<kFp32, V>(at_col(a.part + ((int64_t)seg * 2 + 1) * a.k, c.col));
 #pragma unroll
   for (int e = 0; e < V; ++e) sum[e] = first[e];
   const int last = (r.end - 1) / S;
 #pragma unroll 8
   for (int s = seg + 1; s <= last; ++s) {
-    const Vec<kFp32, V> p = load<kFp32, V>(a.part + (int64_t)s * 2 * a.k + c.col);
+    const Vec<kFp32, V> p = load<kFp32, V>(at_col(a.part + (int64_t)s * 2 * a.k, c.col));
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] += p[e];
   }
-  put<TT, V, ADD, LINES>(row, c.skip, sum, a.scale, old);
+  put<TT, V, ADD, LINES>(row, c, sum, a.scale, old);
 }
 
 // `words` 16-bit zeros, 16-byte aligned

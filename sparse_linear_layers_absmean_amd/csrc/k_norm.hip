@@ -33,8 +33,9 @@ constexpr int kMaxWaves = 16;
 
 // What is known of the rows of an output when a kernel is compiled.  kLines:
 // they are whole 128-byte lines, and many: stored past the caches (4096 x 5120
-// BF16 to fp32 and int8: 42 -> 32 us; rows that end inside a line would be slower
-// so; loads past the caches as well: 42 us, an input is often there still).  kWhole: also exactly as many values as the threads hold.
+// BF16 to fp32 and int8 when the weights were held: 42 -> 32 us; rows that end
+// inside a line would be slower so; loads past the caches as well: 42, an input is
+// often there still).  kWhole: also exactly as many values as the threads hold.
 enum Rows { kAny = 0, kLines = 1, kWhole = 2 };
 
 // 1 / sqrt(v) to fp64's precision: v_rsq_f64 (24 bits) and two Newton steps
@@ -67,7 +68,31 @@ template <int T> __device__ __forceinline__ void add_stats(const Vec<T, V>& x, i
   }
 }
 
-// the row's value of one position
+// Four values to four codes, as actq::q_word (sbl_actq.h) makes them, in fewer
+// instructions: adding 1.5 2^23 rounds to a whole number, ties to even, whose
+// low byte is the code; the quotient RN(v r) decides unless it lies within 2^-15
+// of a half, where |v / s - RN(v r)| could matter, and the IEEE quotient is formed.
+// Clamped first: past 127.5 every quotient gives 127.
+__device__ __forceinline__ uint32_t codes(const float (&v)[V], const actq::Step& st) {
+  constexpr float kWhole = 12582912.0f;
+  float m[V];
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float q = __builtin_amdgcn_fmed3f(v[j] * st.r, -127.0f, 127.0f);
+    m[j] = q + kWhole;
+    near = near || fabsf(q - (m[j] - kWhole)) >= 0.5f - 0x1p-15f;
+  }
+  if (__any(near)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) m[j] = __builtin_amdgcn_fmed3f(v[j] / st.s, -127.0f, 127.0f) + kWhole;
+  }
+  const uint32_t lo = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, m[1]), __builtin_bit_cast(uint32_t, m[0]), 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, m[3]), __builtin_bit_cast(uint32_t, m[2]), 0x0c0c0400u);
+  return lo | hi << 16;
+}
+
+// the row's value of one position (not centered: the mean is zero)
 __device__ __forceinline__ float normal(float x, const Stat& st, float w, float b) {
   return (float)((double)x - st.mean) * st.rstd * w + b;
 }
@@ -77,20 +102,41 @@ __device__ __forceinline__ void load_param(const float* p, int col, int have, fl
 #pragma unroll
   for (int j = 0; j < V; ++j) f[j] = p ? v[j] : none;
 }
-template <int W> __device__ __forceinline__ void load_param(const float* p, int col, float none, float (&f)[W]) {
-#pragma unroll
-  for (int j = 0; j < W; ++j) f[j] = none;
-  if (!p) return;
-  const Vec<kFp32, W> v = load<kFp32, W>(p + col);
-#pragma unroll
-  for (int j = 0; j < W; ++j) f[j] = v[j];
+// the same by a buffer load, without a branch: of no parameters at all it reads zeros
+struct Param {
+  __amdgpu_buffer_rsrc_t r;
+  float none;                                    // what to add: 0, or the value that stands for a parameter that is not there
+};
+__device__ __forceinline__ Param param(const float* p, int k, float none) {
+  return Param{make_rsrc(p, p ? (int64_t)k * 4 : 0), p ? 0.0f : none};
+}
+template <int W> __device__ __forceinline__ void load_param(const Param& p, int col, float (&f)[W]) {
+  if constexpr (W == 4) {
+    const float4 v = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(p.r, (uint32_t)col * 4u, 0, 0));
+    f[0] = v.x + p.none;
+    f[1] = v.y + p.none;
+    f[2] = v.z + p.none;
+    f[3] = v.w + p.none;
+  } else {
+    static_assert(W == 1, "");
+    f[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(p.r, (uint32_t)col * 4u, 0, 0)) + p.none;
+  }
+}
+
+// Keeps a value where it is made: without it sums and addresses move out of
+// their loop or to its end, with everything that they are made from.
+__device__ __forceinline__ void pin(float& f) { asm volatile("" : "+v"(f)); }
+__device__ __forceinline__ int pinned(int i) {
+  asm volatile("" : "+v"(i));
+  return i;
 }
 
 // Rows of at most blockDim.x * SLOTS * W values, one workgroup per row and
-// then the row gridDim.x later.
-template <int TX, int TY, int SLOTS, int W, int ROWS>
+// then the row gridDim.x later.  Held in registers beside the row: the next row,
+// and if HOLD the weights; if not they are read again for every row (from L2).
+template <int TX, int TY, int SLOTS, bool HOLD, int W, int ROWS>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
-  constexpr bool WHOLE = ROWS == kWhole;
+  constexpr bool WHOLE = ROWS == kWhole, AHEAD = SLOTS <= 4 || TX != kFp32;
   typedef typename Mem<TX>::E EX;
   typedef typename Mem<TY>::E EY;
   __shared__ double part[2][2][kMaxWaves];       // of even and odd rows: one barrier per reduction
@@ -100,12 +146,15 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
   const double inv_k = 1.0 / k;
   const EX* x = static_cast<const EX*>(a.x);
   Place at[SLOTS];
-  float w[SLOTS][W], b[SLOTS][W];
+  const Param pw = param(a.w, k, 1.0f), pb = param(a.b, k, 0.0f);
+  float w[HOLD ? SLOTS : 1][W], b[HOLD ? SLOTS : 1][W];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
     at[i] = place<W>((tid + i * (int)blockDim.x) * W, k);
-    load_param<W>(a.w, at[i].col, 1.0f, w[i]);
-    load_param<W>(a.b, at[i].col, 0.0f, b[i]);
+    if constexpr (HOLD) {
+      load_param<W>(pw, at[i].col, w[i]);
+      load_param<W>(pb, at[i].col, b[i]);
+    }
   }
   int64_t row = blockIdx.x;
   Vec<TX, W> next[SLOTS];
@@ -114,7 +163,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
     const EX* p = x + row * k;
     next0 = p[0];
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, W>(p + at[i].col);
+    for (int i = 0; i < SLOTS; ++i) next[i] = load<TX, W>(at_col(p, at[i].col));
   };
   fetch();
   for (int p = 0;; p ^= 1) {
@@ -122,21 +171,44 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
     Vec<TX, W> v[SLOTS];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) v[i] = next[i];
-    const double x0 = a.center ? (double)to_f32<TX>(next0) : 0.0;
+    const EX e0 = a.center ? next0 : (EX)0;
+    const double x0 = (double)to_f32<TX>(e0);
+    // what the sums take: x0, which adds nothing, in place of the vectors past whole lines
+    auto taken = [&](int i) {
+      Vec<TX, W> t = v[i];
+      if (ROWS == kLines && at[i].skip != 0) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) t.e[j] = e0;
+      }
+      return t;
+    };
     row += gridDim.x;
-    if (row < a.m_tok) fetch();
+    if (AHEAD && row < a.m_tok) fetch();
     double s1 = 0.0, s2 = 0.0;
+    if (a.center) {
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
+      for (int i = 0; i < SLOTS; ++i) {
+        const Vec<TX, W> t = taken(i);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        double e = (double)v[i][j] - x0;
-        if (!WHOLE) e = j >= at[i].skip ? e : 0.0;
-        s1 += e;
-        s2 = __builtin_fma(e, e, s2);
+        for (int j = 0; j < W; ++j) {
+          double e = (double)t[j] - x0;
+          if (ROWS == kAny) e = j >= at[i].skip ? e : 0.0;
+          s1 += e;
+          s2 = __builtin_fma(e, e, s2);
+        }
+      }
+      s1 = wave_sum(s1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        const Vec<TX, W> t = taken(i);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float f = ROWS != kAny || j >= at[i].skip ? t[j] : 0.0f;
+          s2 = __builtin_fma((double)f, (double)f, s2);
+        }
       }
     }
-    s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if ((tid & 63) == 0) {
       part[p][0][wave] = s1;
@@ -154,32 +226,47 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
     float y[SLOTS][W];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
+      const Place c{HOLD ? at[i].col : pinned(at[i].col), WHOLE ? 0 : at[i].skip};
+      if constexpr (!HOLD) {
+        forget(v[i]);
+        if (i % 2 == 0) __builtin_amdgcn_sched_barrier(0);   // the weights of two slots at a time
+      }
+      float(&wi)[W] = w[HOLD ? i : 0];
+      float(&bi)[W] = b[HOLD ? i : 0];
+      if constexpr (!HOLD) {
+        load_param<W>(pw, c.col, wi);
+        load_param<W>(pb, c.col, bi);
+      }
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        y[i][j] = normal(v[i][j], st, w[i][j], b[i][j]);
+        // not centered: the mean is zero, and the difference x itself
+        const float d = a.center ? (float)((double)v[i][j] - st.mean) : v[i][j];
+        y[i][j] = d * st.rstd * wi[j] + bi[j];
         mx = fmaxf(mx, fabsf(y[i][j]));          // a column seen twice does not change the largest
       }
-      if (a.y) store_own<TY, W, ROWS != kAny>(static_cast<EY*>(a.y) + base + at[i].col, y[i], WHOLE ? 0 : at[i].skip);
+      if (a.y) store_own<TY, W, ROWS != kAny>(static_cast<EY*>(a.y) + base, c, y[i]);
     }
     if (tid == 0) {
       if (a.mean) a.mean[now] = (float)st.mean;
       if (a.rstd) a.rstd[now] = st.rstd;
     }
-    if (W == V && a.xq) {                        // k % 64 == 0: no vector passes the row's end
-      mx = wave_max(mx);
-      if ((tid & 63) == 0) peak[p][wave] = mx;
-      __syncthreads();
-      float g = peak[p][0];
-      for (int i = 1; i < waves; ++i) g = fmaxf(g, peak[p][i]);
-      const actq::Step sp = actq::make_step(g);
+    if constexpr (W == V) {                      // k % 64 == 0: no vector passes the row's end
+      if (a.xq) {
+        mx = wave_max(mx);
+        if ((tid & 63) == 0) peak[p][wave] = mx;
+        __syncthreads();
+        float g = peak[p][0];
+        for (int i = 1; i < waves; ++i) g = fmaxf(g, peak[p][i]);
+        const actq::Step sp = actq::make_step(g);
 #pragma unroll
-      for (int i = 0; i < SLOTS; ++i)
-        if (WHOLE || at[i].skip == 0)
-          *reinterpret_cast<uint32_t*>(a.xq + base + at[i].col) =
-              actq::q_word(float4{y[i][0], y[i][W > 1 ? 1 : 0], y[i][W > 2 ? 2 : 0], y[i][W > 3 ? 3 : 0]}, sp);
-      if (tid == 0) a.gamma[now] = g;
+        for (int i = 0; i < SLOTS; ++i)
+          if (WHOLE || at[i].skip == 0)
+            *reinterpret_cast<uint32_t*>(at_col(a.xq + base, at[i].col)) = codes(y[i], sp);
+        if (tid == 0) a.gamma[now] = g;
+      }
     }
     if (row >= a.m_tok) break;
+    if constexpr (!AHEAD) fetch();
   }
 }
 
@@ -242,7 +329,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
   for (int c = tid * V; c < k; c += 1024 * V) {
     float y[V];
     value(c, y);
-    *reinterpret_cast<uint32_t*>(a.xq + base + c) = actq::q_word(float4{y[0], y[1], y[2], y[3]}, sp);
+    *reinterpret_cast<uint32_t*>(a.xq + base + c) = codes(y, sp);
   }
   if (tid == 0) a.gamma[blockIdx.x] = g;
 }
@@ -259,13 +346,12 @@ __device__ __forceinline__ float grad(float dy, float xh, float w, float rstd, f
   return rstd * (dy * w - c1 - xh * c2);
 }
 
-// Rows of at most blockDim.x * SLOTS * W values, blockDim.x at most MOST.  Every thread keeps the column sums of its own
-// columns over the workgroup's rows.
+// Rows of at most blockDim.x * SLOTS * W values, blockDim.x at most MOST.  Every
+// thread keeps the column sums of its own columns over the workgroup's rows and, up
+// to 512 threads, holds the next row beside this one and the weights.
 template <int TX, int TD, int SLOTS, int W, int MOST, int ROWS>
 __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, float* part_w, float* part_b) {
-  constexpr bool WHOLE = ROWS == kWhole;
-  // weights and the next row in registers too, where 512 / waves per SIMD leaves them
-  constexpr bool kHold = SLOTS * MOST <= 2048;
+  constexpr bool WHOLE = ROWS == kWhole, KEEP_W = SLOTS * MOST <= 2048, AHEAD = KEEP_W;
   typedef typename Mem<TX>::E EX;
   typedef typename Mem<TD>::E ED;
   __shared__ Pair part[2][kMaxWaves];
@@ -275,11 +361,12 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
   const EX* x = static_cast<const EX*>(a.x);
   const ED* dy = static_cast<const ED*>(a.dy);
   Place at[SLOTS];
-  float w[kHold ? SLOTS : 1][W], sw[SLOTS][W], sb[SLOTS][W];
+  const Param pw = param(a.w, k, 1.0f);
+  float w[KEEP_W ? SLOTS : 1][W], sw[SLOTS][W], sb[SLOTS][W];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
     at[i] = place<W>((tid + i * (int)blockDim.x) * W, k);
-    if constexpr (kHold) load_param<W>(a.w, at[i].col, 1.0f, w[i]);
+    if constexpr (KEEP_W) load_param<W>(pw, at[i].col, w[i]);
 #pragma unroll
     for (int j = 0; j < W; ++j) sw[i][j] = sb[i][j] = 0.0f;
   }
@@ -292,8 +379,8 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
     nr = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      nx[i] = load<TX, W>(x + row * k + at[i].col);
-      nd[i] = load<TD, W>(dy + row * k + at[i].col);
+      nx[i] = load<TX, W>(at_col(x + row * k, at[i].col));
+      nd[i] = load<TD, W>(at_col(dy + row * k, at[i].col));
     }
   };
   fetch();
@@ -306,23 +393,32 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
     for (int i = 0; i < SLOTS; ++i) {
       vx[i] = nx[i];
       vd[i] = nd[i];
+      if (ROWS == kLines && at[i].skip != 0) vd[i] = Vec<TD, W>{};   // past whole lines: adds nothing
     }
     row += gridDim.x;
-    if (kHold && row < a.m_tok) fetch();
+    if (AHEAD && row < a.m_tok) fetch();
+    auto weights = [&](int i) -> const float(&)[W] {
+      float(&wi)[W] = w[KEEP_W ? i : 0];
+      if constexpr (!KEEP_W) load_param<W>(pw, pinned(at[i].col), wi);
+      return wi;
+    };
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      float(&wi)[W] = w[kHold ? i : 0];
-      if constexpr (!kHold) load_param<W>(a.w, at[i].col, 1.0f, wi);
+      const float(&wi)[W] = weights(i);
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const float xh = xhat(vx[i][j], mean, rstd), d = vd[i][j];
         float g = d * wi[j];
-        if (!WHOLE) g = j >= at[i].skip ? g : 0.0f;
+        if (ROWS == kAny) g = j >= at[i].skip ? g : 0.0f;
         s1 += g;
         s2 = __builtin_fmaf(g, xh, s2);
         sw[i][j] = __builtin_fmaf(d, xh, sw[i][j]);
         sb[i][j] += d;
+        if constexpr (!KEEP_W) {
+          pin(sw[i][j]);
+          pin(sb[i][j]);
+        }
       }
     }
     if (a.dx) {
@@ -339,23 +435,26 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
       const float c1 = a.center ? s1 * inv_k : 0.0f, c2 = s2 * inv_k;
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i) {
+        if constexpr (!KEEP_W) {
+          forget(vx[i]);
+          forget(vd[i]);
+        }
+        const float(&wi)[W] = weights(i);
         float d[W];
-        float(&wi)[W] = w[kHold ? i : 0];
-        if constexpr (!kHold) load_param<W>(a.w, at[i].col, 1.0f, wi);
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-          d[j] = grad(vd[i][j], xhat(vx[i][j], mean, rstd), wi[j], rstd, c1, c2);
-        store_own<TX, W, ROWS != kAny>(static_cast<EX*>(a.dx) + base + at[i].col, d, WHOLE ? 0 : at[i].skip);
+        for (int j = 0; j < W; ++j) d[j] = grad(vd[i][j], xhat(vx[i][j], mean, rstd), wi[j], rstd, c1, c2);
+        store_own<TX, W, ROWS != kAny>(static_cast<EX*>(a.dx) + base,
+                                       Place{KEEP_W ? at[i].col : pinned(at[i].col), WHOLE ? 0 : at[i].skip}, d);
       }
     }
     if (row >= a.m_tok) break;
-    if constexpr (!kHold) fetch();
+    if constexpr (!AHEAD) fetch();
   }
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    const int skip = WHOLE ? 0 : at[i].skip;
-    if (part_w) store_own<kFp32, W>(part_w + (int64_t)blockIdx.x * k + at[i].col, sw[i], skip);
-    if (part_b) store_own<kFp32, W>(part_b + (int64_t)blockIdx.x * k + at[i].col, sb[i], skip);
+    const Place c = WHOLE ? Place{at[i].col, 0} : at[i];
+    if (part_w) store_own<kFp32, W>(part_w + (int64_t)blockIdx.x * k, c, sw[i]);
+    if (part_b) store_own<kFp32, W>(part_b + (int64_t)blockIdx.x * k, c, sb[i]);
   }
 }
 
@@ -463,19 +562,22 @@ __global__ __launch_bounds__(256) void zero_floats_kernel(float* p, int n) {
 
 constexpr int64_t kStreamBytes = 16 << 20;       // outputs of less stay in the caches
 constexpr int kWideFinal = 1024;
-constexpr int kMaxSlots = 4;                     // rows of up to 1024 * 4 * V values in registers (8 slots spill)
 
 int vectors(int64_t k) { return (int)((k + V - 1) / V); }
 
-// Slots per thread: one per thread as long as 1024 threads hold the row and
-// there are few rows (all of a row's loads in flight from as many waves as
-// possible); with more rows, 4 (more bytes in flight per wave, fewer waves to
-// join in a reduction), as long as that leaves two waves.
-int slots_for(int nv, int64_t m_tok) {
+// Slots per thread: with few rows, as few as 1024 threads can do with (all of a
+// row's loads in flight from as many waves as possible); with more rows, 4 (more
+// bytes in flight per wave, fewer waves to join in a reduction), as long as that
+// leaves two waves.  Forward, where nothing but the row need be held, 8 for rows
+// that 4 do not take (4096 x 28672 BF16 to fp32 and int8: 338 us by the kernel for
+// longer rows, 168 so, which is the time of its bytes; 13824 values in 8 slots 111,
+// in 4 94).  Backward 8 leave no room for the sums.
+constexpr int kMaxSlots = 8, kMaxGradSlots = 4;
+int slots_for(int nv, int64_t m_tok, int most) {
   int s = 1;
   if (m_tok >= 1024)
     while (s < 4 && nv >= 2 * s * 128) s *= 2;
-  while (s < kMaxSlots && nv > 1024 * s) s *= 2;
+  while (s < most && nv > 1024 * s) s *= 2;
   return s;
 }
 int threads_for(int nv, int slots) { return ((nv + slots - 1) / slots + 63) / 64 * 64; }
@@ -492,26 +594,31 @@ Rows rows_of(const void* out, int64_t k, int64_t bytes, int64_t held, int type) 
   return k == held ? kWhole : kLines;
 }
 
-template <int TX, int TY, int SLOTS> void forward_rows(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
+template <int TX, int TY, int SLOTS, bool HOLD> void forward_rows(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
   const Rows rows = rows_of(a.y, a.k, a.m_tok * a.k * type_bytes(TY), (int64_t)block.x * SLOTS * V, TY);
-  if (rows == kWhole) hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, V, kWhole>), grid, block, 0, s, a);
-  else if (rows == kLines) hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, V, kLines>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, V, kAny>), grid, block, 0, s, a);
+  if (rows == kWhole) hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, HOLD, V, kWhole>), grid, block, 0, s, a);
+  else if (rows == kLines) hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, HOLD, V, kLines>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_kernel<TX, TY, SLOTS, HOLD, V, kAny>), grid, block, 0, s, a);
 }
 
 template <int TX, int TY> hipError_t forward(const NormArgs& a, hipStream_t s) {
-  const int nv = vectors(a.k), slots = slots_for(nv, a.m_tok);
+  const int nv = vectors(a.k), slots = slots_for(nv, a.m_tok, kMaxSlots);
   if (nv > 1024 * kMaxSlots) {
     hipLaunchKernelGGL((norm_long_kernel<TX, TY>), dim3((unsigned)a.m_tok), dim3(1024), 0, s, a);
     return hipGetLastError();
   }
-  const int threads = threads_for(nv, slots);
-  const int64_t most = resident(threads, 4);
+  const int threads = threads_for(nv, slots), waves = threads / 64;
+  // 4 slots: the weights are held (4 waves per SIMD) unless without them one more workgroup fits
+  // a CU (5): 4096 x 5120 BF16 to fp32 and int8 32 us held, 27 not; 16384 x 8192 BF16 108 and 134
+  const bool hold = slots < 4 || (slots == 4 && 16 / waves == 20 / waves);
+  const int64_t most = resident(threads, slots <= 2 ? 6 : slots == 4 && !hold ? 5 : 4);
   const dim3 grid((unsigned)(a.m_tok < most ? a.m_tok : most)), block((unsigned)threads);
-  if (a.k < V) hipLaunchKernelGGL((norm_kernel<TX, TY, 1, 1, kAny>), grid, block, 0, s, a);
-  else if (slots == 1) forward_rows<TX, TY, 1>(a, grid, block, s);
-  else if (slots == 2) forward_rows<TX, TY, 2>(a, grid, block, s);
-  else forward_rows<TX, TY, 4>(a, grid, block, s);
+  if (a.k < V) hipLaunchKernelGGL((norm_kernel<TX, TY, 1, true, 1, kAny>), grid, block, 0, s, a);
+  else if (slots == 1) forward_rows<TX, TY, 1, true>(a, grid, block, s);
+  else if (slots == 2) forward_rows<TX, TY, 2, true>(a, grid, block, s);
+  else if (slots == 4 && hold) forward_rows<TX, TY, 4, true>(a, grid, block, s);
+  else if (slots == 4) forward_rows<TX, TY, 4, false>(a, grid, block, s);
+  else forward_rows<TX, TY, 8, false>(a, grid, block, s);
   return hipGetLastError();
 }
 
@@ -522,8 +629,8 @@ struct GradPlan {
 GradPlan grad_plan(int64_t m_tok, int64_t k) {
   const int nv = vectors(k);
   GradPlan p{0, 256, 0};
-  if (nv <= 1024 * kMaxSlots) {
-    p.slots = slots_for(nv, m_tok);
+  if (nv <= 1024 * kMaxGradSlots) {
+    p.slots = slots_for(nv, m_tok, kMaxGradSlots);
     p.threads = threads_for(nv, p.slots);
     p.parts = resident(p.threads, p.slots == 4 && p.threads <= 512 ? 3 : 4);
   } else {

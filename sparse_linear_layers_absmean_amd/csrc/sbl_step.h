@@ -225,15 +225,34 @@ template <int T, int V> __device__ __forceinline__ Vec<T, V> load_once(const typ
     return v;
   }
 }
+// The compiler knows nothing of v from here on: what it has made of v before
+// (wider numbers, differences) is made again and not kept in registers meanwhile.
+template <int T, int V> __device__ __forceinline__ void forget(Vec<T, V>& v) {
+  if constexpr (sizeof(v) % 4 == 0) {
+    uint32_t w[sizeof(v) / 4];
+    __builtin_memcpy(w, &v, sizeof(v));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(v) / 4); ++i) asm("" : "+v"(w[i]));
+    __builtin_memcpy(&v, w, sizeof(v));
+  }
+}
+
+// element `col` of a row that begins at the same address in every lane: its byte
+// offset in 32 bits, so that the address takes one vector register, not two
+template <class E> __device__ __forceinline__ E* at_col(E* row, int col) {
+  typedef typename std::conditional<std::is_const<E>::value, const uint8_t, uint8_t>::type B;
+  return reinterpret_cast<E*>(reinterpret_cast<B*>(row) + (uint32_t)(col * (int)sizeof(E)));
+}
 // the columns that are this thread's own
 template <int T, int V, bool STREAM = false>
-__device__ __forceinline__ void store_own(typename Mem<T>::E* p, const float (&f)[V], int skip) {
-  if (skip == 0) {
+__device__ __forceinline__ void store_own(typename Mem<T>::E* row, Place at, const float (&f)[V]) {
+  typename Mem<T>::E* p = at_col(row, at.col);
+  if (at.skip == 0) {
     store<T, V, STREAM>(p, f, V);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i >= skip) p[i] = from_f32<T>(f[i]);
+      if (i >= at.skip) p[i] = from_f32<T>(f[i]);
   }
 }
 

@@ -225,6 +225,17 @@ def test_norm_backward_matches_oracle(t, k, tx, td):
             assert np.array_equal(to_np(one[i].double()), first[i])
 
 
+# outputs past the caches, in rows that fill a workgroup's vectors and rows that do not, with the weights held in
+# registers and read again, up to the widest rows of each kernel
+@pytest.mark.parametrize("tx,ty", [("bfloat16", "float32"), ("float32", "float32"), ("float16", "float16")])
+@pytest.mark.parametrize("t,k", [(1650, 5120), (1700, 5184), (1100, 8192), (1100, 8640), (1100, 13824), (1100, 17344),
+                                 (1030, 28672), (1030, 32768)])
+def test_norm_of_many_wide_rows(t, k, tx, ty):
+    test_norm_matches_oracle(t, k, tx, ty)
+    test_norm_with_quantizer_is_norm_and_quant_acts(t, k, tx, ty)
+    test_norm_backward_matches_oracle(t, k, tx, ty)
+
+
 def test_norm_backward_is_the_forwards_slope():
     """Central differences of the forward itself, in fp32 (a step of 2^-6 of the values' size: the difference of two
     sums of 64 products, each off by some 2^-24, over 2^-5)."""
