@@ -6,12 +6,13 @@
 // Backward: dtable[v] = scale * sum of dout[t] over the tokens t with id[t] = v,
 // in fp32, in ascending t, rounded once (added to what dtable holds first, if
 // asked).  Without atomics on floats, so results repeat bit for bit:
-//  1. sort_kernel: the tokens in order of their ids, equal ids in order of t
-//     (`pos`, with their ids `key`), and where each id's run begins (`start`).
-//     Every workgroup owns a range of ids and reads all token ids twice: once
-//     to count (its own ids, and how many tokens lie below its range: that is
-//     where its part of the order begins, so that no workgroup waits for
-//     another), once to place.
+//  1. sort_kernel: the tokens id by id, equal ids in order of t (`pos`, with
+//     their ids `key`), and where each id's run lies (`run`).  Of 2^s workgroups
+//     each owns the ids of one remainder by 2^s (neighbouring ids are often
+//     alike in how many tokens they have: vocabularies are numbered by
+//     frequency) and reads all token ids: to count its own, and those of
+//     smaller remainders, after which its part of the order begins, so that no
+//     workgroup waits for another.
 //  2. sum_kernel: the sorted tokens in segments of S, a workgroup per segment
 //     and chunk of columns, sums in registers while it walks its tokens.  A
 //     run belongs to the segment that it begins in; a run longer than S (text
@@ -118,22 +119,29 @@ template <int TT, int TO> hipError_t forward(const EmbedArgs& a, hipStream_t s) 
 
 constexpr int kSortWaves = 16;
 constexpr int kSortThreads = 64 * kSortWaves;
-constexpr int kMaxRange = 800;                   // ids per workgroup (counters and lists in 64 KB)
+constexpr int kMaxRange = 1024;                  // ids per workgroup: a thread each, counters of 64 KB
 
+// where the tokens of an id lie in the order
+struct Run {
+  int32_t begin, end;
+};
 // Workspace
 struct Order {
-  int32_t* start;                                // [n_vocab + 1] first sorted token of each id; the last: how many
+  Run* run;                                      // [n_vocab + 1]; the last: all tokens
   int32_t* key;                                  // [m_tok] ids in order
   int32_t* pos;                                  // [m_tok] their tokens
 };
 
 struct SortArgs {
   const int64_t* ids;
-  int32_t m_tok, n_vocab, range;                 // range: ids per workgroup
+  int32_t m_tok, n_vocab, bits, range;           // the workgroup's ids: d 2^bits + blockIdx.x, d < range
   Order o;
 };
 
-constexpr int kListed = 192;                     // tokens of the range that a wave remembers from its count
+// Tokens that a wave remembers from its count.  More, and it reads the ids a second
+// time: 262144 tokens of 131072 ids, the most frequent 3 per cent of them, 129 us
+// with 192 and 58 with 768 (evenly drawn 51, all tokens of one id 298).
+constexpr int kListed = 768;
 
 __device__ __forceinline__ uint64_t lanes_below() { return (uint64_t(1) << (threadIdx.x & 63)) - 1; }
 
@@ -167,34 +175,34 @@ template <class F> __device__ __forceinline__ void scan(const int64_t* ids, int 
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
   extern __shared__ uint32_t count[];            // [wave][range]: counts, then the next place
   __shared__ uint32_t below[kSortWaves], sums[kSortWaves];
-  __shared__ uint32_t list[kSortWaves][kListed]; // (token - t0) 2^10 + id - v0, in order
+  __shared__ uint32_t list[kSortWaves][kListed]; // (token - t0) 2^10 + d, in order
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const uint32_t v0 = blockIdx.x * (uint32_t)a.range;
-  const uint32_t range = a.n_vocab - v0 < (uint32_t)a.range ? a.n_vocab - v0 : (uint32_t)a.range;
+  const uint32_t mine0 = blockIdx.x, mask = (1u << a.bits) - 1;
+  const uint32_t range = (uint32_t)a.range;
   for (uint32_t i = tid; i < kSortWaves * (uint32_t)a.range; i += kSortThreads) count[i] = 0;
   __syncthreads();
   // each wave takes a stretch of the tokens
   const int per = ((a.m_tok + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   const int t0 = wave * per, t1 = t0 + per < a.m_tok ? t0 + per : a.m_tok;
   uint32_t* mine = count + wave * a.range;
-  uint32_t low = 0, listed = 0;
+  uint32_t low = 0, listed = 0;                  // of the wave
   scan(a.ids, t0, t1, [&](int t, uint32_t id) {
-    low += id < v0;
-    const uint32_t d = id - v0;                  // below v0: past every range
-    const uint64_t inside = __ballot(d < range);
+    const uint32_t rest = id & mask;
+    const uint64_t known = __ballot(id < (uint32_t)a.n_vocab);
+    low += (uint32_t)__builtin_popcountll(known & __ballot(rest < mine0));
+    const uint64_t inside = known & __ballot(rest == mine0);
     if (!inside) return;
-    if (d < range) {
+    if (inside >> lane & 1) {
+      const uint32_t d = id >> a.bits;
       atomicAdd(&mine[d], 1u);
       const uint32_t at = listed + (uint32_t)__builtin_popcountll(inside & lanes_below());
       if (at < kListed) list[wave][at] = (uint32_t)(t - t0) << 10 | d;
     }
     listed += (uint32_t)__builtin_popcountll(inside);
   });
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) low += __shfl_xor(low, m, 64);
   if (lane == 0) below[wave] = low;
   __syncthreads();
-  // places of id v0 + tid: after the tokens below the range, the ids before it, the waves before each
+  // places of the workgroup's id `tid`: after the tokens of smaller remainders, the ids before it, the waves before each
   uint32_t total = 0;
   if (tid < (int)range)
     for (int w = 0; w < kSortWaves; ++w) total += count[w * a.range + tid];
@@ -209,8 +217,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
   uint32_t base = upto - total;
   for (int w = 0; w < kSortWaves; ++w) base += below[w] + (w < wave ? sums[w] : 0);
   if (tid < (int)range) {
-    a.o.start[v0 + tid] = (int32_t)base;
-    if (v0 + tid == (uint32_t)a.n_vocab - 1) a.o.start[a.n_vocab] = (int32_t)(base + total);
+    const uint32_t v = ((uint32_t)tid << a.bits) + mine0;
+    if (v < (uint32_t)a.n_vocab) a.o.run[v] = Run{(int32_t)base, (int32_t)(base + total)};
+    // the last of all: past its last id no workgroup has a token
+    if (tid == (int)range - 1 && blockIdx.x == gridDim.x - 1) a.o.run[a.n_vocab] = Run{0, (int32_t)(base + total)};
     for (int w = 0; w < kSortWaves; ++w) {
       const uint32_t n = count[w * a.range + tid];
       count[w * a.range + tid] = base;
@@ -228,7 +238,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
       const uint32_t place = mine[which];        // this wave's counters: no other wave touches them
       if (d == which) {
         const uint32_t at = place + (uint32_t)__builtin_popcountll(group & lanes_below());
-        a.o.key[at] = (int32_t)(v0 + d);
+        a.o.key[at] = (int32_t)((d << a.bits) + mine0);
         a.o.pos[at] = t;
       }
       if (lane == first) mine[which] = place + (uint32_t)__builtin_popcountll(group);
@@ -243,7 +253,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
       put(t0 + (int)(e >> 10), has ? e & 1023u : range);
     }
   } else {                                       // too many to remember: read the ids again
-    scan(a.ids, t0, t1, [&](int t, uint32_t id) { put(t, id - v0 < range ? id - v0 : range); });
+    scan(a.ids, t0, t1, [&](int t, uint32_t id) {
+      put(t, id < (uint32_t)a.n_vocab && (id & mask) == mine0 ? id >> a.bits : range);
+    });
   }
 }
 
@@ -274,22 +286,17 @@ __device__ __forceinline__ void put(typename Mem<TT>::E* row, Place c, const flo
   store_own<TT, V, LINES>(row, c, f);
 }
 
-// where the run of id `v` lies
-struct Run {
-  int begin, end;
-};
-__device__ __forceinline__ Run run_of(const Order& o, int v) { return Run{o.start[v], o.start[v + 1]}; }
-
 // Zeros in those of `many` (at most 64) rows from row v0 on that have no token.
 // Neighbouring ones are one stretch of memory, whose 128-byte lines are stored
 // whole and past the caches (rows of an odd length begin anywhere; lines in
 // parts past the caches are slower than within them).  One wave.
 template <class E>
-__device__ __forceinline__ void zero_rows(E* table, const int32_t* start, int n_vocab, int k, int v0, int many) {
+__device__ __forceinline__ void zero_rows(E* table, const Run* run, int n_vocab, int k, int v0, int many) {
   const int lane = threadIdx.x & 63;
   if (v0 >= n_vocab) return;
   const int n = n_vocab - v0 < many ? n_vocab - v0 : many;
-  uint64_t empty = __ballot(lane < n && start[v0 + (lane < n ? lane : 0)] == start[v0 + (lane < n ? lane : 0) + 1]);
+  const Run mine = run[v0 + (lane < n ? lane : 0)];
+  uint64_t empty = __ballot(lane < n && mine.begin == mine.end);
   while (empty) {
     const int from = __builtin_ctzll(empty);
     const uint64_t rest = ~(empty >> from);
@@ -317,12 +324,12 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
   if constexpr (!ADD) {
     if ((int)blockIdx.x >= work) {               // rows without a token
       const int wave = ((int)blockIdx.x - work) * (int)(blockDim.x >> 6) + (int)(threadIdx.x >> 6);
-      zero_rows(table, a.o.start, a.n_vocab, a.k, wave * a.zero_rows, a.zero_rows);
+      zero_rows(table, a.o.run, a.n_vocab, a.k, wave * a.zero_rows, a.zero_rows);
       return;
     }
   }
   const int seg = (int)blockIdx.x / a.chunks, chunk = (int)blockIdx.x - seg * a.chunks;
-  const int total = a.o.start[a.n_vocab], S = a.segment;
+  const int total = a.o.run[a.n_vocab].end, S = a.segment;
   const int i0 = seg * S;
   if (i0 >= total) return;
   const int i1 = i0 + S < total ? i0 + S : total;
@@ -331,7 +338,7 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
   // the tokens of this segment: from the first run that begins in it (or from
   // its start, inside a long run) to the end of the last one that begins in it
   // (or to its own end, inside a long run)
-  const Run head = run_of(a.o, a.o.key[i0]), tail = run_of(a.o, a.o.key[i1 - 1]);
+  const Run head = a.o.run[a.o.key[i0]], tail = a.o.run[a.o.key[i1 - 1]];
   const bool long_head = head.begin < i0 && head.end - head.begin > S;
   const bool long_tail = tail.end > i1 && tail.end - tail.begin > S;
   const int from = head.begin == i0 || long_head ? i0 : head.end;
@@ -386,12 +393,12 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
 template <int TT, int V, bool ADD, bool LINES> __global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
   typedef typename Mem<TT>::E ET;
   const int seg = (int)blockIdx.x / a.chunks, chunk = (int)blockIdx.x - seg * a.chunks;
-  const int total = a.o.start[a.n_vocab], S = a.segment;
+  const int total = a.o.run[a.n_vocab].end, S = a.segment;
   const int i0 = seg * S;
   if (i0 >= total) return;
   const int i1 = i0 + S < total ? i0 + S : total;
   const int v = a.o.key[i1 - 1];
-  const Run r = run_of(a.o, v);
+  const Run r = a.o.run[v];
   if (r.begin < i0 || r.end <= i1 || r.end - r.begin <= S) return;
   if ((int)threadIdx.x >= a.chunk_vecs) return;
   const Place c = place<V>((chunk * a.chunk_vecs + (int)threadIdx.x) * V, a.k);
@@ -423,18 +430,19 @@ constexpr int64_t kAlign = 256;
 int64_t rounded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
 struct Plan {
-  int range, groups;                             // ids per sorting workgroup
+  int bits, range, groups;                       // sorting workgroups: at most 2^bits, of `range` ids
   int vec;                                       // columns per thread
   int chunks, chunk_vecs, threads;
   int segment, segments;
-  int64_t start, key, pos, part, bytes;          // the workspace
+  int64_t run, key, pos, part, bytes;          // the workspace
 };
 
 Plan plan_of(int64_t m_tok, int64_t n_vocab, int64_t k, int dout_type) {
   Plan p{};
-  p.range = (int)((n_vocab + 255) / 256);
-  if (p.range > kMaxRange) p.range = kMaxRange;
-  p.groups = (int)((n_vocab + p.range - 1) / p.range);
+  p.bits = 8;
+  while ((n_vocab - 1) >> p.bits >= kMaxRange) ++p.bits;   // a wave remembers d in 10 bits
+  p.range = (int)(((n_vocab - 1) >> p.bits) + 1);
+  p.groups = (int)(n_vocab < int64_t(1) << p.bits ? n_vocab : int64_t(1) << p.bits);
   p.vec = dout_type == kFp32 ? 4 : 8;
   if (k < p.vec) p.vec = 1;
   const int64_t nv = (k + p.vec - 1) / p.vec;
@@ -453,7 +461,7 @@ Plan plan_of(int64_t m_tok, int64_t n_vocab, int64_t k, int dout_type) {
     at += rounded(bytes);
     return o;
   };
-  p.start = take((n_vocab + 1) * 4);
+  p.run = take((n_vocab + 1) * 8);
   p.key = take(m_tok * 4);
   p.pos = take(m_tok * 4);
   p.part = take((int64_t)p.segments * 2 * k * 4);
@@ -498,9 +506,13 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
   }
   const Plan p = plan_of(g.m_tok, g.n_vocab, g.k, td);
   uint8_t* ws = static_cast<uint8_t*>(g.ws);
-  const Order o{reinterpret_cast<int32_t*>(ws + p.start), reinterpret_cast<int32_t*>(ws + p.key),
+  const Order o{reinterpret_cast<Run*>(ws + p.run), reinterpret_cast<int32_t*>(ws + p.key),
                 reinterpret_cast<int32_t*>(ws + p.pos)};
-  const SortArgs sa{g.ids, (int32_t)g.m_tok, (int32_t)g.n_vocab, p.range, o};
+  const SortArgs sa{g.ids, (int32_t)g.m_tok, (int32_t)g.n_vocab, p.bits, p.range, o};
+  // more dynamic LDS than the default limit: raised once
+  static const bool raised = hipFuncSetAttribute((const void*)sort_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kSortWaves * kMaxRange * 4) == hipSuccess;
+  (void)raised;
   hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
   // rows to zero: a few of each wave, so that there are many waves; at most 64 (the bits of a mask)
   int64_t zero_rows = 4;

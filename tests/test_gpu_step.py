@@ -335,6 +335,15 @@ def test_embedding_backward_matches_oracle(t, v, k, tt, to, skew):
         assert torch.equal(again, d)
 
 
+# one id, two and 1024 of each sorting workgroup, one more than that; ids that a wave remembers and more
+@pytest.mark.parametrize("tt,to", [("bfloat16", "bfloat16"), ("float32", "float16")])
+@pytest.mark.parametrize("skew", [1, 9])
+@pytest.mark.parametrize("t,v", [(5000, 255), (5000, 256), (20000, 257), (13000, 4097), (5000, 262143), (5000, 262144),
+                                 (5000, 262145), (60000, 131072)])
+def test_embedding_backward_around_the_sorts_ranges(t, v, skew, tt, to):
+    test_embedding_backward_matches_oracle(t, v, 5, tt, to, skew)
+
+
 @pytest.mark.parametrize("add", [False, True])
 @pytest.mark.parametrize("t", [1, 7, 8, 9, 16, 17, 63, 64, 65, 640, 1000, 4096])
 def test_embedding_backward_of_one_id(t, add):
