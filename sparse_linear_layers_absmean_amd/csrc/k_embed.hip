@@ -20,6 +20,10 @@
 //     segments' borders into fp32 partial rows.  Rows without a token are
 //     zeroed by further workgroups of the launch (not when adding).
 //  3. join_kernel: the partial rows of each long run, in order.
+// Measured: 65536 tokens of 32000 ids x 3200 BF16 18 + 132 + 6 us (4.7 TB/s in
+// sum_kernel); 16384 of 128256 x 5120, added, from fp32, 10 + 95 + 5 (5.1).
+// sort_kernel's bound is every workgroup's pass over all ids (8 bytes each, from
+// L2): 262144 tokens 51 us at least.
 #include "sbl_step.h"
 
 namespace sbl {

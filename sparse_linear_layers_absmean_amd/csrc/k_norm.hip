@@ -14,10 +14,12 @@
 //   dx = rstd (g - center * mean(g) - xh mean(g xh)),  dw = sum_t dy xh,  db = sum_t dy.
 // Both are bound by memory: x (and dy) read once, the outputs written once.
 // A row lies in the registers of one workgroup from its load to its store;
-// workgroups go over rows, so that weights stay in registers, the next row's
-// loads are in flight while a row is reduced, and the backward's column sums
-// need no memory until the end (one partial row per workgroup, joined in a
-// fixed order by a second launch).
+// workgroups go over rows, so that the next row's loads are in flight while a
+// row is reduced, and the backward's column sums need no memory until the end
+// (one partial row per workgroup, joined in a fixed order by a second launch).
+// Measured, with a large copy at 4.9 TB/s: forward 4096 x 5120 BF16 to fp32 and
+// int8 26 us, 5.7 TB/s; 16384 x 8192 BF16 108 us, 5.0; backward 8192 x 5120 of BF16
+// x and fp32 dy 64 us, 5.2, and 6 for joining the parts.
 #include <algorithm>
 
 #include "sbl_actq.h"
@@ -459,7 +461,8 @@ __global__ __launch_bounds__(MOST) void norm_grad_kernel(const NormGradArgs a, f
 }
 
 // Longer rows: the two means of every row first (one workgroup per row), then
-// every column by a thread of its own, which needs no other.
+// every column by a thread of its own, which needs no other.  x and dy are read
+// twice: 4096 x 28672 of BF16 x and fp32 dy 367 us, 1.9 times its bytes' time.
 template <int TX, int TD>
 __global__ __launch_bounds__(1024) void norm_grad_rows_kernel(const NormGradArgs a, float2* means) {
   __shared__ Pair part[kMaxWaves];
