@@ -553,7 +553,7 @@ int sbl_head_kd_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w,
  *   gamma = max_k |y|,  xq = clamp(rint(RN(y / (max(gamma, 1e-5) / 128))), -127, 127)
  *   x          [m_tok][k], x_dtype (SBL_BF16, SBL_FP16 or SBL_FP32).
  *   weight, bias  [k] fp32, or NULL (1 and 0).
- *   eps        > 0.
+ *   eps        finite, above 0 as an fp32 number.
  *   y          [m_tok][k] output, or NULL: y_dtype is x_dtype, or one of the two
  *              is SBL_FP32; y is rounded once more to a 16-bit type (xq and gamma
  *              come from the fp32 value).

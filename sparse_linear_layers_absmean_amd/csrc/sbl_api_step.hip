@@ -61,7 +61,7 @@ extern "C" {
 int sbl_norm_forward(const void* x, int32_t x_dtype, const float* weight, const float* bias, int64_t m_tok, int64_t k,
                      double eps, int32_t center, void* y, int32_t y_dtype, int8_t* xq, float* gamma, float* mean,
                      float* rstd, sbl_stream stream) {
-  if (!rows_ok(m_tok, k) || !(eps > 0.0) || !std::isfinite(eps)) return SBL_ERR_SHAPE;
+  if (!rows_ok(m_tok, k) || !((float)eps > 0.0f) || !std::isfinite(eps)) return SBL_ERR_SHAPE;
   if (!pair_ok(x_dtype, y_dtype)) return SBL_ERR_UNSUPPORTED;
   if ((xq || gamma) && k % 64 != 0) return SBL_ERR_SHAPE;
   if (m_tok == 0) return SBL_OK;

@@ -261,6 +261,63 @@ def test_norm_backward_is_the_forwards_slope():
             assert abs((up - loss(*args)) / (2 * h) - float(grad[j])) < h * h * 10 + 64 * 4 * S.U32 * 4 / (2 * h)
 
 
+def _at(values, off):
+    """A tensor that begins `off` elements into a larger one of NaNs."""
+    import torch
+    raw = torch.full((values.numel() + off + 64,), float("nan"), dtype=values.dtype, device="cuda")
+    view = raw[off:off + values.numel()].view(values.shape)
+    view.copy_(values)
+    return view
+
+
+@pytest.mark.parametrize("tx,ty", [("bfloat16", "float32"), ("float32", "float32"), ("float16", "float16")])
+@pytest.mark.parametrize("t,k", [(3, 2), (5, 63), (2, 4096), (1100, 5120), (1100, 8640), (2, 33000)])
+def test_norm_of_tensors_anywhere_in_a_buffer(t, k, tx, ty):
+    """Parameters and statistics at any 4 bytes, rows at any 16: the results of aligned ones (outputs that then are no
+    whole lines are stored otherwise), and nothing beside them is read or written."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    say(f"norm anywhere t={t} k={k} {tx} {ty}")
+    rng, x, _, w, b = _norm_inputs(t, k, tx, [88, t, k])
+    dy = _dev(rng.standard_normal((t, k)), ty)[0]
+    w, b, to = _f32(w), _f32(b), _type(ty)
+    y, mean, rstd = sbl.norm(x, w, b, dtype=to)
+    want = sbl.norm_backward(dy, x, mean, rstd, w, want_bias=True)
+    rows = 16 // x.element_size(), 16 // y.element_size()
+    x2, dy2, w2, b2 = _at(x, rows[0]), _at(dy, 3 * rows[1]), _at(w, 1), _at(b, 3)
+    out = Guarded()
+    y2, mean2, rstd2 = out.new((t, k), ty, at=272), out.new((t,), "float32", at=268), out.new((t,), "float32", at=260)
+    sbl.sbl_norm_forward(x2, w2, b2, y=y2, mean=mean2, rstd=rstd2)
+    for got, ref in ((y2, y), (mean2, mean), (rstd2, rstd)):
+        assert torch.equal(got, ref)
+    dx2, dw2, db2 = out.new((t, k), tx, at=304), out.new((k,), "float32", at=260), out.new((k,), "float32", at=268)
+    sbl.sbl_norm_backward(dy2, x2, mean2, rstd2, w2, dx2, dw2, db2, sbl.new_norm_workspace(t, k))
+    for got, ref in zip((dx2, dw2, db2), want):
+        assert torch.equal(got, ref)
+    out.check()
+
+
+@pytest.mark.parametrize("t,k", [(5, 64), (1500, 512), (1100, 5120), (3, 40000 // 64 * 64)])
+def test_norm_of_rows_that_are_not_finite(t, k):
+    """They spoil nothing but themselves."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    rng, x, _, w, b = _norm_inputs(t, k, "bfloat16", [89, t, k])
+    w, b = _f32(w), _f32(b)
+    dy = _dev(rng.standard_normal((t, k)), "float32")[0]
+    want = sbl.norm_quant(x, w, b, dtype=torch.float32)
+    gx = sbl.norm_backward(dy, x, want[3], want[4], w)[0]
+    bad = torch.tensor([1, t - 1], device="cuda")
+    x[1, k // 2], x[t - 1, 0] = float("nan"), float("inf")
+    got = sbl.norm_quant(x, w, b, dtype=torch.float32)
+    keep = torch.ones(t, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    for a, r in zip(got, want):
+        assert torch.equal(a[keep], r[keep])
+    assert not torch.isfinite(got[2][bad]).any()
+    assert torch.equal(sbl.norm_backward(dy, x, got[3], got[4], w)[0][keep], gx[keep])
+
+
 def test_norm_of_no_rows():
     import torch
     from sparse_linear_layers_absmean_amd import sbl

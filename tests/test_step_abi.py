@@ -57,7 +57,7 @@ def test_refusals_of_both_norm_calls(lib, call, kw, status):
 
 @needs_no_gpu
 @pytest.mark.parametrize("kw,status", [
-    (dict(eps=0.0), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=NAN), SHAPE), (dict(eps=INF), SHAPE),
+    (dict(eps=0.0), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=NAN), SHAPE), (dict(eps=INF), SHAPE), (dict(eps=1e-60), SHAPE),
     (dict(xt=0, yt=1), UNSUPPORTED), (dict(xt=1, yt=0), UNSUPPORTED), (dict(xt=1, yt=3), UNSUPPORTED),
     (dict(k=65), SHAPE), (dict(k=32), SHAPE), (dict(xq=None), NULL), (dict(gamma=None), NULL),
     (dict(y=D + 8), ALIGN), (dict(xq=E + 8), ALIGN), (dict(gamma=F + 2), ALIGN), (dict(b=C + 1), ALIGN),
