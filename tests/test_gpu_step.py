@@ -418,6 +418,32 @@ def test_embedding_backward_of_one_id(t, add):
         _same(d, want.to(torch.bfloat16), "dtable")
 
 
+@pytest.mark.parametrize("tt,to", [("bfloat16", "bfloat16"), ("float32", "float16"), ("float16", "float32")])
+@pytest.mark.parametrize("t,v,k", [(9, 20, 3), (4500, 700, 1024), (1200, 3000, 8640), (5000, 300, 1541)])
+def test_embedding_of_tensors_anywhere_in_a_buffer(t, v, k, tt, to):
+    """Rows at any 16 bytes: the results of aligned tensors, and nothing beside them is read or written."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    say(f"embed anywhere t={t} v={v} k={k} {tt} {to}")
+    rng = np.random.default_rng([90, t, v, k])
+    table, dout = _dev(rng.standard_normal((v, k)), tt)[0], _dev(rng.standard_normal((t, k)), to)[0]
+    ids = _i64(_ids(rng, t, v, 3))
+    table2, dout2 = _at(table, 16 // table.element_size()), _at(dout, 48 // dout.element_size())
+    ids2 = torch.full((t + 3,), 1, dtype=torch.int64, device="cuda")[1:t + 1].copy_(ids)
+    out = Guarded()
+    rows = out.new((t, k), to, at=272)
+    sbl.sbl_embed_forward(ids2, table2, rows, 1.5)
+    _same(rows, sbl.embed(ids, table, 1.5, dtype=_type(to)).cpu(), "rows")
+    ws = sbl.new_embed_workspace(t, v, k, _type(to))
+    for add in (False, True):
+        want = table.clone()
+        sbl.sbl_embed_backward(ids, dout, want, ws, 0.7, add)
+        grad = out.new((v, k), tt, at=304, fill=table)
+        sbl.sbl_embed_backward(ids2, dout2, grad, ws, 0.7, add)
+        assert torch.equal(grad, want)
+    out.check()
+
+
 def test_embedding_of_no_tokens_and_any_shape():
     import torch
     from sparse_linear_layers_absmean_amd import sbl
