@@ -5,7 +5,8 @@
 //
 // Backward: dtable[v] = scale * sum of dout[t] over the tokens t with id[t] = v,
 // in fp32, in ascending t, rounded once (added to what dtable holds first, if
-// asked).  Without atomics on floats, so results repeat bit for bit:
+// asked).  Without atomics on floats, so results repeat bit for bit.  Few tokens:
+// few_kernel alone.  More:
 //  1. sort_kernel: the tokens id by id, equal ids in order of t (`pos`, with
 //     their ids `key`), and where each id's run lies (`run`).  Of 2^s workgroups
 //     each owns the ids of one remainder by 2^s (neighbouring ids are often
@@ -265,7 +266,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const SortArgs a) {
 
 // ---------------------------------------------------------------- backward: sums
 
+// Up to here few_kernel.  777 tokens of 50257 ids x 1541 FP16 33 us, by the three
+// kernels 39; 256 of 32000 x 3200, added, 11 and 18; but all of one id 23 and 14
+// (1024 tokens x 3200: 108 and 26), for one workgroup then adds them up.
+constexpr int kFewTokens = 1024;
+
 struct SumArgs {
+  const int64_t* ids;
   const void* dout;
   void* dtable;
   int32_t m_tok, n_vocab, k;
@@ -290,17 +297,12 @@ __device__ __forceinline__ void put(typename Mem<TT>::E* row, Place c, const flo
   store_own<TT, V, LINES>(row, c, f);
 }
 
-// Zeros in those of `many` (at most 64) rows from row v0 on that have no token.
-// Neighbouring ones are one stretch of memory, whose 128-byte lines are stored
-// whole and past the caches (rows of an odd length begin anywhere; lines in
-// parts past the caches are slower than within them).  One wave.
-template <class E>
-__device__ __forceinline__ void zero_rows(E* table, const Run* run, int n_vocab, int k, int v0, int many) {
+// Zeros in the rows v0 + i of the bits i of `empty`.  Neighbouring ones are one
+// stretch of memory, whose 128-byte lines are stored whole and past the caches
+// (rows of an odd length begin anywhere; lines in parts past the caches are slower
+// than within them).  One wave.
+template <class E> __device__ __forceinline__ void zero_rows(E* table, uint64_t empty, int k, int v0) {
   const int lane = threadIdx.x & 63;
-  if (v0 >= n_vocab) return;
-  const int n = n_vocab - v0 < many ? n_vocab - v0 : many;
-  const Run mine = run[v0 + (lane < n ? lane : 0)];
-  uint64_t empty = __ballot(lane < n && mine.begin == mine.end);
   while (empty) {
     const int from = __builtin_ctzll(empty);
     const uint64_t rest = ~(empty >> from);
@@ -328,7 +330,10 @@ template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bound
   if constexpr (!ADD) {
     if ((int)blockIdx.x >= work) {               // rows without a token
       const int wave = ((int)blockIdx.x - work) * (int)(blockDim.x >> 6) + (int)(threadIdx.x >> 6);
-      zero_rows(table, a.o.run, a.n_vocab, a.k, wave * a.zero_rows, a.zero_rows);
+      const int v0 = wave * a.zero_rows, left = a.n_vocab - v0, n = left < a.zero_rows ? left : a.zero_rows;
+      if (n <= 0) return;
+      const Run mine = a.o.run[v0 + (lane < n ? lane : 0)];
+      zero_rows(table, __ballot(lane < n && mine.begin == mine.end), a.k, v0);
       return;
     }
   }
@@ -423,6 +428,77 @@ template <int TT, int V, bool ADD, bool LINES> __global__ __launch_bounds__(kThr
   put<TT, V, ADD, LINES>(row, c, sum, a.scale, old);
 }
 
+// Few tokens: the whole gradient in one launch, without an order.  A workgroup per
+// token and chunk of columns looks for the token's id among all ids; the first
+// token of an id sums those of all.
+template <int TD, int TT, int V, bool ADD, bool LINES> __global__ __launch_bounds__(kThreads) void few_kernel(const SumArgs a) {
+  typedef typename Mem<TT>::E ET;
+  __shared__ int32_t key[kFewTokens];
+  __shared__ uint16_t same[kFewTokens];          // tokens of this workgroup's id, in order
+  __shared__ int many;
+  ET* table = static_cast<ET*>(a.dtable);
+  const int lane = threadIdx.x & 63, work = a.m_tok * a.chunks;
+  for (int t = threadIdx.x; t < a.m_tok; t += blockDim.x) {
+    const int64_t id = a.ids[t];
+    key[t] = id >= 0 && id < a.n_vocab ? (int32_t)id : -1;
+  }
+  __syncthreads();
+  if constexpr (!ADD) {
+    if ((int)blockIdx.x >= work) {               // rows without a token
+      const int wave = ((int)blockIdx.x - work) * (int)(blockDim.x >> 6) + (int)(threadIdx.x >> 6);
+      const int v0 = wave * a.zero_rows, left = a.n_vocab - v0, n = left < a.zero_rows ? left : a.zero_rows;
+      if (n <= 0) return;
+      uint64_t seen = 0;
+      for (int t = lane; t < a.m_tok; t += 64) {
+        const uint32_t d = (uint32_t)(key[t] - v0);
+        if (key[t] >= v0 && d < 64) seen |= uint64_t(1) << d;
+      }
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) seen |= (uint64_t)__shfl_xor((unsigned long long)seen, m, 64);
+      zero_rows(table, ~seen & (n < 64 ? (uint64_t(1) << n) - 1 : ~uint64_t(0)), a.k, v0);
+      return;
+    }
+  }
+  const int token = (int)blockIdx.x / a.chunks, chunk = (int)blockIdx.x - token * a.chunks, v = key[token];
+  if (v < 0) return;
+  if (threadIdx.x < 64) {
+    int n = 0;
+    for (int t = 0; t < a.m_tok; t += 64) {
+      const uint64_t hit = __ballot(t + lane < a.m_tok && key[t + lane < a.m_tok ? t + lane : 0] == v);
+      if (hit >> lane & 1) same[n + __builtin_popcountll(hit & lanes_below())] = (uint16_t)(t + lane);
+      n += __builtin_popcountll(hit);
+    }
+    if (lane == 0) many = n;
+  }
+  __syncthreads();
+  if (same[0] != token) return;
+  const Place c = place<V>((int)threadIdx.x < a.chunk_vecs ? (chunk * a.chunk_vecs + (int)threadIdx.x) * V : a.k + V, a.k);
+  const typename Mem<TD>::E* dout = static_cast<const typename Mem<TD>::E*>(a.dout);
+  ET* row = table + (int64_t)v * a.k;
+  Vec<TT, V> old{};
+  if constexpr (ADD) old = load<TT, V>(at_col(row, c.col));
+  float sum[V] = {};
+  constexpr int U = 8;                           // tokens whose loads are in flight
+  for (int i = 0; i < many; i += 64) {
+    const int n = many - i < 64 ? many - i : 64, pos = lane < n ? same[i + lane] : 0;
+    for (int j = 0; j < n; j += U) {
+      Vec<TD, V> d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j + u >= n) break;
+        d[u] = load_once<TD, V>(at_col(dout + (int64_t)__builtin_amdgcn_readlane(pos, j + u) * a.k, c.col));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j + u >= n) break;
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] += d[u][e];
+      }
+    }
+  }
+  put<TT, V, ADD, LINES>(row, c, sum, a.scale, old);
+}
+
 // `words` 16-bit zeros, 16-byte aligned
 __global__ __launch_bounds__(kThreads) void zero_kernel(uint16_t* p, int64_t words) {
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -473,22 +549,27 @@ Plan plan_of(int64_t m_tok, int64_t n_vocab, int64_t k, int dout_type) {
   return p;
 }
 
-template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const SumArgs& a, bool join, hipStream_t s) {
+template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const SumArgs& a, bool few, bool join, hipStream_t s) {
   const dim3 block((unsigned)((a.chunk_vecs + 63) / 64 * 64)), work((unsigned)(a.segments * a.chunks));
-  hipLaunchKernelGGL((sum_kernel<TD, TT, V, ADD, LINES>), dim3(work.x + (ADD ? 0u : (unsigned)a.zero_groups)), block, 0, s, a);
+  const unsigned zero = ADD ? 0u : (unsigned)a.zero_groups;
+  if (few) {
+    hipLaunchKernelGGL((few_kernel<TD, TT, V, ADD, LINES>), dim3((unsigned)(a.m_tok * a.chunks) + zero), block, 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((sum_kernel<TD, TT, V, ADD, LINES>), dim3(work.x + zero), block, 0, s, a);
   if (join) hipLaunchKernelGGL((join_kernel<TT, V, ADD, LINES>), work, block, 0, s, a);
   return hipGetLastError();
 }
 
-template <int TD, int TT, int V, bool ADD> hipError_t by_row_length(const SumArgs& a, bool join, hipStream_t s) {
-  if (a.k < V) return sums<TD, TT, 1, ADD, false>(a, join, s);
+template <int TD, int TT, int V, bool ADD> hipError_t by_row_length(const SumArgs& a, bool few, bool join, hipStream_t s) {
+  if (a.k < V) return sums<TD, TT, 1, ADD, false>(a, few, join, s);
   if (a.k * type_bytes(TT) % 128 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 128 == 0)
-    return sums<TD, TT, V, ADD, true>(a, join, s);
-  return sums<TD, TT, V, ADD, false>(a, join, s);
+    return sums<TD, TT, V, ADD, true>(a, few, join, s);
+  return sums<TD, TT, V, ADD, false>(a, few, join, s);
 }
 
-template <int TD, int TT, int V> hipError_t backward(const SumArgs& a, bool add, bool join, hipStream_t s) {
-  return add ? by_row_length<TD, TT, V, true>(a, join, s) : by_row_length<TD, TT, V, false>(a, join, s);
+template <int TD, int TT, int V> hipError_t backward(const SumArgs& a, bool add, bool few, bool join, hipStream_t s) {
+  return add ? by_row_length<TD, TT, V, true>(a, few, join, s) : by_row_length<TD, TT, V, false>(a, few, join, s);
 }
 
 }  // namespace
@@ -517,15 +598,16 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
   static const bool raised = hipFuncSetAttribute((const void*)sort_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                                  kSortWaves * kMaxRange * 4) == hipSuccess;
   (void)raised;
-  hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
+  const bool few = g.m_tok <= kFewTokens;
+  if (!few) hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
   // rows to zero: a few of each wave, so that there are many waves; at most 64 (the bits of a mask)
   int64_t zero_rows = 4;
   while (zero_rows < 64 && g.n_vocab / zero_rows > 8192) zero_rows *= 2;
   const int64_t rows = zero_rows * (p.threads / 64), zero = (g.n_vocab + rows - 1) / rows;
-  const SumArgs a{g.dout, g.dtable, (int32_t)g.m_tok, (int32_t)g.n_vocab, g.k, g.scale, p.segment, p.segments, p.chunks,
+  const SumArgs a{g.ids, g.dout, g.dtable, (int32_t)g.m_tok, (int32_t)g.n_vocab, g.k, g.scale, p.segment, p.segments, p.chunks,
                   p.chunk_vecs, (int32_t)zero, (int32_t)zero_rows, o, reinterpret_cast<float*>(ws + p.part)};
   const bool join = g.m_tok > p.segment;         // else no run is longer than a segment
-  return with_types(td, tt, [&](auto d, auto t) { return backward<d.value, t.value, d.value == kFp32 ? 4 : 8>(a, g.add, join, s); });
+  return with_types(td, tt, [&](auto d, auto t) { return backward<d.value, t.value, d.value == kFp32 ? 4 : 8>(a, g.add, few, join, s); });
 }
 
 }  // namespace step

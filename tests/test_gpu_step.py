@@ -395,7 +395,7 @@ def test_embedding_backward_matches_oracle(t, v, k, tt, to, skew):
 # one id, two and 1024 of each sorting workgroup, one more than that; ids that a wave remembers and more
 @pytest.mark.parametrize("tt,to", [("bfloat16", "bfloat16"), ("float32", "float16")])
 @pytest.mark.parametrize("skew", [1, 9])
-@pytest.mark.parametrize("t,v", [(5000, 255), (5000, 256), (20000, 257), (13000, 4097), (5000, 262143), (5000, 262144),
+@pytest.mark.parametrize("t,v", [(5000, 255), (5000, 256), (20000, 257), (13000, 4097), (1024, 300), (1025, 300), (5000, 262143), (5000, 262144),
                                  (5000, 262145), (60000, 131072)])
 def test_embedding_backward_around_the_sorts_ranges(t, v, skew, tt, to):
     test_embedding_backward_matches_oracle(t, v, 5, tt, to, skew)
