@@ -55,8 +55,8 @@ struct Stat {
 // s1, s2: sums of (x - x0) and (x - x0)^2 (not centered: x0 = 0)
 __device__ __forceinline__ Stat statistics(double s1, double s2, double x0, double inv_k, double eps, int center) {
   const double e = center ? s1 * inv_k : 0.0;
-  const double var = fmax(__builtin_fma(-e, e, s2 * inv_k), 0.0);
-  return Stat{x0 + e, (float)rsqrt64(var + eps)};
+  const double var = __builtin_fma(-e, e, s2 * inv_k);
+  return Stat{x0 + e, (float)rsqrt64((var < 0.0 ? 0.0 : var) + eps)};   // a NaN stays one (fmax would make it 0)
 }
 
 template <int T> __device__ __forceinline__ void add_stats(const Vec<T, V>& x, int have, double x0, double& s1, double& s2) {
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
         // not centered: the mean is zero, and the difference x itself
         const float d = a.center ? (float)((double)v[i][j] - st.mean) : v[i][j];
         y[i][j] = d * st.rstd * wi[j] + bi[j];
-        mx = fmaxf(mx, fabsf(y[i][j]));          // a column seen twice does not change the largest
+        mx = larger(mx, fabsf(y[i][j]));         // a column seen twice does not change the largest
       }
       if (a.y) store_own<TY, W, ROWS != kAny>(static_cast<EY*>(a.y) + base, c, y[i]);
     }
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
         if ((tid & 63) == 0) peak[p][wave] = mx;
         __syncthreads();
         float g = peak[p][0];
-        for (int i = 1; i < waves; ++i) g = fmaxf(g, peak[p][i]);
+        for (int i = 1; i < waves; ++i) g = larger(g, peak[p][i]);
         const actq::Step sp = actq::make_step(g);
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i)
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
     value(c, y);
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (c + j < k) mx = fmaxf(mx, fabsf(y[j]));
+      if (c + j < k) mx = larger(mx, fabsf(y[j]));
     if (a.y) store<TY, V>(static_cast<EY*>(a.y) + base + c, y, k - c);
   }
   if (tid == 0) {
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
   if ((tid & 63) == 0) peak[wave] = mx;
   __syncthreads();
   float g = peak[0];
-  for (int i = 1; i < kMaxWaves; ++i) g = fmaxf(g, peak[i]);
+  for (int i = 1; i < kMaxWaves; ++i) g = larger(g, peak[i]);
   const actq::Step sp = actq::make_step(g);
   for (int c = tid * V; c < k; c += 1024 * V) {
     float y[V];

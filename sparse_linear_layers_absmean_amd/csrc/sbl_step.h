@@ -288,12 +288,14 @@ template <class F> __device__ __forceinline__ F wave_sum(F x) {
   x += dpp<0x140, 0xf>(x, (F)0);                // row_mirror
   return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }
+// the larger of two, NaN if either is (v_maximum3_f32; fmaxf would drop it)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_max(float x) {
-  x = fmaxf(x, dpp<0xB1, 0xf>(x, x));
-  x = fmaxf(x, dpp<0x4E, 0xf>(x, x));
-  x = fmaxf(x, dpp<0x141, 0xf>(x, x));
-  x = fmaxf(x, dpp<0x140, 0xf>(x, x));
-  return fmaxf(fmaxf(lane_value(x, 0), lane_value(x, 16)), fmaxf(lane_value(x, 32), lane_value(x, 48)));
+  x = larger(x, dpp<0xB1, 0xf>(x, x));
+  x = larger(x, dpp<0x4E, 0xf>(x, x));
+  x = larger(x, dpp<0x141, 0xf>(x, x));
+  x = larger(x, dpp<0x140, 0xf>(x, x));
+  return larger(larger(lane_value(x, 0), lane_value(x, 16)), larger(lane_value(x, 32), lane_value(x, 48)));
 }
 
 }  // namespace step
