@@ -634,7 +634,8 @@ int sbl_embed_backward(const int64_t* ids, const void* dout, int32_t dout_dtype,
  *   w          [n] weights, w_dtype (SBL_BF16, SBL_FP16 or SBL_FP32), in place.
  *   w_low      [n] int16 or NULL, for SBL_BF16 alone: the low bits of an fp32
  *              weight whose bits are (w << 16) + w_low (w the nearest BF16 value,
- *              ties away from zero, so -2^15 <= w_low < 2^15), in place.  Without
+ *              ties away from zero, so -2^15 <= w_low < 2^15; a NaN is written
+ *              as 0x7FC0 and 0), in place.  Without
  *              it an update below half a BF16 step is lost.
  *   g          [n] gradient, g_dtype (any of the three).
  *   m, v       the states, in place.  state_bits 32: [n] fp32.  state_bits 8:

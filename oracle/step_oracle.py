@@ -176,8 +176,9 @@ def dither(n, seed):
 # ---------------------------------------------------------------- AdamW
 
 def split_master(w):
-    """(BF16 bits, low bits): nearest BF16, ties away from zero."""
-    bits = np.asarray(w, F32).view(np.uint32).astype(np.int64)
+    """(BF16 bits, low bits): nearest BF16, ties away from zero; one NaN for all."""
+    w = np.asarray(w, F32)
+    bits = np.where(np.isnan(w), np.int64(0x7FC00000), w.view(np.uint32).astype(np.int64))
     high = (bits + 0x8000) >> 16
     return high.astype(np.uint16), (bits - (high << 16)).astype(np.int16)
 

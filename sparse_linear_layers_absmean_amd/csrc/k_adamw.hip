@@ -8,7 +8,7 @@
 //
 // Weights.  BF16 masters may carry the 16 bits that BF16 drops: the pair is an
 // fp32 number whose bits are (high << 16) + low, high the nearest BF16 value
-// (ties away from zero), low in [-2^15, 2^15).  An update far below half a
+// (ties away from zero), low in [-2^15, 2^15); a NaN is 0x7FC0 and 0.  An update far below half a
 // BF16 step is then kept, at 4 bytes a weight instead of 6 for an fp32 copy.
 //
 // States in 8 bits: blocks of 256 consecutive values of a tensor share an fp32
@@ -72,7 +72,8 @@ __device__ __forceinline__ float join(uint16_t high, int16_t low) {
   return __builtin_bit_cast(float, ((uint32_t)high << 16) + (uint32_t)(int32_t)low);
 }
 __device__ __forceinline__ void split(float w, uint16_t& high, int16_t& low) {
-  const uint32_t bits = __builtin_bit_cast(uint32_t, w);
+  // one NaN for all: the carry would run through another's exponent and sign (0x7FFFE000 would be -0 and its low bits)
+  const uint32_t bits = w == w ? __builtin_bit_cast(uint32_t, w) : 0x7FC00000u;
   high = (uint16_t)((bits + 0x8000u) >> 16);
   low = (int16_t)(uint16_t)(bits & 0xFFFFu);     // bits - (high << 16) modulo 2^16
 }

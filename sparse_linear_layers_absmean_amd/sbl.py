@@ -1046,8 +1046,9 @@ def embed_backward(ids, dout, n_vocab: int, scale: float = 1.0, dtype=None, add_
 
 
 def split_master(w32):
-    """An fp32 weight as BF16 master and int16 low bits: (w, w_low), nearest BF16, ties away from zero."""
-    bits = w32.contiguous().view(torch.int32)
+    """An fp32 weight as BF16 master and int16 low bits: (w, w_low), nearest BF16, ties away from zero; a NaN as the
+    BF16 0x7FC0 and 0."""
+    bits = w32.contiguous().view(torch.int32).masked_fill(torch.isnan(w32), 0x7FC00000)
     high = (bits + 0x8000) >> 16
     return high.to(torch.int16).view(torch.bfloat16), (bits - (high << 16)).to(torch.int16)
 
