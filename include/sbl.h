@@ -553,7 +553,8 @@ int sbl_head_kd_backward(const uint16_t* h, int64_t h_stride, const uint16_t* w,
  *   gamma = max_k |y|,  xq = clamp(rint(RN(y / (max(gamma, 1e-5) / 128))), -127, 127)
  * A row of x with a value that is not finite: its y, rstd and gamma are NaN, its
  * codes anything; the other rows are what they would be.  A NaN in weight or bias
- * is in its column of y and in every gamma.
+ * is in its column of y and in every gamma.  Products (sbl_linear*) make a row of
+ * NaNs of a token whose gamma is NaN, sbl_linear_backward* a dw of NaNs.
  *   x          [m_tok][k], x_dtype (SBL_BF16, SBL_FP16 or SBL_FP32).
  *   weight, bias  [k] fp32, or NULL (1 and 0).
  *   eps        finite, above 0 as an fp32 number.

@@ -324,7 +324,7 @@ __global__ __launch_bounds__(kBT * NW) void backward_dw_kernel(const uint16_t* _
       if (t < m_tok && kk < k) {
 #pragma unroll
         for (int w = 0; w < kJ / 4; ++w) qv[tt][w] = reinterpret_cast<const uint32_t*>(xq + t * k + kk)[w];
-        ge[tt] = fmaxf(gamma[t], 1e-5f);
+        ge[tt] = gamma_eff(gamma[t]);
       }
     }
   };
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(256) void bwd_xhat_t_kernel(const int8_t* __restric
   float ge = 0.0f;
   if (t0 + t < m_tok) {
     qv = *reinterpret_cast<const u32x4*>(xq + (t0 + t) * k + k0 + 16 * c);
-    ge = fmaxf(gamma[t0 + t], 1e-5f);
+    ge = gamma_eff(gamma[t0 + t]);
   }
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {

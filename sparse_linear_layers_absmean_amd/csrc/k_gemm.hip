@@ -330,7 +330,7 @@ __global__ __launch_bounds__(kThreads * WT, KRT * KCT * WT >= 16 ? 1 : 2) void g
   // output scale per token of the tile; with beta per row group (group
   // scales) the token's max(gamma, 1e-5), the scale being formed per row
   for (int i = tid; i < kBN; i += kThr)
-    scale_lds[i] = t0 + i >= d.m_tok ? 0.0f : GRP ? fmaxf(d.gamma[t0 + i], 1e-5f) : out_scale(d.beta, d.gamma, t0 + i);
+    scale_lds[i] = t0 + i >= d.m_tok ? 0.0f : GRP ? gamma_eff(d.gamma[t0 + i]) : out_scale(d.beta, d.gamma, t0 + i);
   __syncthreads();
   // epilogue: the MFMAs take the activations as A and the weights as B, so
   // lane (li, g) holds C[token 8*(v/4) + 4g + v%4][row li] of each 32 x 32

@@ -299,7 +299,7 @@ __global__ __launch_bounds__(64 * kKgRows) void linear_kgrouped_kernel(
     int s = 0;
     for (int i = 0; i < bpg; ++i) s += kbsum[j * bpg + i];
     const float b = fmaxf(brow[per_block ? j : 0], 1e-5f);
-    const float sc = (b * fmaxf(gamma[t * groups + j], 1e-5f)) * (1.0f / 128.0f);
+    const float sc = (b * gamma_eff(gamma[t * groups + j])) * (1.0f / 128.0f);
     tj = (float)s * sc;
     term[j] = tj;
   }

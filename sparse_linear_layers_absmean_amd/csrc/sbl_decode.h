@@ -25,8 +25,7 @@ __device__ __forceinline__ u32x4 ld16(const void* p) { return *reinterpret_cast<
 
 __device__ __forceinline__ float out_scale_g(const float* beta, float gamma) {
   const float b = fmaxf(beta[0], 1e-5f);
-  const float g = fmaxf(gamma, 1e-5f);
-  return (b * g) * 0.0078125f;   // RN(RN(beta*gamma) * 2^-7); the power of two is exact
+  return (b * gamma_eff(gamma)) * 0.0078125f;   // RN(RN(beta*gamma) * 2^-7); the power of two is exact
 }
 
 __device__ __forceinline__ float out_scale(const float* beta, const float* gamma, int64_t t) {
