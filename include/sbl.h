@@ -250,7 +250,7 @@ int sbl_pack(const int8_t* codes, const uint8_t* mask_bits, int64_t n_out, int64
  *   x      [m_tok][k] fp32 input.
  *   xq     [m_tok][k] int8 output: clamp(rint(x / (max(gamma,1e-5)/128)), -127, 127),
  *          one correctly rounded fp32 division, rint half to even.
- *   gamma  [m_tok] fp32 output: max_k |x[t,k]| (exact).
+ *   gamma  [m_tok] fp32 output: max_k |x[t,k]| (exact; NaN if one of them is).
  * m_tok == 0 is a no-op.
  */
 int sbl_quant_acts(const float* x, int64_t m_tok, int64_t k, int8_t* xq, float* gamma,

@@ -163,13 +163,13 @@ __global__ __launch_bounds__(256) void quant_acts_kgrouped_kernel(const float* _
   const int64_t j = blockIdx.x, t = blockIdx.y, groups = k / kg;
   const float* xr = x + t * k + j * kg;
   float mx = 0.0f;
-  for (int64_t i = threadIdx.x; i < kg; i += 256) mx = fmaxf(mx, fabsf(xr[i]));
+  for (int64_t i = threadIdx.x; i < kg; i += 256) mx = larger(mx, fabsf(xr[i]));
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  for (int off = 32; off > 0; off >>= 1) mx = larger(mx, __shfl_xor(mx, off, 64));
   __shared__ float wmax[4];
   if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = mx;
   __syncthreads();
-  const float g = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+  const float g = larger(larger(wmax[0], wmax[1]), larger(wmax[2], wmax[3]));
   const float sc = fmaxf(g, 1e-5f) * 0.0078125f;
   int8_t* qr = xq + t * k + j * kg;
   for (int64_t i = threadIdx.x; i < kg; i += 256) {

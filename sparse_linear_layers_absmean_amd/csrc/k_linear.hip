@@ -344,8 +344,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_kernel(const GemvLaunch L
       if (i < nxl && o < xbytes) {
         float mx = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, actq::absmax4(xf4[i][j]));
-        atomicMax(&gbits[o / (uint32_t)d.k], __float_as_uint(mx));   // order of non-negative floats = of their bits
+        for (int j = 0; j < 4; ++j) mx = larger(mx, actq::absmax4(xf4[i][j]));
+        atomicMax(&gbits[o / (uint32_t)d.k], __float_as_uint(mx));   // order of non-negative floats = of their bits, a NaN's above all
       }
     }
     __syncthreads();                               // gamma per token

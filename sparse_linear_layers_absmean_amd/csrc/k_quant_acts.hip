@@ -47,24 +47,24 @@ __global__ __launch_bounds__(THREADS) void quant_acts_kernel(const float4* __res
     for (int i = 0; i < PER; ++i)
       v[i] = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(rx, (uint32_t)(tid + i * THREADS) * 16u, 0, kAux));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mx = fmaxf(mx, actq::absmax4(v[i]));
+    for (int i = 0; i < PER; ++i) mx = larger(mx, actq::absmax4(v[i]));
   } else {
     for (int64_t i = tid; i < k4; i += 4 * THREADS) {
       float4 w[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) w[u] = i + u * THREADS < k4 ? xr[i + u * THREADS] : float4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) mx = fmaxf(mx, actq::absmax4(w[u]));
+      for (int u = 0; u < 4; ++u) mx = larger(mx, actq::absmax4(w[u]));
     }
   }
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  for (int off = 32; off > 0; off >>= 1) mx = larger(mx, __shfl_xor(mx, off, 64));
   __shared__ float wmax[kWaves];
   if ((tid & 63) == 0) wmax[tid >> 6] = mx;
   __syncthreads();
   float g = wmax[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) g = fmaxf(g, wmax[i]);
+  for (int i = 1; i < kWaves; ++i) g = larger(g, wmax[i]);
   const actq::Step st = actq::make_step(g);
   if (held) {
 #pragma unroll
@@ -99,15 +99,15 @@ __global__ __launch_bounds__(THREADS) void quant_acts_split_kernel(const float4*
     v[i] = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(rx, (uint32_t)(tid + i * THREADS) * 16u, 0, 0));
   float mx = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) mx = fmaxf(mx, actq::absmax4(v[i]));
+  for (int i = 0; i < PER; ++i) mx = larger(mx, actq::absmax4(v[i]));
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  for (int off = 32; off > 0; off >>= 1) mx = larger(mx, __shfl_xor(mx, off, 64));
   __shared__ float wmax[kWaves];
   if ((tid & 63) == 0) wmax[tid >> 6] = mx;
   __syncthreads();
   float g = wmax[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) g = fmaxf(g, wmax[i]);
+  for (int i = 1; i < kWaves; ++i) g = larger(g, wmax[i]);
   const actq::Step st = actq::make_step(g);
   const int64_t per = (k4 + SPLIT - 1) / SPLIT, i0 = part * per;
   const int64_t i1 = i0 + per < k4 ? i0 + per : k4;

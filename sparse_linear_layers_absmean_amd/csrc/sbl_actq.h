@@ -69,8 +69,9 @@ __device__ __forceinline__ uint32_t q_word(float4 v, const Step& st) {
   return clamp_byte(a) | (clamp_byte(b) << 8) | (clamp_byte(c) << 16) | (clamp_byte(d) << 24);
 }
 
+// NaN if one of the four is
 __device__ __forceinline__ float absmax4(float4 v) {
-  return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+  return larger(larger(fabsf(v.x), fabsf(v.y)), larger(fabsf(v.z), fabsf(v.w)));
 }
 
 }  // namespace actq

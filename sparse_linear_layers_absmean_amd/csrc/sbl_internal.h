@@ -20,9 +20,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, int64
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
 
+// the larger of two, NaN if either is (v_maximum3_f32; fmaxf would drop it)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // max(gamma, 1e-5) of a token's activation scale; a NaN stays one (fmaxf would
 // make it 1e-5, and the token's products small numbers of no meaning)
-__device__ __forceinline__ float gamma_eff(float gamma) { return __builtin_elementwise_maximum(gamma, 1e-5f); }
+__device__ __forceinline__ float gamma_eff(float gamma) { return larger(gamma, 1e-5f); }
 
 // Workspace of the exact beta reduction of one matrix, in 64-bit words
 // (written by the absmean pass of every call, read after it; no state is

@@ -288,8 +288,6 @@ template <class F> __device__ __forceinline__ F wave_sum(F x) {
   x += dpp<0x140, 0xf>(x, (F)0);                // row_mirror
   return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }
-// the larger of two, NaN if either is (v_maximum3_f32; fmaxf would drop it)
-__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_max(float x) {
   x = larger(x, dpp<0xB1, 0xf>(x, x));
   x = larger(x, dpp<0x4E, 0xf>(x, x));
