@@ -25,6 +25,7 @@
 // sum_kernel); 16384 of 128256 x 5120, added, from fp32, 10 + 95 + 5 (5.1).
 // sort_kernel's bound is every workgroup's pass over all ids (8 bytes each, from
 // L2): 262144 tokens 51 us at least.
+#include "sbl_host.h"
 #include "sbl_step.h"
 
 namespace sbl {
@@ -594,12 +595,13 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
   const Order o{reinterpret_cast<Run*>(ws + p.run), reinterpret_cast<int32_t*>(ws + p.key),
                 reinterpret_cast<int32_t*>(ws + p.pos)};
   const SortArgs sa{g.ids, (int32_t)g.m_tok, (int32_t)g.n_vocab, p.bits, p.range, o};
-  // more dynamic LDS than the default limit: raised once
-  static const bool raised = hipFuncSetAttribute((const void*)sort_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                 kSortWaves * kMaxRange * 4) == hipSuccess;
-  (void)raised;
   const bool few = g.m_tok <= kFewTokens;
-  if (!few) hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
+  if (!few) {
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void*)sort_kernel, kSortWaves * kMaxRange * 4);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
+  }
   // rows to zero: a few of each wave, so that there are many waves; at most 64 (the bits of a mask)
   int64_t zero_rows = 4;
   while (zero_rows < 64 && g.n_vocab / zero_rows > 8192) zero_rows *= 2;

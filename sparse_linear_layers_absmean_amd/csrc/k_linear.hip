@@ -27,6 +27,7 @@
 // (grouped GEMV).  Everything integer is exact: |acc| <= 127 k < 2^24.
 #include "sbl_actq.h"
 #include "sbl_decode.h"
+#include "sbl_host.h"
 
 namespace sbl {
 
@@ -585,7 +586,7 @@ int kind_of(int fmt, int n, int m) {
 // slower for N:M, whose decode holds more registers, and for smaller
 // launches).
 template <int KIND>
-void launch_gemv(const GemvLaunch& L, int xlm, bool xf, int spw, bool deep, dim3 grid, dim3 block, size_t lds,
+hipError_t launch_gemv(const GemvLaunch& L, int xlm, bool xf, int spw, bool deep, dim3 grid, dim3 block, size_t lds,
                  hipStream_t s) {
   if (xf) {
     if (spw <= 2) hipLaunchKernelGGL((gemv_kernel<KIND, 1, 2, true>), grid, block, lds, s, L);
@@ -596,18 +597,17 @@ void launch_gemv(const GemvLaunch& L, int xlm, bool xf, int spw, bool deep, dim3
     else if (KIND == kDense2 && deep) hipLaunchKernelGGL((gemv_kernel<kDense2, 1, 6, false>), grid, block, lds, s, L);
     else hipLaunchKernelGGL((gemv_kernel<KIND, 1, 4, false>), grid, block, lds, s, L);
   } else if (xlm == 2) {
-    // more dynamic LDS than the default limit: raised once per kernel
-    static const bool raised = hipFuncSetAttribute((const void*)gemv_kernel<KIND, 2, 2, false>,
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kBigLdsAttr) == hipSuccess &&
-                               hipFuncSetAttribute((const void*)gemv_kernel<KIND, 2, 4, false>,
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kBigLdsAttr) == hipSuccess;
-    (void)raised;
+    static LdsLimit limit[2];
+    const hipError_t e = spw <= 2 ? limit[0].raise((const void*)gemv_kernel<KIND, 2, 2, false>, kBigLdsAttr)
+                                  : limit[1].raise((const void*)gemv_kernel<KIND, 2, 4, false>, kBigLdsAttr);
+    if (e != hipSuccess) return e;
     if (spw <= 2) hipLaunchKernelGGL((gemv_kernel<KIND, 2, 2, false>), grid, block, lds, s, L);
     else hipLaunchKernelGGL((gemv_kernel<KIND, 2, 4, false>), grid, block, lds, s, L);
   } else {
     if (spw <= 2) hipLaunchKernelGGL((gemv_kernel<KIND, 0, 2, false>), grid, block, lds, s, L);
     else hipLaunchKernelGGL((gemv_kernel<KIND, 0, 4, false>), grid, block, lds, s, L);
   }
+  return hipGetLastError();
 }
 
 // Launch shape of a grouped GEMV: k split (waves per tile) and tiles per
@@ -698,10 +698,9 @@ hipError_t launch_gemv_group(int kind, const LinDesc* items, int count, hipStrea
   const size_t lds = xreg + 64 + (g.ks > 1 ? (size_t)g.ks * g.tb * 4 * 64 * sizeof(int32_t) : 0);
   const dim3 grid((unsigned)blocks), block(64 * g.ks * g.tb);
   const bool xf_on = xf != nullptr;
-  if (kind == kDense2) launch_gemv<kDense2>(L, g.xlm, xf_on, g.spw, g.big, grid, block, lds, s);
-  else if (kind == kNm68) launch_gemv<kNm68>(L, g.xlm, xf_on, g.spw, g.big, grid, block, lds, s);
-  else launch_gemv<kNm24>(L, g.xlm, xf_on, g.spw, g.big, grid, block, lds, s);
-  return hipGetLastError();
+  if (kind == kDense2) return launch_gemv<kDense2>(L, g.xlm, xf_on, g.spw, g.big, grid, block, lds, s);
+  if (kind == kNm68) return launch_gemv<kNm68>(L, g.xlm, xf_on, g.spw, g.big, grid, block, lds, s);
+  return launch_gemv<kNm24>(L, g.xlm, xf_on, g.spw, g.big, grid, block, lds, s);
 }
 
 }  // namespace
