@@ -558,6 +558,8 @@ template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const Sum
     return hipGetLastError();
   }
   hipLaunchKernelGGL((sum_kernel<TD, TT, V, ADD, LINES>), dim3(work.x + zero), block, 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (join) hipLaunchKernelGGL((join_kernel<TT, V, ADD, LINES>), work, block, 0, s, a);
   return hipGetLastError();
 }
@@ -598,9 +600,11 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
   const bool few = g.m_tok <= kFewTokens;
   if (!few) {
     static LdsLimit limit;
-    const hipError_t e = limit.raise((const void*)sort_kernel, kSortWaves * kMaxRange * 4);
+    hipError_t e = limit.raise((const void*)sort_kernel, kSortWaves * kMaxRange * 4);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(sort_kernel, dim3((unsigned)p.groups), dim3(kSortThreads), (size_t)kSortWaves * p.range * 4, s, sa);
+    e = hipGetLastError();                       // without an order the sums would read and write anywhere
+    if (e != hipSuccess) return e;
   }
   // rows to zero: a few of each wave, so that there are many waves; at most 64 (the bits of a mask)
   int64_t zero_rows = 4;

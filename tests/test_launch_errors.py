@@ -118,3 +118,12 @@ def test_a_limit_that_cannot_be_raised_is_an_error(calls, call):
     (status, lines), (status2, lines2) = calls((call, 0, 1, 0), (call, 0, 0, 0))
     assert status == LAUNCH and not [x for x in lines if x.startswith("launch")]
     assert status2 == OK and [x for x in lines2 if x.startswith("limit")] and [x for x in lines2 if x.startswith("launch")]
+
+
+def test_sums_do_not_follow_a_sort_that_did_not_start(calls):
+    """The sums take places in memory from the order that the sort writes: without it nothing more is launched."""
+    for failing in (1, 2, 3):
+        status, lines = calls(("embed", 0, 0, failing))[0]
+        kernels = [x.split()[3] for x in lines if x.startswith("launch")]
+        assert status == LAUNCH and len(kernels) == failing
+        assert ["sort_kernel", "sum_kernel", "join_kernel"][failing - 1] in kernels[-1]
