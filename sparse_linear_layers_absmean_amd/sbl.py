@@ -646,8 +646,7 @@ def _here(t, dtype, shape, name: str, device: int):
     """Device pointer of a contiguous tensor of this shape on the current GPU (`device`), or None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _tensor(t, name)
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the current GPU")
     if dtype is not None and t.dtype is not dtype:
@@ -659,9 +658,13 @@ def _here(t, dtype, shape, name: str, device: int):
     return t.data_ptr()
 
 
-def _rows(t, name: str):
+def _tensor(t, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _rows(t, name: str):
+    _tensor(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     return t.shape
@@ -708,8 +711,7 @@ def sbl_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, 
 
 
 def _ids(ids):
-    if not isinstance(ids, torch.Tensor):
-        raise TypeError("ids must be a torch.Tensor")
+    _tensor(ids, "ids")
     device = torch.cuda.current_device()
     return _here(ids, torch.int64, ids.shape, "ids", device), ids.numel(), device
 
@@ -726,6 +728,8 @@ def sbl_embed_forward(ids, table, out, scale: float = 1.0, stream=None):
 
 def sbl_embed_workspace_bytes(m_tok: int, n_vocab: int, k: int, dtype=torch.bfloat16) -> int:
     """dtype: of the gradient that comes in."""
+    if dtype not in _TYPES:
+        raise TypeError(f"dtype is {dtype}, expected one of {tuple(_TYPES)}")
     return load().sbl_embed_workspace_bytes(m_tok, n_vocab, k, _TYPES[dtype])
 
 
@@ -757,6 +761,10 @@ class AdamWItems:
         self.device = None
         self.array = (AdamWItem * len(self.tensors))()
         for i, t in enumerate(self.tensors):
+            for name in ("w", "g", "m", "v"):
+                if name not in t:
+                    raise ValueError(f"tensor {i} has no {name}")
+                _tensor(t[name], name)
             w, n = t["w"], t["w"].numel()
             self._on_device(w, "w")
             small = t["m"].dtype != torch.float32
@@ -776,8 +784,7 @@ class AdamWItems:
             self.set_gradient(i, t["g"])
 
     def _on_device(self, t, name: str):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
+        _tensor(t, name)
         if not t.is_cuda or self.device not in (None, t.device):
             raise ValueError(f"{name} must be on the GPU that the first tensor is on")
         self.device = t.device
@@ -1014,6 +1021,7 @@ def embed(ids, table, scale: float = 1.0, dtype=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return embed(ids, table, scale, dtype)
+    _tensor(ids, "ids")
     _, k = _rows(table, "table")
     out = torch.empty((*ids.shape, k), dtype=_like(table, dtype, "dtype"), device=table.device)
     sbl_embed_forward(ids, table, out, scale)
@@ -1034,6 +1042,11 @@ def embed_backward(ids, dout, n_vocab: int, scale: float = 1.0, dtype=None, add_
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return embed_backward(ids, dout, n_vocab, scale, dtype, add_to, workspace)
+    for t, name in ((ids, "ids"), (dout, "dout"), (add_to, "add_to")):
+        if t is not None or name != "add_to":
+            _tensor(t, name)
+    if dout.dim() == 0:
+        raise ValueError("dout must have a row for each id")
     k = dout.shape[-1]
     if add_to is not None and tuple(add_to.shape) != (n_vocab, k):
         raise ValueError(f"add_to has shape {tuple(add_to.shape)}, expected {(n_vocab, k)}")
@@ -1048,6 +1061,9 @@ def embed_backward(ids, dout, n_vocab: int, scale: float = 1.0, dtype=None, add_
 def split_master(w32):
     """An fp32 weight as BF16 master and int16 low bits: (w, w_low), nearest BF16, ties away from zero; a NaN as the
     BF16 0x7FC0 and 0."""
+    _tensor(w32, "w32")
+    if w32.dtype != torch.float32:
+        raise TypeError(f"w32 has dtype {w32.dtype}, expected torch.float32")
     bits = w32.contiguous().view(torch.int32).masked_fill(torch.isnan(w32), 0x7FC00000)
     high = (bits + 0x8000) >> 16
     return high.to(torch.int16).view(torch.bfloat16), (bits - (high << 16)).to(torch.int16)
@@ -1055,11 +1071,18 @@ def split_master(w32):
 
 def join_master(w, w_low):
     """The fp32 weight that a BF16 master and its low bits are."""
+    for t, dtype, name in ((w, torch.bfloat16, "w"), (w_low, torch.int16, "w_low")):
+        _tensor(t, name)
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if w.shape != w_low.shape:
+        raise ValueError(f"w has shape {tuple(w.shape)}, w_low {tuple(w_low.shape)}")
     return ((w.view(torch.int16).to(torch.int32) << 16) + w_low.to(torch.int32)).view(torch.float32)
 
 
 def adamw_state(w, bits: int = 32):
     """The states of w before the first step, as keys of an AdamWItems dict: m and v, in 8 bits with their scales."""
+    _tensor(w, "w")
     n, device = w.numel(), w.device
     if bits == 32:
         return {name: torch.zeros(n, dtype=torch.float32, device=device) for name in ("m", "v")}
@@ -1072,5 +1095,7 @@ def adamw_state(w, bits: int = 32):
 
 def adamw_schedule(lr: float, beta1: float, beta2: float, step: int, factor: float = 1.0):
     """The five numbers of a step's schedule, as a float32 tensor on the host."""
+    if step < 1:
+        raise ValueError("steps are counted from 1")
     return torch.tensor([lr, 1.0 / (1.0 - beta1 ** step), (1.0 - beta2 ** step) ** -0.5, factor,
                          float(step % (1 << 24))], dtype=torch.float32)

@@ -21,3 +21,28 @@ def test_masters_that_are_nan_stay_nan():
     back = sbl.join_master(high, low).numpy()
     assert np.isnan(back[nan]).all() and np.array_equal(back[~nan].view(np.uint32), bits[~nan])
     assert np.array_equal(S.join_master(*want)[~nan].view(np.uint32), bits[~nan])
+
+
+def test_arguments_that_are_no_tensors_or_of_another_type():
+    """Refused with the binding's own errors, before a GPU is asked for."""
+    import torch
+    from sparse_linear_layers_absmean_amd import sbl
+    x, ids = torch.zeros(2, 64), torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: sbl.split_master(x.bfloat16()), lambda: sbl.split_master(x.double()), lambda: sbl.split_master([1.0]),
+                 lambda: sbl.join_master(x, ids.to(torch.int16)), lambda: sbl.join_master(x.bfloat16(), x.to(torch.int32)),
+                 lambda: sbl.join_master(None, x.to(torch.int16)),
+                 lambda: sbl.embed([0, 1], x), lambda: sbl.embed(ids, [[0.0]]), lambda: sbl.embed_backward([0, 1], x, 4),
+                 lambda: sbl.embed_backward(ids, [[0.0]], 4), lambda: sbl.embed_backward(ids, x, 4, add_to=[[0.0]]),
+                 lambda: sbl.new_embed_workspace(2, 4, 64, torch.float64), lambda: sbl.sbl_embed_workspace_bytes(2, 4, 64, "bf16"),
+                 lambda: sbl.norm_backward(x, [[0.0]], x, x), lambda: sbl.adamw_state([1.0]),
+                 lambda: sbl.AdamWItems([dict(w=[1.0], g=x, m=x, v=x)]), lambda: sbl.AdamWItems([dict(w=x, g=x, m=None, v=x)])):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        sbl.join_master(x.bfloat16(), torch.zeros(2, 63, dtype=torch.int16))
+    for missing in ("w", "g", "m", "v"):
+        with pytest.raises(ValueError, match=missing):
+            sbl.AdamWItems([{n: x for n in ("w", "g", "m", "v") if n != missing}])
+    for step in (0, -1):
+        with pytest.raises(ValueError):
+            sbl.adamw_schedule(1e-3, 0.9, 0.999, step)
