@@ -550,7 +550,7 @@ Plan plan_of(int64_t m_tok, int64_t n_vocab, int64_t k, int dout_type) {
   return p;
 }
 
-template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const SumArgs& a, bool few, bool join, hipStream_t s) {
+template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const SumArgs& a, bool few, hipStream_t s) {
   const dim3 block((unsigned)((a.chunk_vecs + 63) / 64 * 64)), work((unsigned)(a.segments * a.chunks));
   const unsigned zero = ADD ? 0u : (unsigned)a.zero_groups;
   if (few) {
@@ -560,19 +560,20 @@ template <int TD, int TT, int V, bool ADD, bool LINES> hipError_t sums(const Sum
   hipLaunchKernelGGL((sum_kernel<TD, TT, V, ADD, LINES>), dim3(work.x + zero), block, 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (join) hipLaunchKernelGGL((join_kernel<TT, V, ADD, LINES>), work, block, 0, s, a);
+  // (more tokens than few_kernel takes are always more than a segment: a run may be longer than one)
+  hipLaunchKernelGGL((join_kernel<TT, V, ADD, LINES>), work, block, 0, s, a);
   return hipGetLastError();
 }
 
-template <int TD, int TT, int V, bool ADD> hipError_t by_row_length(const SumArgs& a, bool few, bool join, hipStream_t s) {
-  if (a.k < V) return sums<TD, TT, 1, ADD, false>(a, few, join, s);
+template <int TD, int TT, int V, bool ADD> hipError_t by_row_length(const SumArgs& a, bool few, hipStream_t s) {
+  if (a.k < V) return sums<TD, TT, 1, ADD, false>(a, few, s);
   if (a.k * type_bytes(TT) % 128 == 0 && reinterpret_cast<uintptr_t>(a.dtable) % 128 == 0)
-    return sums<TD, TT, V, ADD, true>(a, few, join, s);
-  return sums<TD, TT, V, ADD, false>(a, few, join, s);
+    return sums<TD, TT, V, ADD, true>(a, few, s);
+  return sums<TD, TT, V, ADD, false>(a, few, s);
 }
 
-template <int TD, int TT, int V> hipError_t backward(const SumArgs& a, bool add, bool few, bool join, hipStream_t s) {
-  return add ? by_row_length<TD, TT, V, true>(a, few, join, s) : by_row_length<TD, TT, V, false>(a, few, join, s);
+template <int TD, int TT, int V> hipError_t backward(const SumArgs& a, bool add, bool few, hipStream_t s) {
+  return add ? by_row_length<TD, TT, V, true>(a, few, s) : by_row_length<TD, TT, V, false>(a, few, s);
 }
 
 }  // namespace
@@ -612,8 +613,7 @@ hipError_t launch_embed_backward(const EmbedGradArgs& g, int td, int tt, hipStre
   const int64_t rows = zero_rows * (p.threads / 64), zero = (g.n_vocab + rows - 1) / rows;
   const SumArgs a{g.ids, g.dout, g.dtable, (int32_t)g.m_tok, (int32_t)g.n_vocab, g.k, g.scale, p.segment, p.segments, p.chunks,
                   p.chunk_vecs, (int32_t)zero, (int32_t)zero_rows, o, reinterpret_cast<float*>(ws + p.part)};
-  const bool join = g.m_tok > p.segment;         // else no run is longer than a segment
-  return with_types(td, tt, [&](auto d, auto t) { return backward<d.value, t.value, d.value == kFp32 ? 4 : 8>(a, g.add, few, join, s); });
+  return with_types(td, tt, [&](auto d, auto t) { return backward<d.value, t.value, d.value == kFp32 ? 4 : 8>(a, g.add, few, s); });
 }
 
 }  // namespace step
