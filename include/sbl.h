@@ -643,8 +643,9 @@ int sbl_embed_backward(const int64_t* ids, const void* dout, int32_t dout_dtype,
  *              [n] e4m3 bytes (4 exponent bits, 3 mantissa bits, no infinities)
  *              with an fp32 scale for each 256 consecutive values in m_scale and
  *              v_scale [ceil(n / 256)]: m = byte * scale, sqrt(v) = byte * scale.
- *              New scales are max(RN(amax / 448), 2^-126), amax over the block's
- *              m' or sqrt(v').  m' / scale is rounded to nearest (even);
+ *              New scales are max(RN(amax RN(1 / 448)), 2^-126), amax over the
+ *              block's m' or sqrt(v').  m' / scale, taken as RN(m' RN(1 / scale)),
+ *              and sqrt(v') / scale alike: m's is rounded to nearest (even);
  *              sqrt(v') / scale to one of its two neighbours, at random in
  *              proportion (rounding to nearest would hold v where it is: a step
  *              moves it by 0.05% at beta2 = 0.999; the root held is within about

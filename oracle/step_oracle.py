@@ -161,7 +161,8 @@ def e4m3_cut(t, random, positive):
 
 
 def dither(n, seed):
-    """16 bits for each of n values: the halves of a 32-bit hash of the pair's number."""
+    """16 bits for each of n values: the halves of a 32-bit hash of the pair's number (the mixer of C. Wellons,
+    "Prospecting for Hash Functions", 2018)."""
     h = np.arange((n + 1) // 2, dtype=np.uint64) * np.uint64(0x9E3779B9) + np.uint64(seed)
     mask = np.uint64(0xFFFFFFFF)
     h &= mask

@@ -8,11 +8,12 @@
 //
 // Weights.  BF16 masters may carry the 16 bits that BF16 drops: the pair is an
 // fp32 number whose bits are (high << 16) + low, high the nearest BF16 value
-// (ties away from zero), low in [-2^15, 2^15); a NaN is 0x7FC0 and 0.  An update far below half a
-// BF16 step is then kept, at 4 bytes a weight instead of 6 for an fp32 copy.
+// (ties away from zero), low in [-2^15, 2^15); a NaN is 0x7FC0 and 0.  An update
+// far below half a BF16 step is then kept, at 4 bytes a weight instead of 6 for
+// an fp32 copy.
 //
 // States in 8 bits: blocks of 256 consecutive values of a tensor share an fp32
-// scale s = max(RN(amax / 448), 2^-126), and a value x is held as the e4m3
+// scale s = max(RN(amax RN(1 / 448)), 2^-126), and a value x is held as the e4m3
 // number nearest to RN(x RN(1 / s)) (exponent 4 bits, mantissa 3, at most 448).
 // m is rounded to nearest.  Of v the square root is held (half the exponent
 // range), rounded at random in proportion: at b2 = 0.999 a step moves it by
@@ -79,7 +80,8 @@ __device__ __forceinline__ void split(float w, uint16_t& high, int16_t& low) {
 }
 
 // 16 bits each for values 2 pair and 2 pair + 1: the low and high half of a
-// hash of the pair's number (two rounds of xor-shift and multiply)
+// hash of the pair's number (two rounds of xor-shift and multiply; shifts and
+// factors as published by C. Wellons, "Prospecting for Hash Functions", 2018)
 constexpr uint32_t kNextPair = 0x9E3779B9u;      // what pair + 1 adds to pair * kNextPair + seed
 __device__ __forceinline__ uint32_t dither(uint32_t h) {
   h ^= h >> 16;
