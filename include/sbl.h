@@ -33,7 +33,8 @@
  *    returns SBL_ERR_LAUNCH and sbl_last_hip_error() (per thread) gives the
  *    HIP error code.  No exception, abort or exit crosses this boundary.
  *  - Non-finite inputs (Inf/NaN) are a precondition violation: results are
- *    unspecified but every kernel still terminates and stays in bounds.
+ *    unspecified unless a call's own text says what they are, but every kernel
+ *    still terminates and stays in bounds.
  *  - Shape limits: 64 <= k <= 131072 and k % 64 == 0 (so 127*k < 2^24 and
  *    fp32(acc) is exact); m in {4, 8}; 1 <= n <= m; n_out*k <= 2^34.
  *

@@ -18,9 +18,9 @@
 // workgroups go over rows, so that the next row's loads are in flight while a
 // row is reduced, and the backward's column sums need no memory until the end
 // (one partial row per workgroup, joined in a fixed order by a second launch).
-// Measured, with a large copy at 4.9 TB/s: forward 4096 x 5120 BF16 to fp32 and
-// int8 26 us, 5.7 TB/s; 16384 x 8192 BF16 108 us, 5.0, fp32 197, 5.5; backward 8192 x 5120 of BF16
-// x and fp32 dy 64 us, 5.2, and 6 for joining the parts.
+// Measured, with a large copy at 4.9 TB/s: forward 4096 x 5120 BF16 to fp32 and int8
+// 26 us, 5.7 TB/s; 16384 x 8192 BF16 108 us, 5.0, fp32 197, 5.5; backward 8192 x
+// 5120 of BF16 x and fp32 dy 64 us, 5.2, and 6 for joining the parts.
 #include <algorithm>
 
 #include "sbl_actq.h"
